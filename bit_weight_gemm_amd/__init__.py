@@ -12,7 +12,9 @@ blr_backward_paths_ws (caller-owned workspace), blr_forward_paths_save and
 blr_backward_paths_saved (activations kept by the forward for the backward),
 blr_saved_size, blr_workspace_size,
 blr_backward_workspace_size, tq2_workspace_allocs, tq2_select_path,
-tq2_set_path, tq2_set_m_small, tq2_strerror, tq2_version.
+tq2_set_path, tq2_set_m_small, tq2_strerror, tq2_version; and in include/libtq2_moe.h:
+q4_upload (packs into memory of its own), q4_gemm, q4_dequant, moe_route,
+moe_route_backward and q4_moe.
 
 Every tensor's shape is checked here against the sizes the call derives from x,
 h and l before anything reaches the library: the C ABI takes raw device
@@ -95,6 +97,17 @@ def lib():
                                       p], i32),
         "tq2_strerror": ([i32], ctypes.c_char_p),
         "tq2_version": ([], ctypes.c_char_p),
+    }
+    sig |= {
+        "q4_packed_size": ([i64, i64, i64, i64, i32], sz),
+        "q4_pack": ([p, p, p, p, p], i32),
+        "q4_dequant": ([p, p, p], i32),
+        "q4_gemm_workspace_size": ([p, i64, i32], sz),
+        "q4_gemm": ([p, p, p, i64, i32, p, sz, p], i32),
+        "moe_route": ([p, p, p, p, i64, i64, i64, i64, i64, i64, i32, i32, i32, p], i32),
+        "moe_route_backward": ([p, p, p, p, i64, i64, i64, i32, i32, i32, p], i32),
+        "q4_moe_workspace_size": ([i64, i64, i64, i64, i64, i32], sz),
+        "q4_moe": ([p, p, p, p, p, p, p, i64, i64, i32, p, sz, p], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -432,3 +445,232 @@ def blr_backward_paths_ws(bits_u, bits_v, h, l, g, x, dy, dh, dl, dg, dx=None, g
                           stream=None):
     """blr_backward_paths with a caller-owned workspace (uint8, >= blr_backward_workspace_size bytes)."""
     return _blr_backward_call(bits_u, bits_v, h, l, g, x, dy, dh, dl, dg, dx, gscale, stream, workspace, True)
+
+
+# ---------------------------------------------------------------- 4-bit weights and mixtures of experts
+
+Q4_F32, Q4_F16, Q4_BF16 = 0, 1, 2
+MOE_SOFTMAX, MOE_SIGMOID = 0, 1
+_SCORES = {"softmax": MOE_SOFTMAX, "sigmoid": MOE_SIGMOID}
+_dtypes = None
+
+
+def _dtype_code(t, name):
+    """Q4_* code of a tensor's type."""
+    global _dtypes
+    if _dtypes is None:
+        import torch
+
+        _dtypes = {torch.float32: Q4_F32, torch.float16: Q4_F16, torch.bfloat16: Q4_BF16}
+    code = _dtypes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _arg(t, dtype, shape, name, device=None):
+    """Address of a contiguous GPU tensor of this type and shape (on `device`, if given)."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a tensor on the GPU")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{device}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    """The stream's handle; None: the current stream of `device`, which has to be the current device."""
+    import torch
+
+    if device != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _scratch(need, device, stream):
+    """A temporary workspace of the current stream, kept from reuse until `stream` is done with it."""
+    import torch
+
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None and hasattr(stream, "cuda_stream"):
+        ws.record_stream(stream)
+    return ws
+
+
+class _Q4Struct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("E", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("G", ctypes.c_int64), ("zeros", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class Q4Weight:
+    """A packed 4-bit weight [N][K] (E is None) or stack of them [E][N][K]; its memory is a torch tensor."""
+
+    def __init__(self, data, e, n, k, g, zeros: bool):
+        self.data, self.E, self.N, self.K, self.G, self.zeros = data, e, n, k, g, zeros
+        self.device = data.get_device()
+        self._struct = _Q4Struct(data.data_ptr(), 1 if e is None else e, n, k, g, int(zeros), 0)
+        self.handle = ctypes.addressof(self._struct)
+
+    def device_bytes(self) -> int:
+        return self.data.numel()
+
+
+def q4_upload(codes, scales, zeros=None, stream=None) -> Q4Weight:
+    """Pack a 4-bit weight: codes uint8 [..., N, K/2] (element 2j in the low four bits of byte j), scales float16
+    [..., N, K/G] with G 32, 64 or 128, zeros uint8 like scales (8 everywhere if None); W = (code - zero) * scale.
+    `...` is nothing, or one axis of experts.  The inputs may be freed once the work queued on the stream is done."""
+    import torch
+
+    if codes.dim() not in (2, 3) or codes.numel() == 0:
+        raise ValueError("codes must be [N, K/2] or [E, N, K/2], and not empty")
+    e = codes.shape[0] if codes.dim() == 3 else None
+    n, k = codes.shape[-2], 2 * codes.shape[-1]
+    if scales.dim() != codes.dim() or scales.shape[-1] == 0 or k % scales.shape[-1]:
+        raise ValueError(f"scales must be [{'E, ' if e is not None else ''}{n}, K/G], got {tuple(scales.shape)}")
+    g = k // scales.shape[-1]
+    need = lib().q4_packed_size(e or 1, n, k, g, int(zeros is not None))
+    if need == 0:
+        raise ValueError(f"no packed form for E={e}, N={n}, K={k}, G={g}: G is 32, 64 or 128 and divides K")
+    device = codes.get_device()
+    lead = codes.shape[:-1]
+    pc = _arg(codes, torch.uint8, codes.shape, "codes")
+    ps = _arg(scales, torch.float16, (*lead, k // g), "scales", device)
+    pz = None if zeros is None else _arg(zeros, torch.uint8, (*lead, k // g), "zeros", device)
+    raw = _raw_stream(stream, device)
+    w = Q4Weight(torch.empty(need, dtype=torch.uint8, device=codes.device), e, n, k, g, zeros is not None)
+    if stream is not None and hasattr(stream, "cuda_stream"):
+        for t in (w.data, codes, scales) + (() if zeros is None else (zeros,)):
+            t.record_stream(stream)
+    _check(lib().q4_pack(w.handle, pc, ps, pz, raw), "q4_pack")
+    return w
+
+
+def q4_dequant(w: Q4Weight, out=None, stream=None):
+    """(code - zero) * scale as float32, exact: [N, K] or [E, N, K]."""
+    import torch
+
+    shape = (w.N, w.K) if w.E is None else (w.E, w.N, w.K)
+    raw = _raw_stream(stream, w.device)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=w.data.device)
+    _check(lib().q4_dequant(w.handle, _arg(out, torch.float32, shape, "out", w.device), raw), "q4_dequant")
+    return out
+
+
+def q4_gemm(w: Q4Weight, x, y=None, stream=None):
+    """y[M][N] = x[M][K] @ W^T in x's type (float32, float16 or bfloat16); returns y (allocated if None)."""
+    import torch
+
+    if w.E is not None:
+        raise ValueError("q4_gemm takes a weight without an axis of experts")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, {w.K}]")
+    m = x.shape[0]
+    code = _dtype_code(x, "x")
+    px = _arg(x, x.dtype, (m, w.K), "x", w.device)
+    raw = _raw_stream(stream, w.device)
+    if y is None:
+        y = torch.empty((m, w.N), dtype=x.dtype, device=x.device)
+    py = _arg(y, x.dtype, (m, w.N), "y", w.device)
+    L = lib()
+    need = L.q4_gemm_workspace_size(w.handle, m, code) if m > 16 else 0
+    ws = _scratch(need, x.device, stream) if need else None
+    _check(L.q4_gemm(w.handle, px, py, m, code, ws.data_ptr() if need else None, need, raw), "q4_gemm")
+    return y
+
+
+def _score(score):
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return _SCORES[score]
+
+
+def moe_route(logits, k, bias=None, score="softmax", groups=1, keep=1, group_top=1, renorm=False, idx=None,
+              weights=None, stream=None):
+    """Router of a mixture of experts: (idx int32 [T][k], weights float32 [T][k]) from logits [T][E] (float32,
+    float16 or bfloat16).  Experts are ranked by score + bias (bias float32 [E]), within the `keep` of `groups`
+    equal groups whose `group_top` best keys add up to most; equal keys go to the lower index.  The weights are the scores,
+    divided by their sum if renorm.  Slots that find no expert (logits of -inf) get idx -1 and weight 0."""
+    import torch
+
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    t, e = logits.shape
+    k, sc, code = int(k), _score(score), _dtype_code(logits, "logits")
+    if not 1 <= k <= min(e, 64):
+        raise ValueError(f"k must lie between 1 and {min(e, 64)}, got {k}")
+    if e > 1024 or not 1 <= groups <= 64 or e % groups or not 1 <= keep <= groups or group_top not in (1, 2):
+        raise ValueError(f"no routing over E={e}, groups={groups}, keep={keep}, group_top={group_top}")
+    device = logits.get_device()
+    pl = _arg(logits, logits.dtype, (t, e), "logits")
+    pb = None if bias is None else _arg(bias, torch.float32, (e,), "bias", device)
+    raw = _raw_stream(stream, device)
+    if idx is None:
+        idx = torch.empty((t, k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((t, k), dtype=torch.float32, device=logits.device)
+    _check(lib().moe_route(pl, pb, _arg(idx, torch.int32, (t, k), "idx", device),
+                           _arg(weights, torch.float32, (t, k), "weights", device), t, e, k, groups, keep, group_top,
+                           sc, 1 if renorm else 0, code, raw), "moe_route")
+    return idx, weights
+
+
+def moe_route_backward(logits, idx, dw, score="softmax", renorm=False, dlogits=None, stream=None):
+    """Gradient of moe_route's weights: dlogits [T][E] (logits' type, overwritten; allocated if None) from dw
+    float32 [T][k] and the idx that moe_route gave, the choice held fixed."""
+    import torch
+
+    if logits.dim() != 2 or idx.dim() != 2:
+        raise ValueError("logits must be [T, E] and idx [T, k]")
+    t, e = logits.shape
+    k, sc, code = idx.shape[1], _score(score), _dtype_code(logits, "logits")
+    if not 1 <= k <= 64 or not 1 <= e <= 1024:
+        raise ValueError(f"no routing of k={k} out of E={e}")
+    device = logits.get_device()
+    pl = _arg(logits, logits.dtype, (t, e), "logits")
+    pi, pw = _arg(idx, torch.int32, (t, k), "idx", device), _arg(dw, torch.float32, (t, k), "dw", device)
+    raw = _raw_stream(stream, device)
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    _check(lib().moe_route_backward(pl, pi, pw, _arg(dlogits, logits.dtype, (t, e), "dlogits", device), t, e, k, sc,
+                                    1 if renorm else 0, code, raw), "moe_route_backward")
+    return dlogits
+
+
+def q4_moe(x, idx, weights, gate: Q4Weight, up: Q4Weight, down: Q4Weight, y=None, stream=None):
+    """Experts' gated products, y[t] = sum_j weights[t][j] * down_e(silu(gate_e x_t) * (up_e x_t)) with e = idx[t][j]:
+    x [T][d] (float32, float16 or bfloat16), idx int32 [T][k] (entries outside 0 .. E-1 are dropped), weights float32
+    [T][k], gate and up [E][f][d], down [E][d][f]; returns y [T][d] in x's type (allocated if None)."""
+    import torch
+
+    if gate.E is None or up.E is None or down.E is None:
+        raise ValueError("q4_moe takes weights with an axis of experts")
+    e, f, d = gate.E, gate.N, gate.K
+    if (up.E, up.N, up.K, up.G, up.zeros) != (e, f, d, gate.G, gate.zeros) or (down.E, down.N, down.K) != (e, d, f):
+        raise ValueError(f"gate and up must be alike and down [{e}, {d}, {f}]")
+    if x.dim() != 2 or idx.dim() != 2:
+        raise ValueError("x must be [T, d] and idx [T, k]")
+    t, k = idx.shape
+    code, device = _dtype_code(x, "x"), gate.device
+    if up.device != device or down.device != device:
+        raise ValueError("the weights are on different devices")
+    px = _arg(x, x.dtype, (t, d), "x", device)
+    pi, pw = _arg(idx, torch.int32, (t, k), "idx", device), _arg(weights, torch.float32, (t, k), "weights", device)
+    raw = _raw_stream(stream, device)
+    if y is None:
+        y = torch.empty_like(x)
+    py = _arg(y, x.dtype, (t, d), "y", device)
+    L = lib()
+    need = L.q4_moe_workspace_size(t, k, e, d, f, code)
+    if need == 0:
+        raise ValueError(f"no experts' products for T={t}, k={k}, E={e}, d={d}, f={f}")
+    ws = _scratch(need, x.device, stream)
+    _check(L.q4_moe(px, pi, pw, gate.handle, up.handle, down.handle, py, t, k, code, ws.data_ptr(), need, raw), "q4_moe")
+    return y

@@ -2,6 +2,7 @@
 
 Flags: -O3, C++17, position-independent shared object; packed-FP32 VALU ops are
 disabled for the device code (-Xclang -target-feature -Xclang -packed-fp32-ops).
+Each source is compiled to an object of its own, several at a time.
 """
 
 from __future__ import annotations
@@ -9,11 +10,14 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtq2.so")
-SOURCES = ["libtq2.cpp", "repack.cpp", "tq2_gemv.hip", "mfma_gemm.hip", "blr.hip", "skinny_gemm.hip"]
+SOURCES = ["q4_gemm.hip", "q4_moe.hip", "moe_route.hip", "libtq2.cpp", "libq4.cpp", "repack.cpp", "tq2_gemv.hip",
+           "mfma_gemm.hip", "blr.hip", "skinny_gemm.hip"]
 ARCH = "gfx950"
 
 
@@ -24,20 +28,24 @@ def hipcc() -> str:
     return "hipcc"
 
 
-def compile_cmd(out: str, extra=()) -> list:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    return [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-            "-x", "hip", *srcs,
+def compile_cmd(source: str, out: str, extra=()) -> list:
+    return [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-c",
+            "-x", "hip", os.path.join(CSRC, source),
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             "-Wall", "-Wno-unused-result", *extra, "-o", out]
 
 
 def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
-    cmd = compile_cmd(tmp)
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    with tempfile.TemporaryDirectory(prefix="tq2_build_") as d:
+        objs = [os.path.join(d, os.path.splitext(s)[0] + ".o") for s in SOURCES]
+        cmds = [compile_cmd(s, o) for s, o in zip(SOURCES, objs)]
+        if verbose:
+            print("\n".join(" ".join(c) for c in cmds), flush=True)
+        with ThreadPoolExecutor(min(6, os.cpu_count() or 1)) as pool:
+            for r in [pool.submit(subprocess.run, c, check=True) for c in cmds]:
+                r.result()
+        subprocess.run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], check=True)
     os.replace(tmp, LIB)
     return LIB
 

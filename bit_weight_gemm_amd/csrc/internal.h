@@ -9,6 +9,11 @@
 
 namespace tq2 {
 
+// The current device if it is a gfx950 (else TQ2_ENODEV), and the status code of a
+// HIP error (libtq2.cpp).
+int current_device(int *dev);
+int status_of(hipError_t e);
+
 struct DevWeight {
     int64_t N = 0, K = 0, Npad = 0;
     uint32_t *codes = nullptr;   // [Npad/4][K/16][4]

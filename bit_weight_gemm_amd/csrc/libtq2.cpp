@@ -158,6 +158,14 @@ int scratch_address(int dev, void **out) {
 
 }  // namespace
 
+namespace tq2 {
+
+int current_device(int *dev) { return check_device(dev); }
+
+int status_of(hipError_t e) { return from_hip(e); }
+
+}  // namespace tq2
+
 extern "C" {
 
 const char *tq2_strerror(int status) {
