@@ -58,10 +58,10 @@ def _single_hip_runtime():
 
 def lib():
     """Load libtq2.so (after torch, so both share torch's HIP runtime)."""
-    global _lib
+    global _lib, _dtypes, _get_device, _get_raw_stream, _f32, _i32
     if _lib is not None:
         return _lib
-    import torch  # noqa: F401  -- load torch's HIP runtime first
+    import torch  # load torch's HIP runtime first
 
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is not built; run bit_weight_gemm_amd/build.py")
@@ -113,6 +113,9 @@ def lib():
         f = getattr(L, name)
         f.argtypes = args
         f.restype = res
+    _dtypes = {torch.float32: Q4_F32, torch.float16: Q4_F16, torch.bfloat16: Q4_BF16}
+    _f32, _i32 = torch.float32, torch.int32
+    _get_device, _get_raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _lib = L
     return L
 
@@ -452,25 +455,32 @@ def blr_backward_paths_ws(bits_u, bits_v, h, l, g, x, dy, dh, dl, dg, dx=None, g
 Q4_F32, Q4_F16, Q4_BF16 = 0, 1, 2
 MOE_SOFTMAX, MOE_SIGMOID = 0, 1
 _SCORES = {"softmax": MOE_SOFTMAX, "sigmoid": MOE_SIGMOID}
-_dtypes = None
+# filled in by lib(): types, and torch's current device and stream without the objects around them
+_dtypes = _get_device = _get_raw_stream = _f32 = _i32 = None
 
 
 def _dtype_code(t, name):
     """Q4_* code of a tensor's type."""
-    global _dtypes
-    if _dtypes is None:
-        import torch
-
-        _dtypes = {torch.float32: Q4_F32, torch.float16: Q4_F16, torch.bfloat16: Q4_BF16}
     code = _dtypes.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
     return code
 
 
-def _arg(t, dtype, shape, name, device=None):
-    """Address of a contiguous GPU tensor of this type and shape (on `device`, if given)."""
-    if not t.is_cuda:
+def _gpu_of(t, name) -> int:
+    """Index of the tensor's GPU."""
+    device = t.get_device()
+    if device < 0:
+        raise TypeError(f"{name} must be a tensor on the GPU")
+    return device
+
+
+def _arg(t, dtype, shape, name, device):
+    """Address of a contiguous tensor of this type and shape on GPU `device`.  One test on the way that
+    every call takes: a call's host time is a few microseconds, and so is a small kernel's."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
+    if t.get_device() < 0:
         raise TypeError(f"{name} must be a tensor on the GPU")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -478,19 +488,15 @@ def _arg(t, dtype, shape, name, device=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if device is not None and t.get_device() != device:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{device}")
 
 
 def _raw_stream(stream, device):
     """The stream's handle; None: the current stream of `device`, which has to be the current device."""
-    import torch
-
-    if device != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+    if device != _get_device():
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{_get_device()}")
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _get_raw_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -538,9 +544,9 @@ def q4_upload(codes, scales, zeros=None, stream=None) -> Q4Weight:
     need = lib().q4_packed_size(e or 1, n, k, g, int(zeros is not None))
     if need == 0:
         raise ValueError(f"no packed form for E={e}, N={n}, K={k}, G={g}: G is 32, 64 or 128 and divides K")
-    device = codes.get_device()
+    device = _gpu_of(codes, "codes")
     lead = codes.shape[:-1]
-    pc = _arg(codes, torch.uint8, codes.shape, "codes")
+    pc = _arg(codes, torch.uint8, codes.shape, "codes", device)
     ps = _arg(scales, torch.float16, (*lead, k // g), "scales", device)
     pz = None if zeros is None else _arg(zeros, torch.uint8, (*lead, k // g), "zeros", device)
     raw = _raw_stream(stream, device)
@@ -566,8 +572,7 @@ def q4_dequant(w: Q4Weight, out=None, stream=None):
 
 def q4_gemm(w: Q4Weight, x, y=None, stream=None):
     """y[M][N] = x[M][K] @ W^T in x's type (float32, float16 or bfloat16); returns y (allocated if None)."""
-    import torch
-
+    L = lib()
     if w.E is not None:
         raise ValueError("q4_gemm takes a weight without an axis of experts")
     if x.dim() != 2:
@@ -577,12 +582,13 @@ def q4_gemm(w: Q4Weight, x, y=None, stream=None):
     px = _arg(x, x.dtype, (m, w.K), "x", w.device)
     raw = _raw_stream(stream, w.device)
     if y is None:
-        y = torch.empty((m, w.N), dtype=x.dtype, device=x.device)
+        y = x.new_empty((m, w.N))
     py = _arg(y, x.dtype, (m, w.N), "y", w.device)
-    L = lib()
     need = L.q4_gemm_workspace_size(w.handle, m, code) if m > 16 else 0
     ws = _scratch(need, x.device, stream) if need else None
-    _check(L.q4_gemm(w.handle, px, py, m, code, ws.data_ptr() if need else None, need, raw), "q4_gemm")
+    st = L.q4_gemm(w.handle, px, py, m, code, ws.data_ptr() if need else None, need, raw)
+    if st:
+        _check(st, "q4_gemm")
     return y
 
 
@@ -598,8 +604,7 @@ def moe_route(logits, k, bias=None, score="softmax", groups=1, keep=1, group_top
     float16 or bfloat16).  Experts are ranked by score + bias (bias float32 [E]), within the `keep` of `groups`
     equal groups whose `group_top` best keys add up to most; equal keys go to the lower index.  The weights are the scores,
     divided by their sum if renorm.  Slots that find no expert (logits of -inf) get idx -1 and weight 0."""
-    import torch
-
+    L = lib()
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     t, e = logits.shape
@@ -608,39 +613,41 @@ def moe_route(logits, k, bias=None, score="softmax", groups=1, keep=1, group_top
         raise ValueError(f"k must lie between 1 and {min(e, 64)}, got {k}")
     if e > 1024 or not 1 <= groups <= 64 or e % groups or not 1 <= keep <= groups or group_top not in (1, 2):
         raise ValueError(f"no routing over E={e}, groups={groups}, keep={keep}, group_top={group_top}")
-    device = logits.get_device()
-    pl = _arg(logits, logits.dtype, (t, e), "logits")
-    pb = None if bias is None else _arg(bias, torch.float32, (e,), "bias", device)
+    device = _gpu_of(logits, "logits")
+    pl = _arg(logits, logits.dtype, (t, e), "logits", device)
+    pb = None if bias is None else _arg(bias, _f32, (e,), "bias", device)
     raw = _raw_stream(stream, device)
     if idx is None:
-        idx = torch.empty((t, k), dtype=torch.int32, device=logits.device)
+        idx = logits.new_empty((t, k), dtype=_i32)
     if weights is None:
-        weights = torch.empty((t, k), dtype=torch.float32, device=logits.device)
-    _check(lib().moe_route(pl, pb, _arg(idx, torch.int32, (t, k), "idx", device),
-                           _arg(weights, torch.float32, (t, k), "weights", device), t, e, k, groups, keep, group_top,
-                           sc, 1 if renorm else 0, code, raw), "moe_route")
+        weights = logits.new_empty((t, k), dtype=_f32)
+    st = L.moe_route(pl, pb, _arg(idx, _i32, (t, k), "idx", device), _arg(weights, _f32, (t, k), "weights", device),
+                     t, e, k, groups, keep, group_top, sc, 1 if renorm else 0, code, raw)
+    if st:
+        _check(st, "moe_route")
     return idx, weights
 
 
 def moe_route_backward(logits, idx, dw, score="softmax", renorm=False, dlogits=None, stream=None):
     """Gradient of moe_route's weights: dlogits [T][E] (logits' type, overwritten; allocated if None) from dw
     float32 [T][k] and the idx that moe_route gave, the choice held fixed."""
-    import torch
-
+    L = lib()
     if logits.dim() != 2 or idx.dim() != 2:
         raise ValueError("logits must be [T, E] and idx [T, k]")
     t, e = logits.shape
     k, sc, code = idx.shape[1], _score(score), _dtype_code(logits, "logits")
     if not 1 <= k <= 64 or not 1 <= e <= 1024:
         raise ValueError(f"no routing of k={k} out of E={e}")
-    device = logits.get_device()
-    pl = _arg(logits, logits.dtype, (t, e), "logits")
-    pi, pw = _arg(idx, torch.int32, (t, k), "idx", device), _arg(dw, torch.float32, (t, k), "dw", device)
+    device = _gpu_of(logits, "logits")
+    pl = _arg(logits, logits.dtype, (t, e), "logits", device)
+    pi, pw = _arg(idx, _i32, (t, k), "idx", device), _arg(dw, _f32, (t, k), "dw", device)
     raw = _raw_stream(stream, device)
     if dlogits is None:
-        dlogits = torch.empty_like(logits)
-    _check(lib().moe_route_backward(pl, pi, pw, _arg(dlogits, logits.dtype, (t, e), "dlogits", device), t, e, k, sc,
-                                    1 if renorm else 0, code, raw), "moe_route_backward")
+        dlogits = logits.new_empty((t, e))
+    st = L.moe_route_backward(pl, pi, pw, _arg(dlogits, logits.dtype, (t, e), "dlogits", device), t, e, k, sc,
+                              1 if renorm else 0, code, raw)
+    if st:
+        _check(st, "moe_route_backward")
     return dlogits
 
 
@@ -648,8 +655,7 @@ def q4_moe(x, idx, weights, gate: Q4Weight, up: Q4Weight, down: Q4Weight, y=None
     """Experts' gated products, y[t] = sum_j weights[t][j] * down_e(silu(gate_e x_t) * (up_e x_t)) with e = idx[t][j]:
     x [T][d] (float32, float16 or bfloat16), idx int32 [T][k] (entries outside 0 .. E-1 are dropped), weights float32
     [T][k], gate and up [E][f][d], down [E][d][f]; returns y [T][d] in x's type (allocated if None)."""
-    import torch
-
+    L = lib()
     if gate.E is None or up.E is None or down.E is None:
         raise ValueError("q4_moe takes weights with an axis of experts")
     e, f, d = gate.E, gate.N, gate.K
@@ -662,15 +668,16 @@ def q4_moe(x, idx, weights, gate: Q4Weight, up: Q4Weight, down: Q4Weight, y=None
     if up.device != device or down.device != device:
         raise ValueError("the weights are on different devices")
     px = _arg(x, x.dtype, (t, d), "x", device)
-    pi, pw = _arg(idx, torch.int32, (t, k), "idx", device), _arg(weights, torch.float32, (t, k), "weights", device)
+    pi, pw = _arg(idx, _i32, (t, k), "idx", device), _arg(weights, _f32, (t, k), "weights", device)
     raw = _raw_stream(stream, device)
     if y is None:
-        y = torch.empty_like(x)
+        y = x.new_empty((t, d))
     py = _arg(y, x.dtype, (t, d), "y", device)
-    L = lib()
     need = L.q4_moe_workspace_size(t, k, e, d, f, code)
     if need == 0:
         raise ValueError(f"no experts' products for T={t}, k={k}, E={e}, d={d}, f={f}")
     ws = _scratch(need, x.device, stream)
-    _check(L.q4_moe(px, pi, pw, gate.handle, up.handle, down.handle, py, t, k, code, ws.data_ptr(), need, raw), "q4_moe")
+    st = L.q4_moe(px, pi, pw, gate.handle, up.handle, down.handle, py, t, k, code, ws.data_ptr(), need, raw)
+    if st:
+        _check(st, "q4_moe")
     return y

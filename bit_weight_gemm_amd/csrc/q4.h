@@ -30,7 +30,8 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
 enum Q4Type { kF32 = 0, kF16 = 1, kBF16 = 2 };
 
-constexpr int64_t kQ4Head = 256;  // bytes before the codes: the largest |scale| (f32 bits)
+// Bytes before the codes: each expert's largest |scale| (f32 bits).
+inline size_t q4_head_bytes(int64_t E) { return (size_t)(E * 4 + 255) / 256 * 256; }
 
 struct Q4Layout {
     int64_t nb, ku;                          // row blocks and units of one expert
@@ -43,7 +44,7 @@ inline Q4Layout q4_layout(int64_t E, int64_t N, int64_t K, int64_t G, bool zeros
     L.nb = (N + 15) / 16;
     L.ku = (K + 127) / 128;
     const size_t units = (size_t)E * L.nb * L.ku, groups = units * 16 * (128 / G);
-    L.codes_off = kQ4Head;
+    L.codes_off = q4_head_bytes(E);
     L.scales_off = L.codes_off + units * 1024;
     L.zeros_off = L.scales_off + up(groups * 2);
     L.total = L.zeros_off + (zeros ? up(groups) : 0);
@@ -148,8 +149,10 @@ hipError_t launch_q4_gemm(const Q4View &v, const void *x, void *y, int64_t M, in
 // Experts' products.  Workspace: see MoePlan.
 struct MoePlan {
     int64_t slots;                   // T * k
+    bool tiled;                      // many rows per expert: the tiled products
     int64_t tile_rows, max_tiles;    // rows per tile of the grouped products, and the most tiles there can be
-    size_t off_order, off_tiles, off_h, off_part, total;
+    int64_t ldx, ldh;                // tiled: rows of x and of h in whole units of 128
+    size_t off_order, off_tiles, off_h, off_part, off_x, off_xscale, off_xnorm, off_hscale, off_hplanes, total;
 };
 MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtype);
 hipError_t launch_q4_moe(const MoePlan &p, const void *x, const int32_t *idx, const float *weights, const Q4View &gate,

@@ -1,17 +1,18 @@
 // 4-bit weights: packing, decode to f32, and the dense product's launches.
 #include "q4_skinny.h"
+#include "q4_tiled.h"
 
 namespace tq2 {
 
 namespace {
 
-__global__ void q4_head_kernel(uint32_t *head) {
-    if (threadIdx.x < kQ4Head / 4) head[threadIdx.x] = 0;
+__global__ __launch_bounds__(1024) void q4_head_kernel(uint32_t *head, int E) {
+    if ((int)threadIdx.x < E) head[threadIdx.x] = 0;
 }
 
 // One thread per lane of a unit: its four words, each from four consecutive bytes of
 // the row-major codes; the first 16 lanes also bring their row's scales and zeros.
-// The head collects the largest |scale| (integer maximum: the order does not matter).
+// The head collects each expert's largest |scale| (integer maximum: the order does not matter).
 __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros,
                                                       Q4View v, w4 *oc, uint16_t *os, uint8_t *oz, uint32_t *head,
                                                       int64_t units) {
@@ -56,7 +57,7 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t *codes, cons
         const uint32_t b = (uint32_t)__shfl_xor((int)most, o);
         most = b > most ? b : most;
     }
-    if (lane == 0 && most) atomicMax(head, most);
+    if (lane == 0 && most) atomicMax(&head[unit / v.ku / v.nb], most);
 }
 
 __global__ __launch_bounds__(256) void q4_dequant_kernel(Q4View v, float *out) {
@@ -93,7 +94,7 @@ hipError_t dense_g(const Q4Args &a, hipStream_t s) {
 hipError_t launch_q4_pack(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, const Q4View &v,
                           hipStream_t s) {
     uint32_t *head = const_cast<uint32_t *>(v.head);
-    q4_head_kernel<<<dim3(1), dim3(64), 0, s>>>(head);
+    q4_head_kernel<<<dim3(1), dim3(1024), 0, s>>>(head, v.E);
     const int64_t units = (int64_t)v.E * v.nb * v.ku;
     q4_pack_kernel<<<dim3((unsigned)((units + 3) / 4)), dim3(256), 0, s>>>(
         codes, scales, zeros, v, const_cast<w4 *>(v.codes), const_cast<uint16_t *>(v.scales),
@@ -107,9 +108,33 @@ hipError_t launch_q4_dequant(const Q4View &v, float *out, hipStream_t s) {
     return hipGetLastError();
 }
 
-size_t q4_gemm_workspace(int64_t, int64_t, int64_t, int) { return 0; }
+// The tiled product from kTiledRows rows on (below, the skinny kernel on tiles of 64).
+constexpr int64_t kTiledRows = 256;
 
-hipError_t launch_q4_gemm(const Q4View &v, const void *x, void *y, int64_t M, int dtype, void *, hipStream_t s) {
+size_t q4_gemm_workspace(int64_t, int64_t K, int64_t M, int dtype) {
+    if (M < kTiledRows || q4_plain_x(K, dtype)) return 0;
+    const size_t lda = (size_t)(K + 127) / 128 * 128;
+    return (size_t)q4_planes(dtype) * M * lda * 2 + (size_t)(M * 4 + 255) / 256 * 256;
+}
+
+hipError_t launch_q4_gemm(const Q4View &v, const void *x, void *y, int64_t M, int dtype, void *ws, hipStream_t s) {
+    if (M >= kTiledRows) {
+        Q4TArgs a{};
+        a.w = v, a.y = y, a.M = M;
+        if (q4_plain_x(v.K, dtype)) {
+            a.a = static_cast<const _Float16 *>(x), a.lda = v.K;
+        } else {
+            Q4Prep p{};
+            p.x = x, p.rows = M, p.K = v.K;
+            p.lda = (int64_t)v.ku * 128, p.plane = M * p.lda;
+            p.out = static_cast<_Float16 *>(ws);
+            p.rowscale = reinterpret_cast<float *>(p.out + q4_planes(dtype) * p.plane);
+            const hipError_t e = launch_q4_prep(p, dtype, s);
+            if (e != hipSuccess) return e;
+            a.a = p.out, a.lda = p.lda, a.plane = p.plane, a.rowscale = p.rowscale;
+        }
+        return launch_q4_tiled_dense(a, dtype, 128, s);
+    }
     Q4Args a{};
     a.w = v, a.x = x, a.y = y, a.M = M;
     if (dtype == kF16) return dense_g<kXF16>(a, s);

@@ -6,6 +6,7 @@
 // silu(g) u in their epilogue, the down product times the slot's weight, and the
 // sum of each token's slots in slot order.
 #include "q4_skinny.h"
+#include "q4_tiled.h"
 
 namespace tq2 {
 
@@ -85,20 +86,89 @@ hipError_t product(const MoePlan &p, const Q4Args &a, hipStream_t s) {
     return product_rb<XT, 128, MODE>(p, a, s);
 }
 
+// Few rows per expert: tiles of 16 or 32 rows, h in f32.
+hipError_t skinny(const MoePlan &p, const void *x, const float *weights, const Q4View &gate, const Q4View &up,
+                  const Q4View &down, int64_t k, int dtype, char *b, hipStream_t s) {
+    Q4Args g{};
+    g.w = gate, g.w2 = up, g.x = x, g.y = b + p.off_h, g.topk = (int)k, g.weights = weights;
+    g.ntiles = reinterpret_cast<const int32_t *>(b), g.order = reinterpret_cast<const int32_t *>(b + p.off_order);
+    g.tiles = reinterpret_cast<const int4 *>(b + p.off_tiles);
+    Q4Args d = g;
+    d.w = down, d.x = g.y, d.y = b + p.off_part;
+    hipError_t e;
+    if (dtype == kF16) e = product<kXF16, kGateUp>(p, g, s);
+    else if (dtype == kBF16) e = product<kXBF16, kGateUp>(p, g, s);
+    else e = product<kXF32x3, kGateUp>(p, g, s);
+    if (e != hipSuccess) return e;
+    // h for a 16-bit result is taken in 16 bits (two bfloat16 parts, relative error 2^-17)
+    return dtype == kF32 ? product<kXF32x3, kDown>(p, d, s) : product<kXF32x2, kDown>(p, d, s);
+}
+
+// Many rows per expert.  For 16-bit types h is rounded to f16 under a power of two per
+// row: half a step of f16 (2^-11) in front of a sum over f, as much as the result's own
+// rounding for f16 and an eighth of it for bfloat16; f32 h goes through f32 and two planes.
+hipError_t tiled(const MoePlan &p, const void *x, const float *weights, const Q4View &gate, const Q4View &up,
+                 const Q4View &down, int64_t T, int64_t k, int dtype, char *b, hipStream_t s) {
+    const int planes = q4_planes(dtype), bm = (int)p.tile_rows;
+    const bool plain = q4_plain_x(gate.K, dtype);
+    Q4Prep px{};
+    px.x = x, px.rows = T, px.K = gate.K, px.lda = p.ldx, px.plane = T * p.ldx;
+    px.out = plain ? nullptr : reinterpret_cast<_Float16 *>(b + p.off_x);
+    px.rowscale = reinterpret_cast<float *>(b + p.off_xscale);
+    px.norm_exp = reinterpret_cast<int32_t *>(b + p.off_xnorm);
+    hipError_t e = launch_q4_prep(px, dtype, s);
+    if (e != hipSuccess) return e;
+    Q4TArgs g{};
+    g.w = gate, g.w2 = up, g.topk = (int)k, g.weights = weights, g.y = b + p.off_h, g.ldh = p.ldh;
+    g.ntiles = reinterpret_cast<const int32_t *>(b), g.order = reinterpret_cast<const int32_t *>(b + p.off_order);
+    g.tiles = reinterpret_cast<const int4 *>(b + p.off_tiles);
+    g.a = plain ? static_cast<const _Float16 *>(x) : px.out, g.lda = plain ? gate.K : px.lda, g.plane = px.plane;
+    g.rowscale = px.rowscale, g.norm_exp = px.norm_exp, g.hscale = reinterpret_cast<float *>(b + p.off_hscale);
+    e = launch_q4_tiled_gate_up(g, planes, bm, p.max_tiles, s);
+    if (e != hipSuccess) return e;
+    Q4TArgs d = g;
+    d.w = down, d.y = b + p.off_part, d.rowscale = g.hscale, d.lda = p.ldh, d.plane = p.slots * p.ldh;
+    d.a = reinterpret_cast<const _Float16 *>(b + p.off_h);
+    if (dtype == kF32) {
+        Q4Prep ph{};
+        ph.x = g.y, ph.rows = p.slots, ph.K = gate.N, ph.lda = p.ldh, ph.plane = d.plane;
+        ph.out = reinterpret_cast<_Float16 *>(b + p.off_hplanes), ph.rowscale = g.hscale;
+        e = launch_q4_prep(ph, kF32, s);
+        if (e != hipSuccess) return e;
+        d.a = ph.out;
+    }
+    return launch_q4_tiled_down(d, planes, bm, p.max_tiles, s);
+}
+
 }  // namespace
 
 MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtype) {
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     MoePlan p{};
-    (void)dtype;
+    const bool plain = q4_plain_x(d, dtype), f32 = dtype == kF32;
     p.slots = T * k;
-    p.tile_rows = p.slots <= 16 * E ? 16 : 32;
+    p.tiled = p.slots > 32 * E;
+    p.tile_rows = p.tiled ? (p.slots > 96 * E ? 128 : 64) : p.slots <= 16 * E ? 16 : 32;
     p.max_tiles = p.slots / p.tile_rows + (E < p.slots ? E : p.slots);
-    p.off_order = 256;  // the first 256 bytes hold the number of tiles
-    p.off_tiles = p.off_order + up((size_t)p.slots * 4);
-    p.off_h = p.off_tiles + up((size_t)p.max_tiles * 16);
-    p.off_part = p.off_h + up((size_t)p.slots * f * 4);
-    p.total = p.off_part + up((size_t)p.slots * d * 4);
+    p.ldx = (d + 127) / 128 * 128, p.ldh = (f + 127) / 128 * 128;
+    size_t at = 256;  // the first 256 bytes hold the number of tiles
+    auto take = [&](size_t n) {
+        const size_t off = at;
+        at += up(n);
+        return off;
+    };
+    p.off_order = take((size_t)p.slots * 4);
+    p.off_tiles = take((size_t)p.max_tiles * 16);
+    p.off_h = take((size_t)p.slots * (p.tiled && !f32 ? p.ldh * 2 : f * 4));
+    p.off_part = take((size_t)p.slots * d * 4);
+    if (p.tiled) {
+        p.off_x = take(plain ? 0 : (size_t)q4_planes(dtype) * T * p.ldx * 2);
+        p.off_xscale = take((size_t)T * 4);
+        p.off_xnorm = take((size_t)T * 4);
+        p.off_hscale = take((size_t)p.slots * 4);
+        p.off_hplanes = take(f32 ? (size_t)2 * p.slots * p.ldh * 2 : 0);
+    }
+    p.total = at;
     return p;
 }
 
@@ -108,21 +178,11 @@ hipError_t launch_q4_moe(const MoePlan &p, const void *x, const int32_t *idx, co
     char *b = static_cast<char *>(ws);
     int32_t *ntiles = reinterpret_cast<int32_t *>(b), *order = reinterpret_cast<int32_t *>(b + p.off_order);
     int4 *tiles = reinterpret_cast<int4 *>(b + p.off_tiles);
-    float *h = reinterpret_cast<float *>(b + p.off_h), *part = reinterpret_cast<float *>(b + p.off_part);
+    const float *part = reinterpret_cast<const float *>(b + p.off_part);
     moe_plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(idx, (int)p.slots, gate.E, (int)p.tile_rows, order, tiles, ntiles);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    Q4Args g{};
-    g.w = gate, g.w2 = up, g.x = x, g.y = h, g.topk = (int)k, g.order = order, g.tiles = tiles, g.ntiles = ntiles;
-    g.weights = weights;
-    Q4Args d = g;
-    d.w = down, d.x = h, d.y = part;
-    if (dtype == kF16) e = product<kXF16, kGateUp>(p, g, s);
-    else if (dtype == kBF16) e = product<kXBF16, kGateUp>(p, g, s);
-    else e = product<kXF32x3, kGateUp>(p, g, s);
-    if (e != hipSuccess) return e;
-    // h for a 16-bit result is taken in 16 bits (two bfloat16 parts, relative error 2^-17)
-    e = dtype == kF32 ? product<kXF32x3, kDown>(p, d, s) : product<kXF32x2, kDown>(p, d, s);
+    e = p.tiled ? tiled(p, x, weights, gate, up, down, T, k, dtype, b, s) : skinny(p, x, weights, gate, up, down, k, dtype, b, s);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)((T * down.N / 4 + 255) / 256));
     if (dtype == kF16) moe_sum_kernel<kF16><<<grid, dim3(256), 0, s>>>(part, idx, y, T, (int)k, gate.E, down.N);

@@ -1,0 +1,299 @@
+// Products of many rows with a 4-bit weight, on tiles of BM rows by 256 columns.
+//
+// A workgroup of eight waves; wave w owns two blocks of 16 columns and all BM rows,
+// so every code is decoded once per tile.  x comes as f16 planes (q4_prep_kernel) and
+// goes through registers into two LDS buffers of 128 k, swizzled so that the 16 rows
+// of a fragment read lie on distinct banks; codes and scales go from memory straight
+// into the registers of the wave that decodes them, a unit of 128 k ahead.  One barrier
+// per unit; while unit u is multiplied, unit u+1 moves into the other buffer and the
+// loads of u+2 are sent.
+//
+// The codes are decoded to code - zero, exact in f16, and each group's sum is scaled in f32:
+// acc += scale * part.  Products are exact for f16 x.  bfloat16 rows are
+// brought to f16 by a power of two per row (their 8 bits fit; see q4_prep_kernel), and f32 rows
+// to two f16 parts.
+#pragma once
+
+#include "q4.h"
+
+namespace tq2 {
+
+// kTDense: y = x W^T.  kTGateUp: column block 2i is gate's, 2i+1 up's;
+// h[p][n] = silu(g) u at sorted place p.  kTDown: part[slot][n] = weight[slot] * sum.
+enum Q4TMode { kTDense = 0, kTGateUp = 1, kTDown = 2 };
+
+struct Q4TArgs {
+    Q4View w, w2;
+    const _Float16 *a;       // [planes][rows][lda]
+    int64_t plane, lda;      // elements
+    const float *rowscale;   // [rows]: the power of two that each row was divided by (nullptr: 1)
+    void *y;
+    int64_t M;               // kTDense: rows
+    int tiles_n;
+    int topk;
+    const int32_t *order;
+    const int4 *tiles;
+    const int32_t *ntiles;
+    const float *weights;
+    const int32_t *norm_exp; // kTGateUp, f16 h: exponent above each token's squared norm
+    float *hscale;           // kTGateUp, f16 h: the power of two that each place's row was divided by
+    int64_t ldh;             // kTGateUp, f16 h: row length, whole units of 128 (zeros past N)
+};
+
+__device__ __forceinline__ int q4_lds(int row, int chunk) { return row * 128 + ((chunk ^ (row & 15)) << 3); }
+
+// code - zero of a word's eight codes: the codes inserted into 1024 (or, four bits
+// higher, read as 1024 + 16 code and divided by 16), the zero point taken off; all exact.
+__device__ __forceinline__ h8 q4_word_f16(uint32_t w, uint32_t c0, uint32_t c1, uint32_t magic) {
+    constexpr uint32_t m0 = 0x000F000Fu, m1 = 0x00F000F0u;
+    const h2 k = {(_Float16)0.0625f, (_Float16)0.0625f};
+    const uint32_t v = w >> 8;
+    const h2 p0 = as_h2((w & m0) | (magic & ~m0)) + as_h2(c0);
+    const h2 p1 = __builtin_elementwise_fma(as_h2((w & m1) | (magic & ~m1)), k, as_h2(c1));
+    const h2 p2 = as_h2((v & m0) | (magic & ~m0)) + as_h2(c0);
+    const h2 p3 = __builtin_elementwise_fma(as_h2((v & m1) | (magic & ~m1)), k, as_h2(c1));
+    return h8{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+}
+
+// The power of two by which a row's silu(g) u is divided before it is rounded to f16,
+// so that it stays below 2^15 whatever the weights: |g| <= |x| |w| and |w| <= sqrt(K)
+// most |scale|, likewise u.  The bound lies some 2^14 above typical values, below which
+// f16 has 14 more binades with all its bits.  norm_exp: 2^norm_exp >= |x|^2.
+__device__ __forceinline__ int q4_h_exp(int norm_exp, uint32_t gate_most, uint32_t up_most, int K, bool zeros) {
+    int eg, eu;
+    (void)__builtin_frexpf(__builtin_bit_cast(float, gate_most), &eg);
+    (void)__builtin_frexpf(__builtin_bit_cast(float, up_most), &eu);
+    const int ek = 32 - __builtin_clz(K) + (zeros ? 8 : 6);  // 2^ek >= K most^2, most = 15 (stored zero points) or 8
+    const int e = norm_exp + eg + eu + ek - 15;
+    return e < -100 ? -100 : e > 100 ? 100 : e;
+}
+
+template <int BM, int G, int P, int MODE, int DT>
+__global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
+    constexpr int RB = BM / 16, GPU_ = 128 / G, NCB = 2;
+    constexpr int PPT = BM * 16 / 512;  // 16-byte pieces of a plane's tile per thread
+    __shared__ __attribute__((aligned(16))) _Float16 As[2][P][BM * 128];
+    __shared__ float rs[BM];
+    __shared__ int hexp[BM];
+
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, h = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ku = p.w.ku;
+    const uint32_t magic = f16_magic();
+
+    // Workgroups go round the 8 XCDs: give each XCD a run of neighbouring tiles, N first.
+    int tile = blockIdx.x;
+    const int tiles = gridDim.x;
+    if ((tiles & 7) == 0) tile = (tile & 7) * (tiles >> 3) + (tile >> 3);
+    const int tn = tile % p.tiles_n, tm = tile / p.tiles_n;
+    int e = 0, count;
+    int64_t row0;
+    if constexpr (MODE == kTDense) {
+        row0 = (int64_t)tm * BM;
+        if (row0 >= p.M) return;  // the grid is whole runs of tiles; the whole workgroup
+        count = p.M - row0 < BM ? (int)(p.M - row0) : BM;
+    } else {
+        if (tm >= *p.ntiles) return;  // the whole workgroup
+        const int4 t = p.tiles[tm];
+        e = t.x, row0 = t.y, count = t.z;
+    }
+    auto source = [&](int row) -> int64_t {  // row of A; rows past the last repeat it
+        const int64_t at = row0 + (row < count ? row : count - 1);
+        return MODE == kTGateUp ? (int64_t)(p.order[at] / p.topk) : at;
+    };
+    if (tid < BM) {
+        const int64_t s = source(tid);
+        rs[tid] = p.rowscale ? p.rowscale[s] : 1.0f;
+        if constexpr (MODE == kTGateUp && P == 1) {
+            const int ex = q4_h_exp(p.norm_exp[s], p.w.head[e], p.w2.head[e], p.w.K, p.w.zeros != nullptr);
+            hexp[tid] = ex;
+            if (tn == 0 && tid < count) p.hscale[row0 + tid] = __builtin_ldexpf(1.0f, ex);
+        }
+    }
+    const _Float16 *ap[PPT];
+    int al[PPT];
+#pragma unroll
+    for (int c = 0; c < PPT; ++c) {
+        const int piece = tid + c * 512, row = piece >> 4, chunk = piece & 15;
+        ap[c] = p.a + source(row) * p.lda + chunk * 8;
+        al[c] = q4_lds(row, chunk);
+    }
+    const w4 *cp[NCB];
+    const uint16_t *sp[NCB];
+    const uint8_t *zp[NCB];
+    const bool zeros = p.w.zeros != nullptr;
+    int nb[NCB];
+#pragma unroll
+    for (int cb = 0; cb < NCB; ++cb) {
+        const Q4View &w = MODE == kTGateUp && cb ? p.w2 : p.w;
+        nb[cb] = MODE == kTGateUp ? tn * 8 + wave : tn * 16 + wave * 2 + cb;
+        const int at = nb[cb] < w.nb ? nb[cb] : w.nb - 1;  // past the last: its results are not stored
+        const int64_t unit = ((int64_t)e * w.nb + at) * ku;
+        cp[cb] = w.codes + unit * 64 + lane;
+        sp[cb] = w.scales + (unit * 16 + r) * GPU_;
+        zp[cb] = zeros ? w.zeros + (unit * 16 + r) * GPU_ : nullptr;
+    }
+    w4 areg[P][PPT];
+    auto load_a = [&](int u) {
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+#pragma unroll
+            for (int c = 0; c < PPT; ++c) areg[q][c] = *reinterpret_cast<const w4 *>(ap[c] + q * p.plane + (int64_t)u * 128);
+    };
+    auto store_a = [&](int buf) {
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+#pragma unroll
+            for (int c = 0; c < PPT; ++c) *reinterpret_cast<w4 *>(&As[buf][q][al[c]]) = areg[q][c];
+    };
+    w4 breg[2][NCB];
+    uint2 sreg[2][NCB];
+    uint32_t zreg[2][NCB];
+    auto load_b = [&](int st, int u) {
+#pragma unroll
+        for (int cb = 0; cb < NCB; ++cb) {
+            breg[st][cb] = cp[cb][(int64_t)u * 64];
+            const uint16_t *s = sp[cb] + (int64_t)u * (16 * GPU_);
+            if constexpr (G == 128) sreg[st][cb].x = *s;
+            if constexpr (G == 64) sreg[st][cb].x = *reinterpret_cast<const uint32_t *>(s);
+            if constexpr (G == 32) sreg[st][cb] = *reinterpret_cast<const uint2 *>(s);
+            zreg[st][cb] = 0x08080808u;
+            if (zeros) {
+                const uint8_t *z = zp[cb] + (int64_t)u * (16 * GPU_);
+                if constexpr (G == 128) zreg[st][cb] = *z;
+                if constexpr (G == 64) zreg[st][cb] = *reinterpret_cast<const uint16_t *>(z);
+                if constexpr (G == 32) zreg[st][cb] = *reinterpret_cast<const uint32_t *>(z);
+            }
+        }
+    };
+
+    f4 acc[RB][NCB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int cb = 0; cb < NCB; ++cb) acc[rb][cb] = f4{};
+    auto compute = [&](int buf, int st, auto &&hook) {
+        h8 b[NCB][4];
+        float s[NCB][GPU_];
+#pragma unroll
+        for (int cb = 0; cb < NCB; ++cb)
+#pragma unroll
+            for (int g = 0; g < GPU_; ++g) {
+                s[cb][g] = half_bits((g & 2 ? sreg[st][cb].y : sreg[st][cb].x) >> (16 * (g & 1)));
+                const uint32_t z = (zreg[st][cb] >> (8 * g)) & 255u;
+                const uint32_t c0 = (0xE400u | z) * 0x10001u;
+                const _Float16 f = (_Float16)(-64.0f - (float)z);
+                const uint32_t c1 = (uint32_t)__builtin_bit_cast(uint16_t, f) * 0x10001u;
+#pragma unroll
+                for (int j = g * G / 32; j < (g + 1) * G / 32; ++j) b[cb][j] = q4_word_f16(breg[st][cb][j], c0, c1, magic);
+            }
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            h8 a[P][4];
+#pragma unroll
+            for (int q = 0; q < P; ++q)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    a[q][j] = *reinterpret_cast<const h8 *>(&As[buf][q][q4_lds(rb * 16 + r, 4 * j + h)]);
+#pragma unroll
+            for (int cb = 0; cb < NCB; ++cb)
+#pragma unroll
+                for (int g = 0; g < GPU_; ++g) {
+                    f4 part = {};
+#pragma unroll
+                    for (int q = P - 1; q >= 0; --q)
+#pragma unroll
+                        for (int j = g * G / 32; j < (g + 1) * G / 32; ++j)
+                            part = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[q][j], b[cb][j], part, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[rb][cb][i] += s[cb][g] * part[i];
+                }
+            if (rb == 0) hook();
+        }
+    };
+
+    auto last = [&](int u) { return u < ku ? u : ku - 1; };
+    load_a(0);
+    load_b(0, 0);
+    load_b(1, last(1));
+    store_a(0);
+    load_a(last(1));
+    __syncthreads();
+    for (int u0 = 0; u0 < ku; u0 += 2) {
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            const int u = u0 + st;
+            if (u < ku) {
+                compute(st, st, [&] {
+                    store_a(st ^ 1);
+                    load_a(last(u + 2));
+                });
+                load_b(st, last(u + 2));
+                __syncthreads();
+            }
+        }
+    }
+
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        if constexpr (MODE == kTGateUp) {
+            const int n = nb[0] * 16 + r;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = rb * 16 + 4 * h + i;
+                if (m >= count) continue;
+                const float g = acc[rb][0][i] * rs[m], u = acc[rb][1][i] * rs[m];
+                const float v = n < p.w.N ? g / (1.0f + expf(-g)) * u : 0.0f;
+                if constexpr (P == 1)  // a tile covers a whole unit of h
+                    static_cast<_Float16 *>(p.y)[(row0 + m) * p.ldh + n] = (_Float16)__builtin_ldexpf(v, -hexp[m]);
+                else if (n < p.w.N)
+                    static_cast<float *>(p.y)[(row0 + m) * p.w.N + n] = v;
+            }
+        } else {
+#pragma unroll
+            for (int cb = 0; cb < NCB; ++cb) {
+                const int n = nb[cb] * 16 + r;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int m = rb * 16 + 4 * h + i;
+                    if (m >= count || n >= p.w.N) continue;
+                    const float v = acc[rb][cb][i] * rs[m];
+                    if constexpr (MODE == kTDense) {
+                        store_from_float<DT>(p.y, (row0 + m) * p.w.N + n, v);
+                    } else {
+                        const int slot = p.order[row0 + m];
+                        static_cast<float *>(p.y)[(int64_t)slot * p.w.N + n] = p.weights[slot] * v;
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int BM, int G, int P, int MODE, int DT>
+inline hipError_t run_q4_tiled(Q4TArgs a, int64_t tiles_m, hipStream_t s) {
+    a.tiles_n = MODE == kTGateUp ? (a.w.nb + 7) / 8 : (a.w.nb + 15) / 16;
+    const int64_t grid = (tiles_m * a.tiles_n + 7) / 8 * 8;
+    q4_tiled_kernel<BM, G, P, MODE, DT><<<dim3((unsigned)grid), dim3(512), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+// x as f16 planes (see q4_tiled.hip).
+struct Q4Prep {
+    const void *x;
+    int64_t rows;
+    int K;
+    int64_t lda, plane;      // of the planes (elements)
+    _Float16 *out;           // nullptr: only norm_exp (f16 x used as it is)
+    float *rowscale;
+    int32_t *norm_exp;       // or nullptr
+};
+hipError_t launch_q4_prep(const Q4Prep &p, int dtype, hipStream_t s);
+// Whether x is read as it is: f16 rows of whole units.
+inline bool q4_plain_x(int64_t K, int dtype) { return dtype == kF16 && K % 128 == 0; }
+inline int q4_planes(int dtype) { return dtype == kF32 ? 2 : 1; }
+hipError_t launch_q4_tiled_dense(const Q4TArgs &a, int dtype, int bm, hipStream_t s);
+hipError_t launch_q4_tiled_gate_up(const Q4TArgs &a, int planes, int bm, int64_t tiles, hipStream_t s);
+hipError_t launch_q4_tiled_down(const Q4TArgs &a, int planes, int bm, int64_t tiles, hipStream_t s);
+
+}  // namespace tq2

@@ -1,0 +1,139 @@
+// Launches of the tiled 4-bit products, and x as f16 planes for them.
+#include "q4_tiled.h"
+
+namespace tq2 {
+
+namespace {
+
+// One wave per row.  bfloat16 and f32 rows are multiplied by the power of two that
+// brings their largest finite value into [2^14, 2^15): bfloat16's 8 bits are then exact
+// in f16 down to 2^-32 of the row's largest value, and below that the error is at most 2^-40 of
+// it, sixteen bits under the f32 sums' own.  f32 rows become hi + lo: 22 bits, the sum of
+// two f16 parts, with the same floor.  Past K up to whole units the planes hold zeros.
+template <int DT, int P>
+__global__ __launch_bounds__(256) void q4_prep_kernel(Q4Prep p) {
+    const int lane = threadIdx.x & 63;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= p.rows) return;
+    constexpr int V = DT == kF32 ? 4 : 8;  // elements of a 16-byte piece
+    auto piece = [&](int i, float *v) {    // K is a multiple of 32: whole pieces
+        const int64_t at = row * p.K + (int64_t)i * V;
+        if constexpr (DT == kF32) {
+            const f4 x = *reinterpret_cast<const f4 *>(static_cast<const float *>(p.x) + at);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = x[q];
+        } else {
+            const w4 x = *reinterpret_cast<const w4 *>(static_cast<const uint16_t *>(p.x) + at);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (DT == kBF16) {
+                    v[2 * q] = __builtin_bit_cast(float, x[q] << 16);
+                    v[2 * q + 1] = __builtin_bit_cast(float, x[q] & 0xffff0000u);
+                } else {
+                    v[2 * q] = half_bits(x[q]);
+                    v[2 * q + 1] = half_bits(x[q] >> 16);
+                }
+            }
+        }
+    };
+    const int pieces = p.K / V;
+    int shift = 0;
+    if constexpr (DT != kF16) {
+        float most = 0.0f;
+        for (int i = lane; i < pieces; i += 64) {
+            float v[V];
+            piece(i, v);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float a = __builtin_fabsf(v[q]);
+                most = a > most && a < __builtin_inff() ? a : most;
+            }
+        }
+        for (int o = 1; o < 64; o <<= 1) most = fmaxf(most, __shfl_xor(most, o));
+        if (most > 0.0f) {
+            int e;
+            (void)__builtin_frexpf(most, &e);  // most in [2^(e-1), 2^e)
+            shift = 15 - e;
+            shift = shift > 126 ? 126 : shift;
+        }
+    }
+    float norm = 0.0f;
+    const int padded = (int)(p.lda / V);
+    for (int i = lane; i < (p.out ? padded : pieces); i += 64) {
+        float v[V] = {};
+        if (i < pieces) piece(i, v);
+        _Float16 hi[V], lo[V];
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            const float x = DT == kF16 ? v[q] : __builtin_ldexpf(v[q], shift);
+            norm += x * x;
+            hi[q] = (_Float16)x;
+            if constexpr (P == 2) lo[q] = __builtin_isfinite(x) ? (_Float16)(x - (float)hi[q]) : (_Float16)0.0f;
+        }
+        if (p.out) {
+            typedef _Float16 hv __attribute__((ext_vector_type(V)));
+            hv a, b;
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                a[q] = hi[q];
+                if constexpr (P == 2) b[q] = lo[q];
+            }
+            *reinterpret_cast<hv *>(p.out + row * p.lda + (int64_t)i * V) = a;
+            if constexpr (P == 2) *reinterpret_cast<hv *>(p.out + p.plane + row * p.lda + (int64_t)i * V) = b;
+        }
+    }
+    if (p.rowscale && lane == 0) p.rowscale[row] = __builtin_ldexpf(1.0f, -shift);
+    if (p.norm_exp) {
+        for (int o = 1; o < 64; o <<= 1) norm += __shfl_xor(norm, o);
+        int e = -200;
+        if (norm > 0.0f && norm < __builtin_inff()) {
+            (void)__builtin_frexpf(norm, &e);
+            e += 1 - 2 * shift;  // one more for the sum's own rounding
+        }
+        if (lane == 0) p.norm_exp[row] = e;
+    }
+}
+
+template <int G>
+hipError_t dense(const Q4TArgs &a, int dtype, int bm, hipStream_t s) {
+    const int64_t t64 = (a.M + 63) / 64, t128 = (a.M + 127) / 128;
+    if (dtype == kF32) return bm == 64 ? run_q4_tiled<64, G, 2, kTDense, kF32>(a, t64, s) : run_q4_tiled<128, G, 2, kTDense, kF32>(a, t128, s);
+    if (dtype == kF16) return bm == 64 ? run_q4_tiled<64, G, 1, kTDense, kF16>(a, t64, s) : run_q4_tiled<128, G, 1, kTDense, kF16>(a, t128, s);
+    return bm == 64 ? run_q4_tiled<64, G, 1, kTDense, kBF16>(a, t64, s) : run_q4_tiled<128, G, 1, kTDense, kBF16>(a, t128, s);
+}
+
+template <int G, int MODE>
+hipError_t grouped(const Q4TArgs &a, int planes, int bm, int64_t tiles, hipStream_t s) {
+    if (planes == 1) return bm == 64 ? run_q4_tiled<64, G, 1, MODE, kF32>(a, tiles, s) : run_q4_tiled<128, G, 1, MODE, kF32>(a, tiles, s);
+    return bm == 64 ? run_q4_tiled<64, G, 2, MODE, kF32>(a, tiles, s) : run_q4_tiled<128, G, 2, MODE, kF32>(a, tiles, s);
+}
+
+}  // namespace
+
+hipError_t launch_q4_prep(const Q4Prep &p, int dtype, hipStream_t s) {
+    const dim3 grid((unsigned)((p.rows + 3) / 4)), block(256);
+    if (dtype == kF32) q4_prep_kernel<kF32, 2><<<grid, block, 0, s>>>(p);
+    else if (dtype == kF16) q4_prep_kernel<kF16, 1><<<grid, block, 0, s>>>(p);
+    else q4_prep_kernel<kBF16, 1><<<grid, block, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_q4_tiled_dense(const Q4TArgs &a, int dtype, int bm, hipStream_t s) {
+    if (a.w.G == 32) return dense<32>(a, dtype, bm, s);
+    if (a.w.G == 64) return dense<64>(a, dtype, bm, s);
+    return dense<128>(a, dtype, bm, s);
+}
+
+hipError_t launch_q4_tiled_gate_up(const Q4TArgs &a, int planes, int bm, int64_t tiles, hipStream_t s) {
+    if (a.w.G == 32) return grouped<32, kTGateUp>(a, planes, bm, tiles, s);
+    if (a.w.G == 64) return grouped<64, kTGateUp>(a, planes, bm, tiles, s);
+    return grouped<128, kTGateUp>(a, planes, bm, tiles, s);
+}
+
+hipError_t launch_q4_tiled_down(const Q4TArgs &a, int planes, int bm, int64_t tiles, hipStream_t s) {
+    if (a.w.G == 32) return grouped<32, kTDown>(a, planes, bm, tiles, s);
+    if (a.w.G == 64) return grouped<64, kTDown>(a, planes, bm, tiles, s);
+    return grouped<128, kTDown>(a, planes, bm, tiles, s);
+}
+
+}  // namespace tq2
