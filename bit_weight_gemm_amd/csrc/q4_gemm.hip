@@ -10,54 +10,57 @@ __global__ __launch_bounds__(1024) void q4_head_kernel(uint32_t *head, int E) {
     if ((int)threadIdx.x < E) head[threadIdx.x] = 0;
 }
 
-// One thread per lane of a unit: its four words, each from four consecutive bytes of
-// the row-major codes; the first 16 lanes also bring their row's scales and zeros.
-// The head collects each expert's largest |scale| (integer maximum: the order does not matter).
+// One workgroup per block of 16 rows of an expert, its four waves taking the units in
+// turn.  Lane (r, h) reads 16 bytes of row r (k = 128u + 32h .. +31), orders the nibbles
+// and hands word c to lane (r, c) as its word h; the first 16 lanes also bring their
+// row's scales and zeros.  The head collects each expert's largest |scale| (integer
+// maximum: the order does not matter), which a wave adds to only where it is larger.
 __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros,
-                                                      Q4View v, w4 *oc, uint16_t *os, uint8_t *oz, uint32_t *head,
-                                                      int64_t units) {
-    const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t unit = gid >> 6;
-    const int lane = gid & 63, r = lane & 15, h = lane >> 4;
+                                                      Q4View v, w4 *oc, uint16_t *os, uint8_t *oz, uint32_t *head) {
+    __shared__ uint32_t words[4][16][4][4 + 1];  // [wave][r][h of the reader][word]
+    const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4, wave = threadIdx.x >> 6;
+    const int nb = blockIdx.x, e = blockIdx.y;
+    const int n = nb * 16 + r;
+    const int64_t row = (int64_t)e * v.N + n, unit0 = ((int64_t)e * v.nb + nb) * v.ku;
+    const int gpu = 128 / v.G, kg = v.K / v.G;
     uint32_t most = 0;
-    if (unit < units) {
-        const int u = (int)(unit % v.ku);
-        const int64_t eb = unit / v.ku;
-        const int nb = (int)(eb % v.nb);
-        const int64_t e = eb / v.nb;
-        const int n = nb * 16 + r;
-        w4 out = {0, 0, 0, 0};
-        const int64_t row = e * v.N + n;
-        if (n < v.N) {
-            for (int j = 0; j < 4; ++j) {
-                const int k = u * 128 + 32 * j + 8 * h;
-                if (k >= v.K) break;
-                const uint32_t b = *reinterpret_cast<const uint32_t *>(codes + (row * v.K + k) / 2);
-                uint32_t w = 0;
-                for (int s = 0; s < 4; ++s)
-                    w |= ((b >> (8 * s)) & 15u) << (4 * s) | ((b >> (8 * s + 4)) & 15u) << (16 + 4 * s);
-                out[j] = w;
-            }
+    for (int u0 = 0; u0 < v.ku; u0 += 4) {
+        const int u = u0 + wave;
+        const int k = u * 128 + 32 * h;  // K is a multiple of 32: whole pieces
+        w4 in = {0, 0, 0, 0};
+        if (n < v.N && u < v.ku && k < v.K) {
+            const uint32_t *b = reinterpret_cast<const uint32_t *>(codes + (row * v.K + k) / 2);
+            in = w4{b[0], b[1], b[2], b[3]};
         }
-        oc[gid] = out;
-        if (h == 0) {
-            const int gpu = 128 / v.G, kg = v.K / v.G;
-            for (int g = 0; g < gpu; ++g) {
-                const int kgi = u * gpu + g;
-                const bool in = n < v.N && kgi < kg;
-                const uint16_t s = in ? scales[row * kg + kgi] : 0;
-                os[(unit * 16 + r) * gpu + g] = s;
-                if (oz) oz[(unit * 16 + r) * gpu + g] = in ? zeros[row * kg + kgi] : 8;
-                const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_fabsf(half_bits(s)));
-                most = a > most ? a : most;
-            }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                w |= ((in[c] >> (8 * s)) & 15u) << (4 * s) | ((in[c] >> (8 * s + 4)) & 15u) << (16 + 4 * s);
+            words[wave][r][h][c] = w;
         }
+        __syncthreads();
+        if (u < v.ku) {
+            oc[(unit0 + u) * 64 + lane] = w4{words[wave][r][0][h], words[wave][r][1][h], words[wave][r][2][h], words[wave][r][3][h]};
+            if (h == 0)
+                for (int g = 0; g < gpu; ++g) {
+                    const int at = u * gpu + g;
+                    const bool has = n < v.N && at < kg;
+                    const uint16_t s = has ? scales[row * kg + at] : 0;
+                    os[((unit0 + u) * 16 + r) * gpu + g] = s;
+                    if (oz) oz[((unit0 + u) * 16 + r) * gpu + g] = has ? zeros[row * kg + at] : 8;
+                    const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_fabsf(half_bits(s)));
+                    most = a > most ? a : most;
+                }
+        }
+        __syncthreads();
     }
     for (int o = 1; o < 64; o <<= 1) {
         const uint32_t b = (uint32_t)__shfl_xor((int)most, o);
         most = b > most ? b : most;
     }
-    if (lane == 0 && most) atomicMax(&head[unit / v.ku / v.nb], most);
+    if (lane == 0 && most > *const_cast<volatile uint32_t *>(&head[e])) atomicMax(&head[e], most);
 }
 
 __global__ __launch_bounds__(256) void q4_dequant_kernel(Q4View v, float *out) {
@@ -70,13 +73,12 @@ __global__ __launch_bounds__(256) void q4_dequant_kernel(Q4View v, float *out) {
 
 template <int XT, int G>
 hipError_t dense(const Q4Args &a, hipStream_t s) {
-    // Column blocks per workgroup: one while that fits the 256 compute units in one
-    // round of workgroups, more beyond, so that x is read less often.
+    // Column blocks per wave: one while that fits the 256 compute units in two
+    // rounds of workgroups, more beyond, so that x is read less often.
     const int64_t nb = a.w.nb;
     if (a.M <= 16) {
         if (nb <= 512) return run_q4_skinny<XT, G, 1, 1, kDense>(a, 1, s);
-        if (nb <= 1024) return run_q4_skinny<XT, G, 1, 2, kDense>(a, 1, s);
-        return run_q4_skinny<XT, G, 1, 4, kDense>(a, 1, s);
+        return run_q4_skinny<XT, G, 1, 2, kDense>(a, 1, s);
     }
     if (a.M <= 32 || XT == kXF32x3) return run_q4_skinny<XT, G, 2, 2, kDense>(a, (a.M + 31) / 32, s);
     return run_q4_skinny<XT, G, 4, 2, kDense>(a, (a.M + 63) / 64, s);
@@ -95,10 +97,9 @@ hipError_t launch_q4_pack(const uint8_t *codes, const uint16_t *scales, const ui
                           hipStream_t s) {
     uint32_t *head = const_cast<uint32_t *>(v.head);
     q4_head_kernel<<<dim3(1), dim3(1024), 0, s>>>(head, v.E);
-    const int64_t units = (int64_t)v.E * v.nb * v.ku;
-    q4_pack_kernel<<<dim3((unsigned)((units + 3) / 4)), dim3(256), 0, s>>>(
+    q4_pack_kernel<<<dim3((unsigned)v.nb, (unsigned)v.E), dim3(256), 0, s>>>(
         codes, scales, zeros, v, const_cast<w4 *>(v.codes), const_cast<uint16_t *>(v.scales),
-        const_cast<uint8_t *>(v.zeros), head, units);
+        const_cast<uint8_t *>(v.zeros), head);
     return hipGetLastError();
 }
 

@@ -5,7 +5,7 @@
 // sorted by expert, and the list of row tiles), the gate and up products with
 // silu(g) u in their epilogue, the down product times the slot's weight, and the
 // sum of each token's slots in slot order.
-#include "q4_skinny.h"
+#include "q4_row.h"
 #include "q4_tiled.h"
 
 namespace tq2 {
@@ -86,6 +86,38 @@ hipError_t product(const MoePlan &p, const Q4Args &a, hipStream_t s) {
     return product_rb<XT, 128, MODE>(p, a, s);
 }
 
+template <int XT, int PH>
+hipError_t row_gate_up(const Q4RowArgs &a, int64_t slots, hipStream_t s) {
+    if (a.w.G == 32) return run_q4_row<XT, 32, 2, 8, 2, kRowGateUp, PH, kF32>(a, slots, s);
+    if (a.w.G == 64) return run_q4_row<XT, 64, 2, 8, 2, kRowGateUp, PH, kF32>(a, slots, s);
+    return run_q4_row<XT, 128, 2, 8, 2, kRowGateUp, PH, kF32>(a, slots, s);
+}
+
+template <int XT, int DT>
+hipError_t row_down_sum(const Q4RowArgs &a, int64_t T, hipStream_t s) {
+    if (a.w.G == 32) return run_q4_row<XT, 32, 1, 16, 4, kRowDownSum, 1, DT>(a, T, s);
+    if (a.w.G == 64) return run_q4_row<XT, 64, 1, 16, 4, kRowDownSum, 1, DT>(a, T, s);
+    return run_q4_row<XT, 128, 1, 16, 4, kRowDownSum, 1, DT>(a, T, s);
+}
+
+// A few slots: two launches, every slot with its own expert's weights; h in two
+// bfloat16 parts (relative error 2^-17) for 16-bit types, in three, which are exact, for f32.
+hipError_t direct(const MoePlan &p, const void *x, const int32_t *idx, const float *weights, const Q4View &gate,
+                  const Q4View &up, const Q4View &down, void *y, int64_t T, int64_t k, int dtype, char *b, hipStream_t s) {
+    Q4RowArgs g{};
+    g.w = gate, g.w2 = up, g.x = x, g.y = b + p.off_h, g.topk = (int)k, g.weights = weights, g.idx = idx, g.ldh = p.ldh;
+    hipError_t e;
+    if (dtype == kF16) e = row_gate_up<kXF16, 2>(g, p.slots, s);
+    else if (dtype == kBF16) e = row_gate_up<kXBF16, 2>(g, p.slots, s);
+    else e = row_gate_up<kXF32x3, 3>(g, p.slots, s);
+    if (e != hipSuccess) return e;
+    Q4RowArgs d = g;
+    d.w = down, d.x = g.y, d.y = y;
+    if (dtype == kF16) return row_down_sum<kXF32x2, kF16>(d, T, s);
+    if (dtype == kBF16) return row_down_sum<kXF32x2, kBF16>(d, T, s);
+    return row_down_sum<kXF32x3, kF32>(d, T, s);
+}
+
 // Few rows per expert: tiles of 16 or 32 rows, h in f32.
 hipError_t skinny(const MoePlan &p, const void *x, const float *weights, const Q4View &gate, const Q4View &up,
                   const Q4View &down, int64_t k, int dtype, char *b, hipStream_t s) {
@@ -142,15 +174,21 @@ hipError_t tiled(const MoePlan &p, const void *x, const float *weights, const Q4
 
 }  // namespace
 
+// Up to kDirectSlots slots, each reads its expert's weights for itself; their rows have to fit in LDS.
+constexpr int64_t kDirectSlots = 32;
+constexpr size_t kDirectLds = 48 * 1024;
+
 MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtype) {
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     MoePlan p{};
     const bool plain = q4_plain_x(d, dtype), f32 = dtype == kF32;
     p.slots = T * k;
-    p.tiled = p.slots > 32 * E;
+    p.ldx = (d + 127) / 128 * 128, p.ldh = (f + 127) / 128 * 128;
+    p.direct = p.slots <= kDirectSlots && q4_row_lds(p.ldx / 128, f32 ? 3 : 1) <= kDirectLds &&
+               q4_row_lds(k * (p.ldh / 128), f32 ? 3 : 2) <= kDirectLds;
+    p.tiled = !p.direct && p.slots > 32 * E;
     p.tile_rows = p.tiled ? (p.slots > 96 * E ? 128 : 64) : p.slots <= 16 * E ? 16 : 32;
     p.max_tiles = p.slots / p.tile_rows + (E < p.slots ? E : p.slots);
-    p.ldx = (d + 127) / 128 * 128, p.ldh = (f + 127) / 128 * 128;
     size_t at = 256;  // the first 256 bytes hold the number of tiles
     auto take = [&](size_t n) {
         const size_t off = at;
@@ -159,7 +197,7 @@ MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtyp
     };
     p.off_order = take((size_t)p.slots * 4);
     p.off_tiles = take((size_t)p.max_tiles * 16);
-    p.off_h = take((size_t)p.slots * (p.tiled && !f32 ? p.ldh * 2 : f * 4));
+    p.off_h = take((size_t)p.slots * (p.direct ? p.ldh * 6 : p.tiled && !f32 ? p.ldh * 2 : f * 4));
     p.off_part = take((size_t)p.slots * d * 4);
     if (p.tiled) {
         p.off_x = take(plain ? 0 : (size_t)q4_planes(dtype) * T * p.ldx * 2);
@@ -176,6 +214,7 @@ hipError_t launch_q4_moe(const MoePlan &p, const void *x, const int32_t *idx, co
                          const Q4View &up, const Q4View &down, void *y, int64_t T, int64_t k, int dtype, void *ws,
                          hipStream_t s) {
     char *b = static_cast<char *>(ws);
+    if (p.direct) return direct(p, x, idx, weights, gate, up, down, y, T, k, dtype, b, s);
     int32_t *ntiles = reinterpret_cast<int32_t *>(b), *order = reinterpret_cast<int32_t *>(b + p.off_order);
     int4 *tiles = reinterpret_cast<int4 *>(b + p.off_tiles);
     const float *part = reinterpret_cast<const float *>(b + p.off_part);

@@ -1,12 +1,14 @@
 // Products of few rows with a 4-bit weight: y[m][n] = sum_k x[m][k] (code - zero) scale.
 //
-// A workgroup of eight waves owns CB blocks of 16 output columns and RB blocks of
-// 16 rows.  Its waves take the 128-k units in turn (wave w the units w, w+8, ...),
-// so at each turn they read eight adjacent units of a column block.  A wave loads a
-// unit's codes as one contiguous kilobyte per column block and its x straight into
-// the A operand's registers (lane l: row l%16, k = 32j + 8(l/16) .. +7): nothing
-// goes through LDS and no wave waits for another until the eight partial tiles are
-// added, in wave order, at the end.  Both streams run D units ahead.
+// A wave owns CB blocks of 16 output columns and RB blocks of 16 rows.  WK of a
+// workgroup's eight waves share them and take the 128-k units in turn (the w-th the units
+// w, w + WK, ...), so at each turn they read adjacent units of a column block; the
+// others have the next columns.  A wave loads a unit's codes as one contiguous kilobyte
+// per column block and its x straight into the A operand's registers (lane l: row
+// l%16, k = 32j + 8(l/16) .. +7): nothing goes through LDS and no wave waits for
+// another until the WK partial tiles are added, in wave order, at the end.  Both
+// streams run D units ahead.  WK is the smallest that gives the chip eight waves per
+// compute unit: a wave that has one unit only spends its time on its first loads.
 //
 // The codes are decoded to 16 + code (q4_word16); each group's sum is corrected and
 // scaled in f32: acc += scale (part - (16 + zero) S), with S = sum x over the group
@@ -46,6 +48,7 @@ struct Q4Args {
     const int4 *tiles;       // {expert, first place, rows, 0}
     const int32_t *ntiles;
     const float *weights;    // [slots]
+    int log_wk;              // waves that share a column block: 1 << log_wk
 };
 
 template <int XT>
@@ -60,6 +63,30 @@ __device__ __forceinline__ float q4_slow_dot(const void *x, int64_t row, const Q
         acc += v * q4_weight_at(w, e, n, k);
     }
     return acc;
+}
+
+// Eight floats as P bfloat16 parts: each part is cut, so that what is left is exact,
+// except the last of two, which is rounded to nearest even.
+template <int P>
+__device__ __forceinline__ void q4_split(w4 lo, w4 hi, w4 *out) {
+    uint32_t v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t &a = v[2 * i], &b = v[2 * i + 1];
+            if (P == 2 && q == 1) {
+                typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+                const b2 t = {(__bf16)__builtin_bit_cast(float, a), (__bf16)__builtin_bit_cast(float, b)};
+                out[q][i] = __builtin_bit_cast(uint32_t, t);
+                continue;
+            }
+            out[q][i] = __builtin_amdgcn_perm(b, a, 0x07060302u);  // the upper halves
+            if (q + 1 < P) {
+                a = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a) - __builtin_bit_cast(float, a & 0xffff0000u));
+                b = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, b) - __builtin_bit_cast(float, b & 0xffff0000u));
+            }
+        }
 }
 
 template <int XT, int G, int RB, int CB, int D, int MODE>
@@ -85,6 +112,7 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
         const int4 t = p.tiles[blockIdx.y];
         e = t.x, row0 = t.y, count = t.z;
     }
+    const int wk = wave & ((1 << p.log_wk) - 1), wn = wave >> p.log_wk, cols = (8 >> p.log_wk) * NC;
     // rows past the last repeat it (their results are not stored)
     int64_t xoff[RB];
 #pragma unroll
@@ -102,7 +130,7 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
         const Q4View &w = MODE == kGateUp && (cb & 1) ? p.w2 : p.w;
-        int nb = blockIdx.x * NC + (MODE == kGateUp ? cb >> 1 : cb);
+        int nb = blockIdx.x * cols + wn * NC + (MODE == kGateUp ? cb >> 1 : cb);
         nb = nb < w.nb ? nb : w.nb - 1;
         const int64_t unit = ((int64_t)e * w.nb + nb) * ku;
         cp[cb] = w.codes + unit * 64 + lane;
@@ -118,17 +146,8 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
             breg[st][cb] = cp[cb][(int64_t)u * 64];
-            const uint16_t *s = sp[cb] + (int64_t)u * (16 * GPU_);
-            if constexpr (G == 128) sreg[st][cb].x = *s;
-            if constexpr (G == 64) sreg[st][cb].x = *reinterpret_cast<const uint32_t *>(s);
-            if constexpr (G == 32) sreg[st][cb] = *reinterpret_cast<const uint2 *>(s);
-            zreg[st][cb] = 0x08080808u;
-            if (zeros) {
-                const uint8_t *z = zp[cb] + (int64_t)u * (16 * GPU_);
-                if constexpr (G == 128) zreg[st][cb] = *z;
-                if constexpr (G == 64) zreg[st][cb] = *reinterpret_cast<const uint16_t *>(z);
-                if constexpr (G == 32) zreg[st][cb] = *reinterpret_cast<const uint32_t *>(z);
-            }
+            const int64_t at = (int64_t)u * (16 * GPU_);
+            q4_load_groups<G>(sp[cb] + at, zeros ? zp[cb] + at : nullptr, sreg[st][cb], zreg[st][cb]);
         }
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
@@ -145,28 +164,6 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
                 }
             }
     };
-    // the bfloat16 parts of eight floats
-    auto split = [&](w4 lo, w4 hi, w4 *out) {
-        uint32_t v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-#pragma unroll
-        for (int q = 0; q < P; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t &a = v[2 * i], &b = v[2 * i + 1];
-                if (P == 2 && q == 1) {  // the last of two parts is rounded to nearest even
-                    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-                    const b2 t = {(__bf16)__builtin_bit_cast(float, a), (__bf16)__builtin_bit_cast(float, b)};
-                    out[q][i] = __builtin_bit_cast(uint32_t, t);
-                    continue;
-                }
-                out[q][i] = __builtin_amdgcn_perm(b, a, 0x07060302u);  // the upper halves: cut, so the rest is exact
-                if (q + 1 < P) {
-                    a = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a) - __builtin_bit_cast(float, a & 0xffff0000u));
-                    b = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, b) - __builtin_bit_cast(float, b & 0xffff0000u));
-                }
-            }
-    };
-
     f4 acc[RB][CB];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
@@ -182,7 +179,7 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
             w4 a[RB][P];
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) {
-                if constexpr (F32) split(areg[st][rb][2 * j], areg[st][rb][2 * j + 1], a[rb]);
+                if constexpr (F32) q4_split<P>(areg[st][rb][2 * j], areg[st][rb][2 * j + 1], a[rb]);
                 else a[rb][0] = areg[st][rb][j];
                 if constexpr (!EXACT) {
                     if (first) sum[rb] = f4{};
@@ -218,17 +215,17 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
         }
     };
 
-    const int n = (ku - wave + 7) >> 3;  // units of this wave: wave, wave + 8, ...
+    const int step = 1 << p.log_wk, n = (ku - wk + step - 1) >> p.log_wk;  // this wave's units
 #pragma unroll
     for (int st = 0; st < D; ++st)
-        if (st < n) load(st, wave + 8 * st);
+        if (st < n) load(st, wk + step * st);
     for (int t0 = 0; t0 < n; t0 += D) {
 #pragma unroll
         for (int st = 0; st < D; ++st) {
             const int t = t0 + st;
             if (t < n) {
                 compute(st);
-                if (t + D < n) load(st, wave + 8 * (t + D));
+                if (t + D < n) load(st, wk + step * (t + D));
             }
         }
     }
@@ -239,25 +236,24 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
         for (int cb = 0; cb < CB; ++cb) red[wave][rb * CB + cb][lane] = acc[rb][cb];
     __syncthreads();
     // lane l of a tile holds column l%16, rows 4(l/16) .. +3
-    auto total = [&](int blk, int row, int col) {
+    auto total = [&](int group, int blk, int row, int col) {
         const int l = (row >> 2) * 16 + col;
         float v = 0.0f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v += red[q][blk][l][row & 3];
+        for (int q = 0; q < step; ++q) v += red[(group << p.log_wk) + q][blk][l][row & 3];
         return v;
     };
-    for (int it = tid; it < RB * NC * 256; it += 512) {
-        const int blk = it >> 8, rb = blk / NC, cb = blk % NC;
+    for (int it = tid; it < RB * cols * 256; it += 512) {
+        const int blk = it >> 8, cb = blk % NC, rb = blk / NC % RB, group = blk / (NC * RB);
         const int row = (it & 255) >> 4, col = it & 15;
-        const int m = rb * 16 + row, nn = (blockIdx.x * NC + cb) * 16 + col;
+        const int m = rb * 16 + row, nn = (blockIdx.x * cols + group * NC + cb) * 16 + col;
         if (m >= count || nn >= p.w.N) continue;
         if constexpr (MODE == kDense) {
-            float v = total(rb * CB + cb, row, col);
+            float v = total(group, rb * CB + cb, row, col);
             if (!__builtin_isfinite(v)) v = q4_slow_dot<XT>(p.x, (int64_t)row0 + m, p.w, 0, nn);
             constexpr int DT = XT == kXF16 ? kF16 : XT == kXBF16 ? kBF16 : kF32;
             store_from_float<DT>(p.y, ((int64_t)row0 + m) * p.w.N + nn, v);
         } else if constexpr (MODE == kGateUp) {
-            float g = total(rb * CB + 2 * cb, row, col), u = total(rb * CB + 2 * cb + 1, row, col);
+            float g = total(group, rb * CB + 2 * cb, row, col), u = total(group, rb * CB + 2 * cb + 1, row, col);
             if (!__builtin_isfinite(g) || !__builtin_isfinite(u)) {
                 const int64_t tok = p.order[row0 + m] / p.topk;
                 g = q4_slow_dot<XT>(p.x, tok, p.w, e, nn);
@@ -265,7 +261,7 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
             }
             static_cast<float *>(p.y)[((int64_t)row0 + m) * p.w.N + nn] = g / (1.0f + expf(-g)) * u;
         } else {
-            float v = total(rb * CB + cb, row, col);
+            float v = total(group, rb * CB + cb, row, col);
             if (!__builtin_isfinite(v)) v = q4_slow_dot<XT>(p.x, (int64_t)row0 + m, p.w, e, nn);
             const int slot = p.order[row0 + m];
             static_cast<float *>(p.y)[(int64_t)slot * p.w.N + nn] = p.weights[slot] * v;
@@ -273,15 +269,20 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
     }
 }
 
-// Units in flight (D): the codes and x of D units wait in registers, at most 256 a
-// lane with one workgroup of eight waves on a compute unit.
+// The waves per compute unit that a launch wants before it splits a column block's k
+// no further.
+constexpr int64_t kWavesWanted = 2048;
+
 template <int XT, int G, int RB, int CB, int MODE>
-inline hipError_t run_q4_skinny(const Q4Args &a, int64_t grid_y, hipStream_t s) {
+inline hipError_t run_q4_skinny(Q4Args a, int64_t grid_y, hipStream_t s) {
     constexpr int PERX = XT == kXF32x2 || XT == kXF32x3 ? 8 : 4;
     constexpr int REGS = 4 * (RB * PERX + CB);  // registers of one unit in flight
-    constexpr int D = REGS <= 32 ? 4 : REGS <= 72 ? 2 : 1;
+    constexpr int D = REGS <= 20 ? 4 : REGS <= 48 ? 2 : 1;
     constexpr int NC = MODE == kGateUp ? CB / 2 : CB;
-    const dim3 grid((unsigned)((a.w.nb + NC - 1) / NC), (unsigned)grid_y);
+    const int64_t blocks = (a.w.nb + NC - 1) / NC;
+    while (a.log_wk < 3 && (blocks * grid_y << a.log_wk) < kWavesWanted && (2 << a.log_wk) <= a.w.ku) ++a.log_wk;
+    const int64_t wn = 8 >> a.log_wk;
+    const dim3 grid((unsigned)((blocks + wn - 1) / wn), (unsigned)grid_y);
     q4_skinny_kernel<XT, G, RB, CB, D, MODE><<<grid, dim3(512), 0, s>>>(a);
     return hipGetLastError();
 }

@@ -74,7 +74,7 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     constexpr int PPT = BM * 16 / 512;  // 16-byte pieces of a plane's tile per thread
     __shared__ __attribute__((aligned(16))) _Float16 As[2][P][BM * 128];
     __shared__ float rs[BM];
-    __shared__ int hexp[BM];
+    __shared__ int hexp[BM];   // kTGateUp: exponent of the row's h; kTDown: its slot
 
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, h = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -104,6 +104,11 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     if (tid < BM) {
         const int64_t s = source(tid);
         rs[tid] = p.rowscale ? p.rowscale[s] : 1.0f;
+        if constexpr (MODE == kTDown) {
+            const int slot = p.order[s];
+            hexp[tid] = slot;
+            rs[tid] *= p.weights[slot];
+        }
         if constexpr (MODE == kTGateUp && P == 1) {
             const int ex = q4_h_exp(p.norm_exp[s], p.w.head[e], p.w2.head[e], p.w.K, p.w.zeros != nullptr);
             hexp[tid] = ex;
@@ -153,17 +158,8 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
 #pragma unroll
         for (int cb = 0; cb < NCB; ++cb) {
             breg[st][cb] = cp[cb][(int64_t)u * 64];
-            const uint16_t *s = sp[cb] + (int64_t)u * (16 * GPU_);
-            if constexpr (G == 128) sreg[st][cb].x = *s;
-            if constexpr (G == 64) sreg[st][cb].x = *reinterpret_cast<const uint32_t *>(s);
-            if constexpr (G == 32) sreg[st][cb] = *reinterpret_cast<const uint2 *>(s);
-            zreg[st][cb] = 0x08080808u;
-            if (zeros) {
-                const uint8_t *z = zp[cb] + (int64_t)u * (16 * GPU_);
-                if constexpr (G == 128) zreg[st][cb] = *z;
-                if constexpr (G == 64) zreg[st][cb] = *reinterpret_cast<const uint16_t *>(z);
-                if constexpr (G == 32) zreg[st][cb] = *reinterpret_cast<const uint32_t *>(z);
-            }
+            const int64_t at = (int64_t)u * (16 * GPU_);
+            q4_load_groups<G>(sp[cb] + at, zeros ? zp[cb] + at : nullptr, sreg[st][cb], zreg[st][cb]);
         }
     };
 
@@ -261,8 +257,7 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
                     if constexpr (MODE == kTDense) {
                         store_from_float<DT>(p.y, (row0 + m) * p.w.N + n, v);
                     } else {
-                        const int slot = p.order[row0 + m];
-                        static_cast<float *>(p.y)[(int64_t)slot * p.w.N + n] = p.weights[slot] * v;
+                        static_cast<float *>(p.y)[(int64_t)hexp[m] * p.w.N + n] = v;
                     }
                 }
             }

@@ -37,17 +37,31 @@ __global__ __launch_bounds__(256) void q4_prep_kernel(Q4Prep p) {
         }
     };
     const int pieces = p.K / V;
+    // the first kHold pieces of a lane stay in registers between the two passes
+    constexpr int kHold = 8;
+    float held[DT == kF16 ? 1 : kHold][V];
     int shift = 0;
     if constexpr (DT != kF16) {
         float most = 0.0f;
-        for (int i = lane; i < pieces; i += 64) {
-            float v[V];
-            piece(i, v);
+        auto look = [&](const float *v) {
 #pragma unroll
             for (int q = 0; q < V; ++q) {
                 const float a = __builtin_fabsf(v[q]);
                 most = a > most && a < __builtin_inff() ? a : most;
             }
+        };
+#pragma unroll
+        for (int c = 0; c < kHold; ++c) {
+#pragma unroll
+            for (int q = 0; q < V; ++q) held[c][q] = 0.0f;
+            if (lane + 64 * c < pieces) piece(lane + 64 * c, held[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < kHold; ++c) look(held[c]);
+        for (int i = lane + 64 * kHold; i < pieces; i += 64) {
+            float v[V];
+            piece(i, v);
+            look(v);
         }
         for (int o = 1; o < 64; o <<= 1) most = fmaxf(most, __shfl_xor(most, o));
         if (most > 0.0f) {
@@ -59,28 +73,30 @@ __global__ __launch_bounds__(256) void q4_prep_kernel(Q4Prep p) {
     }
     float norm = 0.0f;
     const int padded = (int)(p.lda / V);
-    for (int i = lane; i < (p.out ? padded : pieces); i += 64) {
-        float v[V] = {};
-        if (i < pieces) piece(i, v);
-        _Float16 hi[V], lo[V];
+    auto put = [&](int i, const float *v) {
+        typedef _Float16 hv __attribute__((ext_vector_type(V)));
+        hv a, b;
 #pragma unroll
         for (int q = 0; q < V; ++q) {
             const float x = DT == kF16 ? v[q] : __builtin_ldexpf(v[q], shift);
             norm += x * x;
-            hi[q] = (_Float16)x;
-            if constexpr (P == 2) lo[q] = __builtin_isfinite(x) ? (_Float16)(x - (float)hi[q]) : (_Float16)0.0f;
+            a[q] = (_Float16)x;
+            if constexpr (P == 2) b[q] = __builtin_isfinite(x) ? (_Float16)(x - (float)a[q]) : (_Float16)0.0f;
         }
-        if (p.out) {
-            typedef _Float16 hv __attribute__((ext_vector_type(V)));
-            hv a, b;
+        if (!p.out) return;
+        *reinterpret_cast<hv *>(p.out + row * p.lda + (int64_t)i * V) = a;
+        if constexpr (P == 2) *reinterpret_cast<hv *>(p.out + p.plane + row * p.lda + (int64_t)i * V) = b;
+    };
+    constexpr int kFrom = DT == kF16 ? 0 : kHold;
+    if constexpr (DT != kF16) {
 #pragma unroll
-            for (int q = 0; q < V; ++q) {
-                a[q] = hi[q];
-                if constexpr (P == 2) b[q] = lo[q];
-            }
-            *reinterpret_cast<hv *>(p.out + row * p.lda + (int64_t)i * V) = a;
-            if constexpr (P == 2) *reinterpret_cast<hv *>(p.out + p.plane + row * p.lda + (int64_t)i * V) = b;
-        }
+        for (int c = 0; c < kHold; ++c)
+            if (lane + 64 * c < padded) put(lane + 64 * c, held[c]);
+    }
+    for (int i = lane + 64 * kFrom; i < padded; i += 64) {
+        float v[V] = {};
+        if (i < pieces) piece(i, v);
+        put(i, v);
     }
     if (p.rowscale && lane == 0) p.rowscale[row] = __builtin_ldexpf(1.0f, -shift);
     if (p.norm_exp) {
