@@ -12,14 +12,17 @@
 // it is never chosen, and slots that find no expert get idx -1 and weight 0, which
 // the experts' products skip.  A NaN logit ranks first, so that it shows.
 //
-// Keys that are sums are formed and compared in f64: near ties decide whole numbers,
-// and over 16384 tokens of 256 experts f32 scores swap a pair every few calls.
+// Keys that are sums of scores decide whole numbers in near ties: over 16384 tokens of
+// 256 experts f32 scores swap a pair every few calls, so such keys count in f64.  They
+// are formed in f32 first, with a bound on their error; a token whose decisions (the
+// order of its first k + 1 keys, and which groups stay) all have more than that
+// between them is done, the others, a few in a thousand, are done again in f64.
+// Without a bias the order inside groups is the logits' own, which has no error.
 //
-// One wave per token, lane l holding the experts l, l + 64, ... .  The k passes over
-// the keys compare their f32 roundings (monotonic in the key) by a wave maximum in
-// DPP; only when several keys share the largest rounding are the f64 values looked at.
-#include <type_traits>
-
+// One wave per token.  A group has 2^log_lanes lanes, each with every 2^log_lanes-th of
+// its experts, so a group's best keys are found in its own lanes.  Keys are compared as
+// integers that order like them: a wave maximum is then six DPP instructions, and a pass
+// for one slot about thirty.
 #include "q4.h"
 
 namespace tq2 {
@@ -51,24 +54,55 @@ __device__ __forceinline__ float wave_sum(float v) {
     return a + b;
 }
 
+template <int CTRL>
+__device__ __forceinline__ int dppi(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+// v of the lane in the other half of each pair of 16-lane rows, or of the wave: the
+// swap leaves one operand with the lower half's values in both, the other the upper's.
+__device__ __forceinline__ int2 both16(int v) {
+    const auto r = __builtin_amdgcn_permlane16_swap((unsigned)v, (unsigned)v, false, false);
+    return int2{(int)r[0], (int)r[1]};
+}
+__device__ __forceinline__ int2 both32(int v) {
+    const auto r = __builtin_amdgcn_permlane32_swap((unsigned)v, (unsigned)v, false, false);
+    return int2{(int)r[0], (int)r[1]};
+}
+template <typename I>
+__device__ __forceinline__ I imax(I a, I b) {
+    return a > b ? a : b;
+}
+template <typename I>
+__device__ __forceinline__ I imin(I a, I b) {
+    return a < b ? a : b;
+}
+
+// Maximum over the wave, as a scalar.
+template <typename I>
+__device__ __forceinline__ I wave_imax(I v) {
+    v = imax(v, (I)dppi<0xB1>((int)v));
+    v = imax(v, (I)dppi<0x4E>((int)v));
+    v = imax(v, (I)dppi<0x124>((int)v));
+    v = imax(v, (I)dppi<0x128>((int)v));
+    int2 b = both16((int)v);
+    v = imax((I)b.x, (I)b.y);
+    b = both32((int)v);
+    return (I)__builtin_amdgcn_readfirstlane((int)imax((I)b.x, (I)b.y));
+}
+
+__device__ __forceinline__ double dpp_sum16(double v) {
+    auto add = [&](auto f) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        v += __builtin_bit_cast(double, (uint64_t)(uint32_t)f((int)(b >> 32)) << 32 | (uint32_t)f((int)b));
+    };
+    add(dppi<0xB1>), add(dppi<0x4E>), add(dppi<0x141>), add(dppi<0x140>);  // exchanges: every lane's sum has the same bits
+    return v;
+}
+
 __device__ __forceinline__ double wave_sum(double v) {
-    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
-    return v;
-}
-
-__device__ __forceinline__ double wave_max(double v) {
-    for (int o = 1; o < 64; o <<= 1) {
-        const double b = __shfl_xor(v, o);
-        v = b > v ? b : v;
-    }
-    return v;
-}
-
-__device__ __forceinline__ double uniform(double v, int lane) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, lane);
-    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    v = dpp_sum16(v);
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
 }
 
 __device__ __forceinline__ float uniform(float v, int lane) {
@@ -76,131 +110,267 @@ __device__ __forceinline__ float uniform(float v, int lane) {
 }
 
 constexpr float kNone = -__builtin_inff();
+constexpr int kGone = -0x7fffffff - 1;  // below every key
 
-// V: experts per lane.  KEYS: keys are sums of scores (f64), else the logits.
+// Integers that order as the floats do (-0 as 0, NaN above all).
+__device__ __forceinline__ int order_of(float v) {
+    const int b = __builtin_bit_cast(int, v + 0.0f);
+    return v != v ? 0x7fffffff : b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float value_of(int o) { return __builtin_bit_cast(float, o ^ ((o >> 31) & 0x7fffffff)); }
+__device__ __forceinline__ int64_t order_of(double v) {
+    const int64_t b = __builtin_bit_cast(int64_t, v + 0.0);
+    return v != v ? 0x7fffffffffffffff : b ^ ((b >> 63) & 0x7fffffffffffffff);
+}
+__device__ __forceinline__ double value_of(int64_t o) {
+    return __builtin_bit_cast(double, o ^ ((o >> 63) & 0x7fffffffffffffff));
+}
+constexpr int kNoneOrder = (int)0x807fffff;  // order_of(-inf)
+constexpr int64_t kNoneOrder64 = (int64_t)0x800fffffffffffff, kGone64 = -0x7fffffffffffffff - 1;
+
+// Maximum of 64-bit orders over the wave: the upper halves, then the lower ones of those.
+__device__ __forceinline__ int64_t wave_imax(int64_t v) {
+    const int hi = (int)(v >> 32), m = wave_imax(hi);
+    const uint32_t lo = wave_imax(hi == m ? (uint32_t)v : 0u);
+    return (int64_t)((uint64_t)(uint32_t)m << 32 | lo);
+}
+
+template <bool SIGMOID>
+__device__ __forceinline__ double score64(float l, float most, double total) {
+    if (l == kNone) return 0.0;
+    return SIGMOID ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)most) / total;
+}
+
+// exp of v in [-200, 200] to about two steps of f32: the product with log2(e) in two
+// parts around the hardware's exp2.
+__device__ __forceinline__ float exp_of(float v) {
+    v = __builtin_amdgcn_fmed3f(v, -200.0f, 200.0f);
+    const float t = v * 1.44269504f;
+    const float rest = __builtin_fmaf(v, 1.44269504f, -t) + v * 1.92596299e-8f;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return rest == 0.0f || e > 3e38f ? e : __builtin_fmaf(e, rest * 0.69314718f, e);
+}
+
+// (a, b) and (c, d), each the best two of a set, to the best two of both.
+template <typename I>
+__device__ __forceinline__ void merge2(I &a, I &b, I c, I d) {
+    b = imax(imin(a, c), imax(b, d));
+    a = imax(a, c);
+}
+
+// The best two of each group of 2^log_lanes lanes, in all its lanes.
+__device__ __forceinline__ void best_two(int &a, int &b, int log_lanes) {
+    if (log_lanes > 0) merge2(a, b, dppi<0xB1>(a), dppi<0xB1>(b));    // lane ^ 1
+    if (log_lanes > 1) merge2(a, b, dppi<0x4E>(a), dppi<0x4E>(b));    // lane ^ 2
+    if (log_lanes > 2) merge2(a, b, dppi<0x141>(a), dppi<0x141>(b));  // mirrored in eight lanes
+    if (log_lanes > 3) merge2(a, b, dppi<0x140>(a), dppi<0x140>(b));  // mirrored in sixteen
+    if (log_lanes > 4) {
+        const int2 p = both16(a), q = both16(b);
+        a = p.x, b = q.x;
+        merge2(a, b, p.y, q.y);
+    }
+    if (log_lanes > 5) {
+        const int2 p = both32(a), q = both32(b);
+        a = p.x, b = q.x;
+        merge2(a, b, p.y, q.y);
+    }
+}
+__device__ __forceinline__ void best_two(int64_t &a, int64_t &b, int log_lanes) {
+    for (int o = 0; o < log_lanes; ++o) merge2(a, b, (int64_t)__shfl_xor(a, 1 << o), (int64_t)__shfl_xor(b, 1 << o));
+}
+
+// Where a lane's experts lie: expert(c) = first + c * lanes for c < own.
+struct Place {
+    int lanes, group, first, own;
+};
+
+// One pass over the keys: the largest, with the lowest expert among equal ones, goes.
+// Returns the expert (-1: none is left) and its key.
+template <int V, typename I>
+__device__ __forceinline__ int take_best(I (&key)[V], const Place &at, int lane, I none, I gone, I &best) {
+    I top = key[0];
+    int c = 0;
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+        if (key[i] > top) top = key[i], c = i;
+    best = wave_imax(top);
+    if (best <= none) return -1;
+    const int mine = at.first + c * at.lanes;
+    uint64_t who = __ballot(top == best);
+    if (who & (who - 1)) {  // several lanes: the lowest expert
+        const int low = -wave_imax(top == best ? -mine : kGone);
+        who = __ballot(top == best && mine == low);
+    }
+    const int w = __builtin_ctzll(who);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (lane == w && c == i) key[i] = gone;
+    return __builtin_amdgcn_readlane(mine, w);
+}
+
+// Whether this lane's group is one of the `keep` with the largest keys (own: the group's key).
+template <typename I>
+__device__ __forceinline__ bool stays(const RouteArgs &p, I own, const Place &at, int log_lanes) {
+    int place = 0;
+    for (int q = 0; q < p.groups; ++q) {
+        I v;
+        if constexpr (sizeof(I) == 8) {
+            const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)own, q << log_lanes);
+            const uint32_t hi = __builtin_amdgcn_readlane((int)(own >> 32), q << log_lanes);
+            v = (I)((uint64_t)hi << 32 | lo);
+        } else {
+            v = __builtin_amdgcn_readlane(own, q << log_lanes);
+        }
+        if (v > own || (v == own && q < at.group)) ++place;
+    }
+    return at.group < p.groups && place < p.keep;
+}
+
+// Slots of one token in f64; lane j < k gets slot j's expert.
+template <int V, bool SIGMOID>
+__device__ int route_exact(const RouteArgs &p, const float (&l)[V], float most, const Place &at, int log_lanes, int lane) {
+    int64_t key[V];
+    double total = 1.0;
+    if constexpr (!SIGMOID) {
+        total = 0.0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) total += l[i] == kNone ? 0.0 : exp((double)l[i] - (double)most);
+        total = wave_sum(total);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        double v = score64<SIGMOID>(l[i], most, total);
+        if (p.bias && i < at.own) v += (double)p.bias[at.first + i * at.lanes];
+        key[i] = i < at.own && l[i] != kNone ? order_of(v) : kNoneOrder64;
+    }
+    if (p.groups > 1) {
+        int64_t a = kNoneOrder64, b = kNoneOrder64;
+#pragma unroll
+        for (int i = 0; i < V; ++i) merge2(a, b, key[i], kNoneOrder64);
+        best_two(a, b, log_lanes);
+        if (p.group_top > 1 && b > kNoneOrder64) a = order_of(value_of(a) + value_of(b));
+        if (!stays(p, a, at, log_lanes)) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = kNoneOrder64;
+        }
+    }
+    int mine = -1;
+    for (int j = 0; j < p.k; ++j) {
+        int64_t best;
+        const int e = take_best<V, int64_t>(key, at, lane, kNoneOrder64, kGone64, best);
+        if (e < 0) break;
+        if (lane == j) mine = e;
+    }
+    return mine;
+}
+
+// V: experts per lane.  KEYS: keys are sums of scores, else the logits.
 template <int DT, int V, bool KEYS, bool SIGMOID>
-__global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p) {
-    typedef typename std::conditional<KEYS, double, float>::type F;
-    __shared__ F keys[kWaves][V * 64];
+__global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p, int log_lanes) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
-    if (t >= p.T) return;  // no barrier below: each wave uses its own LDS
-    const int E = p.E;
+    if (t >= p.T) return;
+    const int n = p.n;
+    Place at;
+    at.lanes = 1 << log_lanes, at.group = lane >> log_lanes;
+    const int i0 = lane & (at.lanes - 1);
+    at.first = at.group * n + i0;
+    at.own = at.group < p.groups && i0 < n ? (n - i0 + at.lanes - 1) >> log_lanes : 0;
 
-    float l[V];
+    float l[V], key[V];
+    int order[V];  // decides among experts: the logit where there is no bias, else the key
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = lane + 64 * i;
-        l[i] = e < E ? load_as_float<DT>(p.logits, t * E + e) : kNone;
+        const int e = i < at.own ? at.first + i * at.lanes : 0;
+        l[i] = load_as_float<DT>(p.logits, t * p.E + e);
+        key[i] = KEYS && p.bias ? p.bias[e] : 0.0f;
     }
-    F score[V], key[V];
-    F most = kNone, total = 1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = i < at.own ? l[i] : kNone;
+    float most = kNone, total = 1.0f;
     if constexpr (!SIGMOID) {
-        float m = kNone;
+        float m = l[0];
 #pragma unroll
-        for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
-        most = wave_max(m);
-        total = 0;
+        for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+        most = uniform(wave_max(m), 0);
     }
+    float error = 0.0f;  // bound on a key's error
+    if constexpr (KEYS || !SIGMOID) {
+        float score[V];
+        if constexpr (!SIGMOID) {
+            total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if constexpr (SIGMOID) score[i] = (F)1 / ((F)1 + exp(-(F)l[i]));
-        else {
-            score[i] = l[i] == kNone ? (F)0 : exp((F)l[i] - most);
-            total += score[i];
+            for (int i = 0; i < V; ++i) total += score[i] = l[i] == kNone ? 0.0f : KEYS ? exp_of(l[i] - most) : expf(l[i] - most);
+            // one lane's sum for all: the lanes' orders of addition differ
+            total = uniform(wave_sum(total), 0);
         }
-    }
-    if constexpr (!SIGMOID) {
-        total = wave_sum(total);
+        if constexpr (KEYS) {
+            float mag = 0.0f;
+            const float inv = 1.0f / total;
 #pragma unroll
-        for (int i = 0; i < V; ++i) score[i] /= total;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane + 64 * i;
-        key[i] = KEYS ? score[i] : (F)l[i];
-        if (KEYS && p.bias && e < E) key[i] += (F)p.bias[e];
-        if (l[i] == kNone) key[i] = kNone;
-        if (key[i] != key[i]) key[i] = __builtin_inff();
-    }
-    if (p.groups > 1) {
-        const int n = E / p.groups;
-#pragma unroll
-        for (int i = 0; i < V; ++i) keys[wave][lane + 64 * i] = key[i];
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        // lane g: the best two keys of group g, starting at another place in each
-        // group so that the lanes read different banks
-        F a = kNone, b = kNone;
-        if (lane < p.groups) {
-            int at = lane % n;
-            for (int i = 0; i < n; ++i) {
-                const F v = keys[wave][lane * n + at];
-                if (v > a) b = a, a = v;
-                else if (v > b) b = v;
-                if (++at == n) at = 0;
+            for (int i = 0; i < V; ++i) {
+                const float sc = SIGMOID ? __builtin_amdgcn_rcpf(1.0f + exp_of(-l[i])) : score[i] * inv;
+                key[i] += sc;
+                if (l[i] != l[i]) key[i] = l[i];
+                const float m = sc + __builtin_fabsf(key[i]);
+                if (l[i] != kNone && m < __builtin_inff()) mag = fmaxf(mag, m);
             }
-            if (p.group_top > 1 && n > 1) a = b == kNone ? a : a + b;
-        }
-        // its place: the groups that beat it
-        int place = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            const F v = uniform(a, g);
-            if (v > a || (v == a && g < lane)) ++place;
-        }
-        const uint64_t kept = __ballot(lane < p.groups && place < p.keep);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 64 * i;
-            if (e < E && !((kept >> (e / n)) & 1)) key[i] = kNone;
+            // exp, sum, quotient and sum with the bias: below eight steps of 2^-24 each
+            error = 0x1p-21f * uniform(wave_max(mag), 0);
         }
     }
-    float hi[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) hi[i] = (float)key[i];
+    for (int i = 0; i < V; ++i) {
+        order[i] = order_of(l[i]);
+        if constexpr (KEYS) {
+            const int o = order[i] == kNoneOrder ? kNoneOrder : order_of(key[i]);
+            key[i] = __builtin_bit_cast(float, o);  // the key's order, for the groups
+            if (p.bias || o == kNoneOrder) order[i] = o;
+        }
+    }
+    bool close = false;  // some decision within the keys' error
+    if (p.groups > 1) {
+        int a = kNoneOrder, b = kNoneOrder;
+#pragma unroll
+        for (int i = 0; i < V; ++i) merge2(a, b, KEYS ? __builtin_bit_cast(int, key[i]) : order[i], kNoneOrder);
+        best_two(a, b, log_lanes);
+        if (p.group_top > 1 && b > kNoneOrder) a = order_of(value_of(a) + value_of(b));
+        const bool in = stays(p, a, at, log_lanes);
+        if (KEYS && p.keep < p.groups) {
+            const float low = value_of(-wave_imax(in ? -a : kGone)), high = value_of(wave_imax(!in ? a : kGone));
+            close = low - high <= 4.0f * error;
+        }
+        if (!in) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) order[i] = kNoneOrder;
+        }
+    }
 
     int mine = -1;
-    F w = 0, sum = 0;
-    for (int j = 0; j < p.k; ++j) {
-        float m = hi[0];
-#pragma unroll
-        for (int i = 1; i < V; ++i) m = fmaxf(m, hi[i]);
-        m = wave_max(m);
-        if (m == kNone) break;
-        // the experts whose key rounds to the maximum
-        uint64_t at[V];
-        int many = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            at[i] = __ballot(hi[i] == m);
-            many += __popcll(at[i]);
+    const bool fuzzy = KEYS && p.bias;          // the order is that of keys with an error
+    const int passes = fuzzy ? p.k + 1 : p.k;  // one more key, to see how near it comes
+    float before = 0.0f;
+    for (int j = 0; j < passes; ++j) {
+        int best;
+        const int e = take_best<V, int>(order, at, lane, kNoneOrder, kGone, best);
+        if (e < 0) break;
+        if (fuzzy) {
+            if (j && before - value_of(best) <= 2.0f * error) close = true;
+            before = value_of(best);
         }
-        if (KEYS && many > 1) {
-            F top = kNone;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (hi[i] == m && key[i] > top) top = key[i];
-            top = wave_max(top);
-#pragma unroll
-            for (int i = 0; i < V; ++i) at[i] = __ballot(hi[i] == m && key[i] == top);
-        }
-        int e = 0;
-        F s = 0;
-#pragma unroll
-        for (int i = V - 1; i >= 0; --i)
-            if (at[i]) {
-                const int at_lane = __builtin_ctzll(at[i]);
-                e = 64 * i + at_lane;
-                s = uniform(score[i], at_lane);
-            }
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (e == lane + 64 * i) hi[i] = kNone;
-        sum += s;
-        if (lane == j) mine = e, w = s;
+        if (lane == j && j < p.k) mine = e;
     }
-    if (p.renorm && sum != 0) w /= sum;
+    if constexpr (KEYS) {
+        if (close) mine = route_exact<V, SIGMOID>(p, l, most, at, log_lanes, lane);  // wave-uniform
+    }
+    // the chosen scores in f64, one per lane
+    const float chosen = load_as_float<DT>(p.logits, t * p.E + (mine < 0 ? 0 : mine));
+    double w = mine < 0 ? 0.0 : score64<SIGMOID>(chosen, most, (double)total);
+    if (p.renorm) {
+        const double sum = p.k <= 16 ? dpp_sum16(w) : wave_sum(w);
+        if (sum != 0.0) w /= sum;
+    }
     if (lane < p.k) {
         p.idx[t * p.k + lane] = mine;
         p.weights[t * p.k + lane] = (float)w;
@@ -276,22 +446,27 @@ __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(const void 
 }
 
 template <int DT, int V>
-hipError_t route_v(const RouteArgs &a, hipStream_t s) {
+hipError_t route_v(const RouteArgs &a, int log_lanes, hipStream_t s) {
     const bool keys = a.bias || (a.groups > 1 && a.group_top > 1);
     const dim3 grid((unsigned)((a.T + kWaves - 1) / kWaves)), block(kWaves * 64);
-    if (keys && a.sigmoid) route_kernel<DT, V, true, true><<<grid, block, 0, s>>>(a);
-    else if (keys) route_kernel<DT, V, true, false><<<grid, block, 0, s>>>(a);
-    else if (a.sigmoid) route_kernel<DT, V, false, true><<<grid, block, 0, s>>>(a);
-    else route_kernel<DT, V, false, false><<<grid, block, 0, s>>>(a);
+    if (keys && a.sigmoid) route_kernel<DT, V, true, true><<<grid, block, 0, s>>>(a, log_lanes);
+    else if (keys) route_kernel<DT, V, true, false><<<grid, block, 0, s>>>(a, log_lanes);
+    else if (a.sigmoid) route_kernel<DT, V, false, true><<<grid, block, 0, s>>>(a, log_lanes);
+    else route_kernel<DT, V, false, false><<<grid, block, 0, s>>>(a, log_lanes);
     return hipGetLastError();
 }
 
 template <int DT>
-hipError_t route(const RouteArgs &a, hipStream_t s) {
-    if (a.E <= 64) return route_v<DT, 1>(a, s);
-    if (a.E <= 128) return route_v<DT, 2>(a, s);
-    if (a.E <= 256) return route_v<DT, 4>(a, s);
-    return route_v<DT, 16>(a, s);
+hipError_t route(RouteArgs a, hipStream_t s) {
+    a.n = a.E / a.groups;
+    int log_lanes = 6;  // the most lanes that 64 have for each group
+    while ((a.groups << log_lanes) > 64) --log_lanes;
+    const int own = (a.n + (1 << log_lanes) - 1) >> log_lanes;  // at most 31 for 1024 experts
+    if (own <= 1) return route_v<DT, 1>(a, log_lanes, s);
+    if (own <= 2) return route_v<DT, 2>(a, log_lanes, s);
+    if (own <= 4) return route_v<DT, 4>(a, log_lanes, s);
+    if (own <= 8) return route_v<DT, 8>(a, log_lanes, s);
+    return route_v<DT, 32>(a, log_lanes, s);
 }
 
 template <int DT, int V>

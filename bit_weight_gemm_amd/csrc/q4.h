@@ -182,6 +182,7 @@ struct RouteArgs {
     float *weights;
     int64_t T;
     int E, k, groups, keep, group_top, dtype;
+    int n;                   // experts per group (set by the launcher)
     bool sigmoid, renorm;
 };
 hipError_t launch_moe_route(const RouteArgs &a, hipStream_t s);
