@@ -31,19 +31,6 @@ namespace {
 
 constexpr int kWaves = 4;  // tokens per workgroup
 
-__device__ __forceinline__ float wave_max(float v) {
-    v = fmaxf(v, dpp<0xB1>(v));
-    v = fmaxf(v, dpp<0x4E>(v));
-    v = fmaxf(v, dpp<0x124>(v));
-    v = fmaxf(v, dpp<0x128>(v));
-    float a = v, b = v;
-    swap16(a, b);
-    v = fmaxf(a, b);
-    a = v, b = v;
-    swap32(a, b);
-    return fmaxf(a, b);
-}
-
 __device__ __forceinline__ float wave_sum(float v) {
     v = row16_sum(v);
     float a = v, b = v;
@@ -56,7 +43,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 template <int CTRL>
 __device__ __forceinline__ int dppi(int v) {
-    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+    return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, false);
 }
 // v of the lane in the other half of each pair of 16-lane rows, or of the wave: the
 // swap leaves one operand with the lower half's values in both, the other the upper's.
@@ -77,17 +64,16 @@ __device__ __forceinline__ I imin(I a, I b) {
     return a < b ? a : b;
 }
 
-// Maximum over the wave, as a scalar.
+// Maximum over the wave, as a scalar: over each row of 16 lanes in DPP, then of the four rows.
 template <typename I>
 __device__ __forceinline__ I wave_imax(I v) {
     v = imax(v, (I)dppi<0xB1>((int)v));
     v = imax(v, (I)dppi<0x4E>((int)v));
-    v = imax(v, (I)dppi<0x124>((int)v));
-    v = imax(v, (I)dppi<0x128>((int)v));
-    int2 b = both16((int)v);
-    v = imax((I)b.x, (I)b.y);
-    b = both32((int)v);
-    return (I)__builtin_amdgcn_readfirstlane((int)imax((I)b.x, (I)b.y));
+    v = imax(v, (I)dppi<0x141>((int)v));
+    v = imax(v, (I)dppi<0x140>((int)v));
+    const I a = (I)__builtin_amdgcn_readlane((int)v, 0), b = (I)__builtin_amdgcn_readlane((int)v, 16);
+    const I c = (I)__builtin_amdgcn_readlane((int)v, 32), d = (I)__builtin_amdgcn_readlane((int)v, 48);
+    return imax(imax(a, b), imax(c, d));
 }
 
 __device__ __forceinline__ double dpp_sum16(double v) {
@@ -128,6 +114,9 @@ __device__ __forceinline__ double value_of(int64_t o) {
 constexpr int kNoneOrder = (int)0x807fffff;  // order_of(-inf)
 constexpr int64_t kNoneOrder64 = (int64_t)0x800fffffffffffff, kGone64 = -0x7fffffffffffffff - 1;
 
+// The largest float of the wave (NaN is passed over), as a scalar.
+__device__ __forceinline__ float wave_max(float v) { return value_of(wave_imax(v != v ? kNoneOrder : order_of(v))); }
+
 // Maximum of 64-bit orders over the wave: the upper halves, then the lower ones of those.
 __device__ __forceinline__ int64_t wave_imax(int64_t v) {
     const int hi = (int)(v >> 32), m = wave_imax(hi);
@@ -141,14 +130,14 @@ __device__ __forceinline__ double score64(float l, float most, double total) {
     return SIGMOID ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)most) / total;
 }
 
-// exp of v in [-200, 200] to about two steps of f32: the product with log2(e) in two
-// parts around the hardware's exp2.
+// exp of v to about two steps of f32 (v limited to +-88, where it is next to 0 or 2^127):
+// the product with log2(e) in two parts around the hardware's exp2.
 __device__ __forceinline__ float exp_of(float v) {
-    v = __builtin_amdgcn_fmed3f(v, -200.0f, 200.0f);
+    v = __builtin_amdgcn_fmed3f(v, -88.0f, 88.0f);
     const float t = v * 1.44269504f;
-    const float rest = __builtin_fmaf(v, 1.44269504f, -t) + v * 1.92596299e-8f;
+    const float rest = __builtin_fmaf(v, 1.92596299e-8f, __builtin_fmaf(v, 1.44269504f, -t));
     const float e = __builtin_amdgcn_exp2f(t);
-    return rest == 0.0f || e > 3e38f ? e : __builtin_fmaf(e, rest * 0.69314718f, e);
+    return __builtin_fmaf(e, rest * 0.69314718f, e);
 }
 
 // (a, b) and (c, d), each the best two of a set, to the best two of both.
@@ -184,15 +173,37 @@ struct Place {
     int lanes, group, first, own;
 };
 
-// One pass over the keys: the largest, with the lowest expert among equal ones, goes.
-// Returns the expert (-1: none is left) and its key.
+// A lane's keys in falling order, equal ones by expert (V <= 4: exchanges of neighbours; more: none,
+// take_best looks for the largest).  from[i]: which of the lane's experts key[i] is.
 template <int V, typename I>
-__device__ __forceinline__ int take_best(I (&key)[V], const Place &at, int lane, I none, I gone, I &best) {
-    I top = key[0];
-    int c = 0;
+__device__ __forceinline__ void sort_keys(I (&key)[V], int (&from)[V]) {
 #pragma unroll
-    for (int i = 1; i < V; ++i)
-        if (key[i] > top) top = key[i], c = i;
+    for (int i = 0; i < V; ++i) from[i] = i;
+    if constexpr (V > 1 && V <= 4) {
+#pragma unroll
+        for (int pass = 0; pass + 1 < V; ++pass)
+#pragma unroll
+            for (int i = 0; i + 1 < V - pass; ++i)
+                if (key[i + 1] > key[i]) {
+                    const I k = key[i];
+                    key[i] = key[i + 1], key[i + 1] = k;
+                    const int f = from[i];
+                    from[i] = from[i + 1], from[i + 1] = f;
+                }
+    }
+}
+
+// One pass over the keys (sort_keys'): the largest, with the lowest expert among equal
+// ones, goes.  Returns the expert (-1: none is left) and its key.
+template <int V, typename I>
+__device__ __forceinline__ int take_best(I (&key)[V], int (&from)[V], const Place &at, int lane, I none, I gone, I &best) {
+    I top = key[0];
+    int c = from[0], pos = 0;
+    if constexpr (V > 4) {
+#pragma unroll
+        for (int i = 1; i < V; ++i)
+            if (key[i] > top) top = key[i], c = i, pos = i;
+    }
     best = wave_imax(top);
     if (best <= none) return -1;
     const int mine = at.first + c * at.lanes;
@@ -202,9 +213,15 @@ __device__ __forceinline__ int take_best(I (&key)[V], const Place &at, int lane,
         who = __ballot(top == best && mine == low);
     }
     const int w = __builtin_ctzll(who);
+    if constexpr (V > 4) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (lane == w && c == i) key[i] = gone;
+        for (int i = 0; i < V; ++i)
+            if (lane == w && pos == i) key[i] = gone;
+    } else if (lane == w) {
+#pragma unroll
+        for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1], from[i] = from[i + 1];
+        key[V - 1] = gone;
+    }
     return __builtin_amdgcn_readlane(mine, w);
 }
 
@@ -254,10 +271,11 @@ __device__ int route_exact(const RouteArgs &p, const float (&l)[V], float most, 
             for (int i = 0; i < V; ++i) key[i] = kNoneOrder64;
         }
     }
-    int mine = -1;
+    int mine = -1, from[V];
+    sort_keys<V>(key, from);
     for (int j = 0; j < p.k; ++j) {
         int64_t best;
-        const int e = take_best<V, int64_t>(key, at, lane, kNoneOrder64, kGone64, best);
+        const int e = take_best<V, int64_t>(key, from, at, lane, kNoneOrder64, kGone64, best);
         if (e < 0) break;
         if (lane == j) mine = e;
     }
@@ -293,7 +311,7 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p, int log
         float m = l[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
-        most = uniform(wave_max(m), 0);
+        most = wave_max(m);
     }
     float error = 0.0f;  // bound on a key's error
     if constexpr (KEYS || !SIGMOID) {
@@ -317,7 +335,7 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p, int log
                 if (l[i] != kNone && m < __builtin_inff()) mag = fmaxf(mag, m);
             }
             // exp, sum, quotient and sum with the bias: below eight steps of 2^-24 each
-            error = 0x1p-21f * uniform(wave_max(mag), 0);
+            error = 0x1p-21f * wave_max(mag);
         }
     }
 #pragma unroll
@@ -347,13 +365,14 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p, int log
         }
     }
 
-    int mine = -1;
+    int mine = -1, from[V];
+    sort_keys<V>(order, from);
     const bool fuzzy = KEYS && p.bias;          // the order is that of keys with an error
     const int passes = fuzzy ? p.k + 1 : p.k;  // one more key, to see how near it comes
     float before = 0.0f;
     for (int j = 0; j < passes; ++j) {
         int best;
-        const int e = take_best<V, int>(order, at, lane, kNoneOrder, kGone, best);
+        const int e = take_best<V, int>(order, from, at, lane, kNoneOrder, kGone, best);
         if (e < 0) break;
         if (fuzzy) {
             if (j && before - value_of(best) <= 2.0f * error) close = true;
