@@ -16,7 +16,7 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtq2.so")
-SOURCES = ["q4_tiled.hip", "q4_gemm.hip", "q4_moe.hip", "moe_route.hip", "libtq2.cpp", "libq4.cpp", "repack.cpp", "tq2_gemv.hip",
+SOURCES = ["q4_tiled.hip", "q4_gemm.hip", "q4_group.hip", "q4_moe.hip", "moe_route.hip", "libtq2.cpp", "libq4.cpp", "repack.cpp", "tq2_gemv.hip",
            "mfma_gemm.hip", "blr.hip", "skinny_gemm.hip"]
 ARCH = "gfx950"
 

@@ -112,18 +112,18 @@ __device__ __forceinline__ f4 mfma16(w4 a, w4 b, f4 c) {
 
 __device__ __forceinline__ float half_bits(uint32_t h) { return (float)__builtin_bit_cast(_Float16, (uint16_t)h); }
 
-// A row's scales (f16, the first in the low half of .x) and zero points (a byte each; 8
-// where zeros is null) in a unit: 128/G of them.
+// Row r's scales (f16, the first in the low half of .x) and zero points (a byte each; 8
+// where zeros is null) in a unit, from the unit's places (uniform in a wave): 128/G of them.
 template <int G>
-__device__ __forceinline__ void q4_load_groups(const uint16_t *scales, const uint8_t *zeros, uint2 &s, uint32_t &z) {
-    if constexpr (G == 128) s.x = *scales;
-    if constexpr (G == 64) s.x = *reinterpret_cast<const uint32_t *>(scales);
-    if constexpr (G == 32) s = *reinterpret_cast<const uint2 *>(scales);
+__device__ __forceinline__ void q4_load_groups(const uint16_t *scales, const uint8_t *zeros, int r, uint2 &s, uint32_t &z) {
+    if constexpr (G == 128) s.x = scales[r];
+    if constexpr (G == 64) s.x = reinterpret_cast<const uint32_t *>(scales)[r];
+    if constexpr (G == 32) s = reinterpret_cast<const uint2 *>(scales)[r];
     z = 0x08080808u;
     if (zeros) {
-        if constexpr (G == 128) z = *zeros;
-        if constexpr (G == 64) z = *reinterpret_cast<const uint16_t *>(zeros);
-        if constexpr (G == 32) z = *reinterpret_cast<const uint32_t *>(zeros);
+        if constexpr (G == 128) z = zeros[r];
+        if constexpr (G == 64) z = reinterpret_cast<const uint16_t *>(zeros)[r];
+        if constexpr (G == 32) z = reinterpret_cast<const uint32_t *>(zeros)[r];
     }
 }
 
@@ -165,6 +165,7 @@ hipError_t launch_q4_gemm(const Q4View &v, const void *x, void *y, int64_t M, in
 struct MoePlan {
     int64_t slots;                   // T * k
     bool direct;                     // a few slots: no plan
+    bool grouped;                    // a few rows per expert: no plan either
     bool tiled;                      // many rows per expert: the tiled products
     int64_t tile_rows, max_tiles;    // rows per tile of the grouped products, and the most tiles there can be
     int64_t ldx, ldh;                // tiled: rows of x and of h in whole units of 128

@@ -5,6 +5,7 @@
 // sorted by expert, and the list of row tiles), the gate and up products with
 // silu(g) u in their epilogue, the down product times the slot's weight, and the
 // sum of each token's slots in slot order.
+#include "q4_group.h"
 #include "q4_row.h"
 #include "q4_tiled.h"
 
@@ -118,6 +119,34 @@ hipError_t direct(const MoePlan &p, const void *x, const int32_t *idx, const flo
     return row_down_sum<kXF32x3, kF32>(d, T, s);
 }
 
+template <int DT>
+void launch_sum(const float *part, const int32_t *idx, void *y, int64_t T, int64_t k, int E, int d, hipStream_t s) {
+    moe_sum_kernel<DT><<<dim3((unsigned)((T * d / 4 + 255) / 256)), dim3(256), 0, s>>>(part, idx, y, T, (int)k, E, d);
+}
+
+hipError_t sum(const float *part, const int32_t *idx, void *y, int64_t T, int64_t k, int E, int d, int dtype, hipStream_t s) {
+    if (dtype == kF16) launch_sum<kF16>(part, idx, y, T, k, E, d, s);
+    else if (dtype == kBF16) launch_sum<kBF16>(part, idx, y, T, k, E, d, s);
+    else launch_sum<kF32>(part, idx, y, T, k, E, d, s);
+    return hipGetLastError();
+}
+
+// A few rows per expert: every expert's workgroups find their slots, no plan.  As in
+// tiled(), h for 16-bit types is rounded to f16 under a power of two per row.
+hipError_t grouped(const MoePlan &p, const void *x, const int32_t *idx, const float *weights, const Q4View &gate,
+                   const Q4View &up, const Q4View &down, void *y, int64_t T, int64_t k, int dtype, char *b, hipStream_t s) {
+    Q4GroupArgs g{};
+    g.w = gate, g.w2 = up, g.x = x, g.y = reinterpret_cast<float *>(b + p.off_h), g.idx = idx, g.weights = weights;
+    g.slots = (int)p.slots, g.topk = (int)k;
+    hipError_t e = launch_q4_group_gate_up(g, dtype, s);
+    if (e != hipSuccess) return e;
+    Q4GroupArgs d = g;
+    d.w = down, d.x = g.y, d.y = reinterpret_cast<float *>(b + p.off_part);
+    e = launch_q4_group_down(d, q4_planes(dtype), s);
+    if (e != hipSuccess) return e;
+    return sum(d.y, idx, y, T, k, gate.E, down.N, dtype, s);
+}
+
 // Few rows per expert: tiles of 16 or 32 rows, h in f32.
 hipError_t skinny(const MoePlan &p, const void *x, const float *weights, const Q4View &gate, const Q4View &up,
                   const Q4View &down, int64_t k, int dtype, char *b, hipStream_t s) {
@@ -186,7 +215,9 @@ MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtyp
     p.ldx = (d + 127) / 128 * 128, p.ldh = (f + 127) / 128 * 128;
     p.direct = p.slots <= kDirectSlots && q4_row_lds(p.ldx / 128, f32 ? 3 : 1) <= kDirectLds &&
                q4_row_lds(k * (p.ldh / 128), f32 ? 3 : 2) <= kDirectLds;
-    p.tiled = !p.direct && p.slots > 32 * E;
+    p.grouped = !p.direct && p.slots <= kGroupMaxSlots && p.slots <= 24 * E && d <= kGroupMaxK && f <= kGroupMaxK &&
+                q4_group_lds(d > f ? d : f, q4_planes(dtype), 16) <= kGroupLds;
+    p.tiled = !p.direct && !p.grouped && p.slots > 32 * E;
     p.tile_rows = p.tiled ? (p.slots > 96 * E ? 128 : 64) : p.slots <= 16 * E ? 16 : 32;
     p.max_tiles = p.slots / p.tile_rows + (E < p.slots ? E : p.slots);
     size_t at = 256;  // the first 256 bytes hold the number of tiles
@@ -215,6 +246,7 @@ hipError_t launch_q4_moe(const MoePlan &p, const void *x, const int32_t *idx, co
                          hipStream_t s) {
     char *b = static_cast<char *>(ws);
     if (p.direct) return direct(p, x, idx, weights, gate, up, down, y, T, k, dtype, b, s);
+    if (p.grouped) return grouped(p, x, idx, weights, gate, up, down, y, T, k, dtype, b, s);
     int32_t *ntiles = reinterpret_cast<int32_t *>(b), *order = reinterpret_cast<int32_t *>(b + p.off_order);
     int4 *tiles = reinterpret_cast<int4 *>(b + p.off_tiles);
     const float *part = reinterpret_cast<const float *>(b + p.off_part);
@@ -223,11 +255,7 @@ hipError_t launch_q4_moe(const MoePlan &p, const void *x, const int32_t *idx, co
     if (e != hipSuccess) return e;
     e = p.tiled ? tiled(p, x, weights, gate, up, down, T, k, dtype, b, s) : skinny(p, x, weights, gate, up, down, k, dtype, b, s);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)((T * down.N / 4 + 255) / 256));
-    if (dtype == kF16) moe_sum_kernel<kF16><<<grid, dim3(256), 0, s>>>(part, idx, y, T, (int)k, gate.E, down.N);
-    else if (dtype == kBF16) moe_sum_kernel<kBF16><<<grid, dim3(256), 0, s>>>(part, idx, y, T, (int)k, gate.E, down.N);
-    else moe_sum_kernel<kF32><<<grid, dim3(256), 0, s>>>(part, idx, y, T, (int)k, gate.E, down.N);
-    return hipGetLastError();
+    return sum(part, idx, y, T, k, gate.E, down.N, dtype, s);
 }
 
 }  // namespace tq2

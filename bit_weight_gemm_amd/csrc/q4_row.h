@@ -79,9 +79,9 @@ __global__ __launch_bounds__(WAVES * 64) void q4_row_kernel(Q4RowArgs p) {
             int nb = blockIdx.x * NC + (MODE == kRowGateUp ? cb >> 1 : cb);
             nb = nb < w.nb ? nb : w.nb - 1;  // past the last: not stored
             const int64_t unit = ((int64_t)e * w.nb + nb) * ku + u;
-            breg[st][cb] = w.codes[unit * 64 + lane];
-            q4_load_groups<G>(w.scales + (unit * 16 + r) * GPU_, zeros ? w.zeros + (unit * 16 + r) * GPU_ : nullptr,
-                              sreg[st][cb], zreg[st][cb]);
+            breg[st][cb] = (w.codes + unit * 64)[lane];
+            q4_load_groups<G>(w.scales + unit * (16 * GPU_), zeros ? w.zeros + unit * (16 * GPU_) : nullptr, r, sreg[st][cb],
+                              zreg[st][cb]);
         }
     };
     const int n = (items - wave + WAVES - 1) / WAVES;  // this wave's items: wave, wave + WAVES, ...

@@ -133,9 +133,9 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
         int nb = blockIdx.x * cols + wn * NC + (MODE == kGateUp ? cb >> 1 : cb);
         nb = nb < w.nb ? nb : w.nb - 1;
         const int64_t unit = ((int64_t)e * w.nb + nb) * ku;
-        cp[cb] = w.codes + unit * 64 + lane;
-        sp[cb] = w.scales + (unit * 16 + r) * GPU_;
-        zp[cb] = zeros ? w.zeros + (unit * 16 + r) * GPU_ : nullptr;
+        cp[cb] = w.codes + unit * 64;  // the wave's; the lane's part is added at each load
+        sp[cb] = w.scales + unit * (16 * GPU_);
+        zp[cb] = w.zeros + unit * (16 * GPU_);
     }
 
     w4 areg[D][RB][F32 ? 8 : 4];
@@ -145,9 +145,9 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
     auto load = [&](int st, int u) {
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
-            breg[st][cb] = cp[cb][(int64_t)u * 64];
+            breg[st][cb] = (cp[cb] + (int64_t)u * 64)[lane];
             const int64_t at = (int64_t)u * (16 * GPU_);
-            q4_load_groups<G>(sp[cb] + at, zeros ? zp[cb] + at : nullptr, sreg[st][cb], zreg[st][cb]);
+            q4_load_groups<G>(sp[cb] + at, zeros ? zp[cb] + at : nullptr, r, sreg[st][cb], zreg[st][cb]);
         }
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)

@@ -55,6 +55,21 @@ __device__ __forceinline__ h8 q4_word_f16(uint32_t w, uint32_t c0, uint32_t c1, 
     return h8{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
 }
 
+// The pairs that q4_word_f16 adds: -(1024 + zero) and -(64 + zero), exact in f16.
+__device__ __forceinline__ void q4_zero_pairs(uint32_t zero, uint32_t &c0, uint32_t &c1) {
+    c0 = (0xE400u | zero) * 0x10001u;
+    const _Float16 f = (_Float16)(-64.0f - (float)zero);
+    c1 = (uint32_t)__builtin_bit_cast(uint16_t, f) * 0x10001u;
+}
+
+// The exponent by which a row with the largest finite value `most` is shifted to bring
+// that into [2^14, 2^15) (0 for a row of zeros).
+__device__ __forceinline__ int q4_row_shift(float most) {
+    int e = 15;
+    if (most > 0.0f) (void)__builtin_frexpf(most, &e);  // most in [2^(e-1), 2^e)
+    return 15 - e > 126 ? 126 : 15 - e;
+}
+
 // The power of two by which a row's silu(g) u is divided before it is rounded to f16,
 // so that it stays below 2^15 whatever the weights: |g| <= |x| |w| and |w| <= sqrt(K)
 // most |scale|, likewise u.  The bound lies some 2^14 above typical values, below which
@@ -134,9 +149,9 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
         nb[cb] = MODE == kTGateUp ? tn * 8 + wave : tn * 16 + wave * 2 + cb;
         const int at = nb[cb] < w.nb ? nb[cb] : w.nb - 1;  // past the last: its results are not stored
         const int64_t unit = ((int64_t)e * w.nb + at) * ku;
-        cp[cb] = w.codes + unit * 64 + lane;
-        sp[cb] = w.scales + (unit * 16 + r) * GPU_;
-        zp[cb] = zeros ? w.zeros + (unit * 16 + r) * GPU_ : nullptr;
+        cp[cb] = w.codes + unit * 64;  // the wave's; the lane's part is added at each load
+        sp[cb] = w.scales + unit * (16 * GPU_);
+        zp[cb] = w.zeros + unit * (16 * GPU_);
     }
     w4 areg[P][PPT];
     auto load_a = [&](int u) {
@@ -157,9 +172,9 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     auto load_b = [&](int st, int u) {
 #pragma unroll
         for (int cb = 0; cb < NCB; ++cb) {
-            breg[st][cb] = cp[cb][(int64_t)u * 64];
+            breg[st][cb] = (cp[cb] + (int64_t)u * 64)[lane];
             const int64_t at = (int64_t)u * (16 * GPU_);
-            q4_load_groups<G>(sp[cb] + at, zeros ? zp[cb] + at : nullptr, sreg[st][cb], zreg[st][cb]);
+            q4_load_groups<G>(sp[cb] + at, zeros ? zp[cb] + at : nullptr, r, sreg[st][cb], zreg[st][cb]);
         }
     };
 
@@ -177,9 +192,8 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
             for (int g = 0; g < GPU_; ++g) {
                 s[cb][g] = half_bits((g & 2 ? sreg[st][cb].y : sreg[st][cb].x) >> (16 * (g & 1)));
                 const uint32_t z = (zreg[st][cb] >> (8 * g)) & 255u;
-                const uint32_t c0 = (0xE400u | z) * 0x10001u;
-                const _Float16 f = (_Float16)(-64.0f - (float)z);
-                const uint32_t c1 = (uint32_t)__builtin_bit_cast(uint16_t, f) * 0x10001u;
+                uint32_t c0, c1;
+                q4_zero_pairs(z, c0, c1);
 #pragma unroll
                 for (int j = g * G / 32; j < (g + 1) * G / 32; ++j) b[cb][j] = q4_word_f16(breg[st][cb][j], c0, c1, magic);
             }

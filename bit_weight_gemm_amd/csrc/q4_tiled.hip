@@ -64,12 +64,7 @@ __global__ __launch_bounds__(256) void q4_prep_kernel(Q4Prep p) {
             look(v);
         }
         for (int o = 1; o < 64; o <<= 1) most = fmaxf(most, __shfl_xor(most, o));
-        if (most > 0.0f) {
-            int e;
-            (void)__builtin_frexpf(most, &e);  // most in [2^(e-1), 2^e)
-            shift = 15 - e;
-            shift = shift > 126 ? 126 : shift;
-        }
+        shift = q4_row_shift(most);
     }
     float norm = 0.0f;
     const int padded = (int)(p.lda / V);
