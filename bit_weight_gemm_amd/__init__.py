@@ -14,7 +14,9 @@ blr_saved_size, blr_workspace_size,
 blr_backward_workspace_size, tq2_workspace_allocs, tq2_select_path,
 tq2_set_path, tq2_set_m_small, tq2_strerror, tq2_version; and in include/libtq2_moe.h:
 q4_upload (packs into memory of its own), q4_gemm, q4_dequant, moe_route,
-moe_route_backward and q4_moe.
+moe_route_backward and q4_moe.  The last three and q4_gemm go through a compiled
+module (csrc/binding.cpp): beside their kernels' few microseconds, checks and
+conversions in Python would be the larger part.
 
 Every tensor's shape is checked here against the sizes the call derives from x,
 h and l before anything reaches the library: the C ABI takes raw device
@@ -58,7 +60,7 @@ def _single_hip_runtime():
 
 def lib():
     """Load libtq2.so (after torch, so both share torch's HIP runtime)."""
-    global _lib, _dtypes, _get_device, _get_raw_stream, _f32, _i32
+    global _lib, _compiled
     if _lib is not None:
         return _lib
     import torch  # load torch's HIP runtime first
@@ -113,10 +115,11 @@ def lib():
         f = getattr(L, name)
         f.argtypes = args
         f.restype = res
-    _dtypes = {torch.float32: Q4_F32, torch.float16: Q4_F16, torch.bfloat16: Q4_BF16}
-    _f32, _i32 = torch.float32, torch.int32
-    _get_device, _get_raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    _lib = L
+    from . import _binding as calls
+
+    calls.bind(*(ctypes.cast(f, p).value for f in (L.q4_gemm_workspace_size, L.q4_gemm, L.moe_route, L.moe_route_backward,
+                                                   L.q4_moe_workspace_size, L.q4_moe)))
+    _lib, _compiled = L, calls
     return L
 
 
@@ -455,59 +458,22 @@ def blr_backward_paths_ws(bits_u, bits_v, h, l, g, x, dy, dh, dl, dg, dx=None, g
 Q4_F32, Q4_F16, Q4_BF16 = 0, 1, 2
 MOE_SOFTMAX, MOE_SIGMOID = 0, 1
 _SCORES = {"softmax": MOE_SOFTMAX, "sigmoid": MOE_SIGMOID}
-# filled in by lib(): types, and torch's current device and stream without the objects around them
-_dtypes = _get_device = _get_raw_stream = _f32 = _i32 = None
+_compiled = None  # the calls' tensor checks and marshalling (csrc/binding.cpp); set by lib()
 
 
-def _dtype_code(t, name):
-    """Q4_* code of a tensor's type."""
-    code = _dtypes.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    return code
+def _calls():
+    """The compiled calls, bound to the library's entry points."""
+    lib()
+    return _compiled
 
 
-def _gpu_of(t, name) -> int:
-    """Index of the tensor's GPU."""
-    device = t.get_device()
-    if device < 0:
-        raise TypeError(f"{name} must be a tensor on the GPU")
-    return device
-
-
-def _arg(t, dtype, shape, name, device):
-    """Address of a contiguous tensor of this type and shape on GPU `device`.  One test on the way that
-    every call takes: a call's host time is a few microseconds, and so is a small kernel's."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
-        return t.data_ptr()
-    if t.get_device() < 0:
-        raise TypeError(f"{name} must be a tensor on the GPU")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{device}")
-
-
-def _raw_stream(stream, device):
-    """The stream's handle; None: the current stream of `device`, which has to be the current device."""
-    if device != _get_device():
-        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{_get_device()}")
-    if stream is None:
-        return _get_raw_stream(device)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _scratch(need, device, stream):
-    """A temporary workspace of the current stream, kept from reuse until `stream` is done with it."""
+def _on(stream):
+    """The stream as a torch stream (a raw handle is wrapped), or None."""
+    if stream is None or hasattr(stream, "cuda_stream"):
+        return stream
     import torch
 
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    if stream is not None and hasattr(stream, "cuda_stream"):
-        ws.record_stream(stream)
-    return ws
+    return torch.cuda.ExternalStream(int(stream))
 
 
 class _Q4Struct(ctypes.Structure):
@@ -520,6 +486,7 @@ class Q4Weight:
 
     def __init__(self, data, e, n, k, g, zeros: bool):
         self.data, self.E, self.N, self.K, self.G, self.zeros = data, e, n, k, g, zeros
+        self.like = (e, n, k, g, zeros)
         self.device = data.get_device()
         self._struct = _Q4Struct(data.data_ptr(), 1 if e is None else e, n, k, g, int(zeros), 0)
         self.handle = ctypes.addressof(self._struct)
@@ -544,14 +511,14 @@ def q4_upload(codes, scales, zeros=None, stream=None) -> Q4Weight:
     need = lib().q4_packed_size(e or 1, n, k, g, int(zeros is not None))
     if need == 0:
         raise ValueError(f"no packed form for E={e}, N={n}, K={k}, G={g}: G is 32, 64 or 128 and divides K")
-    device = _gpu_of(codes, "codes")
-    lead = codes.shape[:-1]
-    pc = _arg(codes, torch.uint8, codes.shape, "codes", device)
-    ps = _arg(scales, torch.float16, (*lead, k // g), "scales", device)
-    pz = None if zeros is None else _arg(zeros, torch.uint8, (*lead, k // g), "zeros", device)
-    raw = _raw_stream(stream, device)
+    c, lead, stream = _calls(), codes.shape[:-1], _on(stream)
+    pc = c.address(codes, "u8", codes.shape, "codes", None)
+    device = codes.get_device()
+    ps = c.address(scales, "f16", (*lead, k // g), "scales", device)
+    pz = None if zeros is None else c.address(zeros, "u8", (*lead, k // g), "zeros", device)
+    raw = c.stream(stream, device)
     w = Q4Weight(torch.empty(need, dtype=torch.uint8, device=codes.device), e, n, k, g, zeros is not None)
-    if stream is not None and hasattr(stream, "cuda_stream"):
+    if stream is not None:
         for t in (w.data, codes, scales) + (() if zeros is None else (zeros,)):
             t.record_stream(stream)
     _check(lib().q4_pack(w.handle, pc, ps, pz, raw), "q4_pack")
@@ -562,34 +529,25 @@ def q4_dequant(w: Q4Weight, out=None, stream=None):
     """(code - zero) * scale as float32, exact: [N, K] or [E, N, K]."""
     import torch
 
+    c, stream = _calls(), _on(stream)
     shape = (w.N, w.K) if w.E is None else (w.E, w.N, w.K)
-    raw = _raw_stream(stream, w.device)
+    raw = c.stream(stream, w.device)
     if out is None:
         out = torch.empty(shape, dtype=torch.float32, device=w.data.device)
-    _check(lib().q4_dequant(w.handle, _arg(out, torch.float32, shape, "out", w.device), raw), "q4_dequant")
+        if stream is not None:
+            out.record_stream(stream)
+    _check(lib().q4_dequant(w.handle, c.address(out, "f32", shape, "out", w.device), raw), "q4_dequant")
     return out
 
 
 def q4_gemm(w: Q4Weight, x, y=None, stream=None):
     """y[M][N] = x[M][K] @ W^T in x's type (float32, float16 or bfloat16); returns y (allocated if None)."""
-    L = lib()
     if w.E is not None:
         raise ValueError("q4_gemm takes a weight without an axis of experts")
-    if x.dim() != 2:
-        raise ValueError(f"x must be [M, {w.K}]")
-    m = x.shape[0]
-    code = _dtype_code(x, "x")
-    px = _arg(x, x.dtype, (m, w.K), "x", w.device)
-    raw = _raw_stream(stream, w.device)
-    if y is None:
-        y = x.new_empty((m, w.N))
-    py = _arg(y, x.dtype, (m, w.N), "y", w.device)
-    need = L.q4_gemm_workspace_size(w.handle, m, code) if m > 16 else 0
-    ws = _scratch(need, x.device, stream) if need else None
-    st = L.q4_gemm(w.handle, px, py, m, code, ws.data_ptr() if need else None, need, raw)
-    if st:
-        _check(st, "q4_gemm")
-    return y
+    out = (_compiled or _calls()).gemm(w.handle, w.device, x, y, stream if stream is None else _on(stream))
+    if out.__class__ is int:
+        _check(out, "q4_gemm")
+    return out
 
 
 def _score(score):
@@ -604,80 +562,35 @@ def moe_route(logits, k, bias=None, score="softmax", groups=1, keep=1, group_top
     float16 or bfloat16).  Experts are ranked by score + bias (bias float32 [E]), within the `keep` of `groups`
     equal groups whose `group_top` best keys add up to most; equal keys go to the lower index.  The weights are the scores,
     divided by their sum if renorm.  Slots that find no expert (logits of -inf) get idx -1 and weight 0."""
-    L = lib()
-    if logits.dim() != 2:
-        raise ValueError("logits must be [T, E]")
-    t, e = logits.shape
-    k, sc, code = int(k), _score(score), _dtype_code(logits, "logits")
-    if not 1 <= k <= min(e, 64):
-        raise ValueError(f"k must lie between 1 and {min(e, 64)}, got {k}")
-    if e > 1024 or not 1 <= groups <= 64 or e % groups or not 1 <= keep <= groups or group_top not in (1, 2):
-        raise ValueError(f"no routing over E={e}, groups={groups}, keep={keep}, group_top={group_top}")
-    device = _gpu_of(logits, "logits")
-    pl = _arg(logits, logits.dtype, (t, e), "logits", device)
-    pb = None if bias is None else _arg(bias, _f32, (e,), "bias", device)
-    raw = _raw_stream(stream, device)
-    if idx is None:
-        idx = logits.new_empty((t, k), dtype=_i32)
-    if weights is None:
-        weights = logits.new_empty((t, k), dtype=_f32)
-    st = L.moe_route(pl, pb, _arg(idx, _i32, (t, k), "idx", device), _arg(weights, _f32, (t, k), "weights", device),
-                     t, e, k, groups, keep, group_top, sc, 1 if renorm else 0, code, raw)
-    if st:
-        _check(st, "moe_route")
-    return idx, weights
+    out = (_compiled or _calls()).route(logits, k, bias, _score(score), groups, keep, group_top, renorm, idx, weights,
+                                       stream if stream is None else _on(stream))
+    if out.__class__ is int:
+        _check(out, "moe_route")
+    return out
 
 
 def moe_route_backward(logits, idx, dw, score="softmax", renorm=False, dlogits=None, stream=None):
     """Gradient of moe_route's weights: dlogits [T][E] (logits' type, overwritten; allocated if None) from dw
     float32 [T][k] and the idx that moe_route gave, the choice held fixed."""
-    L = lib()
-    if logits.dim() != 2 or idx.dim() != 2:
-        raise ValueError("logits must be [T, E] and idx [T, k]")
-    t, e = logits.shape
-    k, sc, code = idx.shape[1], _score(score), _dtype_code(logits, "logits")
-    if not 1 <= k <= 64 or not 1 <= e <= 1024:
-        raise ValueError(f"no routing of k={k} out of E={e}")
-    device = _gpu_of(logits, "logits")
-    pl = _arg(logits, logits.dtype, (t, e), "logits", device)
-    pi, pw = _arg(idx, _i32, (t, k), "idx", device), _arg(dw, _f32, (t, k), "dw", device)
-    raw = _raw_stream(stream, device)
-    if dlogits is None:
-        dlogits = logits.new_empty((t, e))
-    st = L.moe_route_backward(pl, pi, pw, _arg(dlogits, logits.dtype, (t, e), "dlogits", device), t, e, k, sc,
-                              1 if renorm else 0, code, raw)
-    if st:
-        _check(st, "moe_route_backward")
-    return dlogits
+    out = (_compiled or _calls()).route_backward(logits, idx, dw, _score(score), renorm, dlogits,
+                                                stream if stream is None else _on(stream))
+    if out.__class__ is int:
+        _check(out, "moe_route_backward")
+    return out
 
 
 def q4_moe(x, idx, weights, gate: Q4Weight, up: Q4Weight, down: Q4Weight, y=None, stream=None):
     """Experts' gated products, y[t] = sum_j weights[t][j] * down_e(silu(gate_e x_t) * (up_e x_t)) with e = idx[t][j]:
     x [T][d] (float32, float16 or bfloat16), idx int32 [T][k] (entries outside 0 .. E-1 are dropped), weights float32
     [T][k], gate and up [E][f][d], down [E][d][f]; returns y [T][d] in x's type (allocated if None)."""
-    L = lib()
     if gate.E is None or up.E is None or down.E is None:
         raise ValueError("q4_moe takes weights with an axis of experts")
-    e, f, d = gate.E, gate.N, gate.K
-    if (up.E, up.N, up.K, up.G, up.zeros) != (e, f, d, gate.G, gate.zeros) or (down.E, down.N, down.K) != (e, d, f):
-        raise ValueError(f"gate and up must be alike and down [{e}, {d}, {f}]")
-    if x.dim() != 2 or idx.dim() != 2:
-        raise ValueError("x must be [T, d] and idx [T, k]")
-    t, k = idx.shape
-    code, device = _dtype_code(x, "x"), gate.device
-    if up.device != device or down.device != device:
+    if up.like != gate.like or (down.E, down.N, down.K) != (gate.E, gate.K, gate.N):
+        raise ValueError(f"gate and up must be alike and down [{gate.E}, {gate.K}, {gate.N}]")
+    if up.device != gate.device or down.device != gate.device:
         raise ValueError("the weights are on different devices")
-    px = _arg(x, x.dtype, (t, d), "x", device)
-    pi, pw = _arg(idx, _i32, (t, k), "idx", device), _arg(weights, _f32, (t, k), "weights", device)
-    raw = _raw_stream(stream, device)
-    if y is None:
-        y = x.new_empty((t, d))
-    py = _arg(y, x.dtype, (t, d), "y", device)
-    need = L.q4_moe_workspace_size(t, k, e, d, f, code)
-    if need == 0:
-        raise ValueError(f"no experts' products for T={t}, k={k}, E={e}, d={d}, f={f}")
-    ws = _scratch(need, x.device, stream)
-    st = L.q4_moe(px, pi, pw, gate.handle, up.handle, down.handle, py, t, k, code, ws.data_ptr(), need, raw)
-    if st:
-        _check(st, "q4_moe")
-    return y
+    out = (_compiled or _calls()).moe(x, idx, weights, gate.handle, up.handle, down.handle, gate.device, y,
+                                     stream if stream is None else _on(stream))
+    if out.__class__ is int:
+        _check(out, "q4_moe")
+    return out
