@@ -67,7 +67,7 @@ int q4_dequant(const q4_weight *w, float *w_out, void *stream) {
 
 size_t q4_gemm_workspace_size(const q4_weight *w, int64_t M, int dtype) {
     if (!w || q4_packed_size(w->E, w->N, w->K, w->G, w->zeros) == 0 || M < 0 || M > kMaxRows || !known(dtype)) return 0;
-    return tq2::q4_gemm_workspace(w->N, w->K, M, dtype);
+    return tq2::q4_gemm_workspace(w->N, w->K, w->G, M, dtype);
 }
 
 int q4_gemm(const q4_weight *w, const void *x, void *y, int64_t M, int dtype, void *workspace, size_t workspace_bytes,

@@ -110,6 +110,9 @@ __device__ __forceinline__ f4 mfma16(w4 a, w4 b, f4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
 }
 
+// v is computed by this point of the program (no instruction).
+__device__ __forceinline__ void q4_here(f4 &v) { asm volatile("" : "+v"(v)); }
+
 __device__ __forceinline__ float half_bits(uint32_t h) { return (float)__builtin_bit_cast(_Float16, (uint16_t)h); }
 
 // Row r's scales (f16, the first in the low half of .x) and zero points (a byte each; 8
@@ -158,7 +161,7 @@ __device__ __forceinline__ float q4_weight_at(const Q4View &w, int e, int n, int
 hipError_t launch_q4_pack(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, const Q4View &v,
                           hipStream_t s);
 hipError_t launch_q4_dequant(const Q4View &v, float *out, hipStream_t s);
-size_t q4_gemm_workspace(int64_t N, int64_t K, int64_t M, int dtype);
+size_t q4_gemm_workspace(int64_t N, int64_t K, int64_t G, int64_t M, int dtype);
 hipError_t launch_q4_gemm(const Q4View &v, const void *x, void *y, int64_t M, int dtype, void *ws, hipStream_t s);
 
 // Experts' products.  Workspace: see MoePlan.

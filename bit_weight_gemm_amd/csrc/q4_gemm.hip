@@ -71,17 +71,21 @@ __global__ __launch_bounds__(256) void q4_dequant_kernel(Q4View v, float *out) {
     out[i] = q4_weight_at(v, (int)(en / v.N), (int)(en % v.N), k);
 }
 
+// Column blocks per wave: one while that gives each of the 256 compute units one workgroup
+// at most (N = K = 4096, one row: 5.0 us, with two 5.9), two beyond (N = 5003, sixteen rows: 7.6
+// us, with one 8.8), so that x is read less often; four for f32 x beyond two workgroups each (x is
+// split for all columns at once; N = 14336, K = 4096, one row 16.5, with two 20.3 us).
 template <int XT, int G>
 hipError_t dense(const Q4Args &a, hipStream_t s) {
-    // Column blocks per wave: one while that fits the 256 compute units in two
-    // rounds of workgroups, more beyond, so that x is read less often.
     const int64_t nb = a.w.nb;
     if (a.M <= 16) {
-        if (nb <= 512) return run_q4_skinny<XT, G, 1, 1, kDense>(a, 1, s);
+        if (nb <= 256) return run_q4_skinny<XT, G, 1, 1, kDense>(a, 1, s);
+        if constexpr (XT == kXF32x3) {
+            if (nb > 512) return run_q4_skinny<XT, G, 1, 4, kDense>(a, 1, s);
+        }
         return run_q4_skinny<XT, G, 1, 2, kDense>(a, 1, s);
     }
-    if (a.M <= 32 || XT == kXF32x3) return run_q4_skinny<XT, G, 2, 2, kDense>(a, (a.M + 31) / 32, s);
-    return run_q4_skinny<XT, G, 4, 2, kDense>(a, (a.M + 63) / 64, s);
+    return run_q4_skinny<XT, G, 2, 2, kDense>(a, (a.M + 31) / 32, s);
 }
 
 template <int XT>
@@ -109,32 +113,93 @@ hipError_t launch_q4_dequant(const Q4View &v, float *out, hipStream_t s) {
     return hipGetLastError();
 }
 
-// The tiled product from kTiledRows rows on (below, the skinny kernel on tiles of 64).
-constexpr int64_t kTiledRows = 256;
+namespace {
 
-size_t q4_gemm_workspace(int64_t, int64_t K, int64_t M, int dtype) {
-    if (M < kTiledRows || q4_plain_x(K, dtype)) return 0;
-    const size_t lda = (size_t)(K + 127) / 128 * 128;
-    return (size_t)q4_planes(dtype) * M * lda * 2 + (size_t)(M * 4 + 255) / 256 * 256;
+// How M rows are multiplied: tiles of bm rows with the units in `split` shares, or, bm 0, the
+// skinny kernel on blocks of 32 rows.
+struct Deal {
+    int bm, split;
+};
+
+// The shortest by an estimate in microseconds, whose constants were fitted to measured times
+// (M = 33 .. 2048; N x K = 4096 x 4096, 14336 x 4096, 5003 x 4000, 1024 x 1024 and 1000 x 8192;
+// all G and types).  A kernel takes as many rounds of the 256 compute units as its workgroups need,
+// and in each so many microseconds a unit of 128 k; shares are written and joined at 8 TB/s.
+// f16, 4096 x 4096, estimate against measured: 64 rows skinny 10.8 / 11.3, 128 rows in
+// 8 shares 17.6 / 17.3 (skinny 19.6), 256 rows in 4 shares 23 / 22.6 (skinny 35, one share 41), 512 rows in
+// 2 shares 34 / 35 (one 43), 2048 rows in tiles of 128 67 / 75 (of 64: 93).
+Deal deal(int64_t N, int64_t K, int64_t G, int64_t M, int dtype) {
+    if (M <= 32) return Deal{0, 1};  // 4096 x 4096: 11 us, in tiles at least 14
+    constexpr double kCus = 256;
+    const bool f32 = dtype == kF32, fine = G == 32;
+    const double nb = (double)((N + 15) / 16), ku = (double)((K + 127) / 128);
+    auto up = [](double v) { return (double)(int64_t)(v + 0.999999); };
+    Deal best{0, 1};
+    double least;
+    {
+        const double blocks = up(nb / 2), rows = (double)((M + 31) / 32);
+        double wk = 1;
+        while (wk < 8 && blocks * rows * wk < kWavesWanted && 2 * wk <= ku) wk *= 2;
+        least = up(up(blocks * wk / 8) * rows / kCus) * (2.0 + up(ku / wk) * (f32 ? (fine ? 4.5 : 3.9) : (fine ? 2.6 : 2.2)));
+    }
+    for (int bm = 64; bm <= 128; bm *= 2) {
+        if (bm == 128 && f32 && fine) continue;  // its registers do not suffice
+        const double tiles = up(nb / 16) * up((double)M / bm);
+        const double unit = f32 ? (bm == 64 ? (fine ? 2.4 : 2.0) : 3.4) : (bm == 64 ? (fine ? 1.6 : 1.35) : (fine ? 2.4 : 1.95));
+        for (int split = 1; split <= 16 && split <= ku && (split == 1 || tiles * split <= kCus); ++split) {
+            const double us = 5.5 + (q4_plain_x(K, dtype) ? 0.0 : 5.0) + up(tiles * split / kCus) * up(ku / split) * unit +
+                              (split == 1 ? 0.0 : 3.5 + (double)split * M * N * 1e-6);
+            if (us < least) least = us, best = Deal{bm, split};
+        }
+    }
+    return best;
+}
+
+struct DenseWs {
+    size_t off_scale, off_part, total;
+    int64_t part_stride;
+};
+DenseWs dense_ws(const Deal &d, int64_t N, int64_t K, int64_t M, int dtype) {
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    DenseWs w{};
+    const bool plain = q4_plain_x(K, dtype);
+    w.off_scale = plain ? 0 : up((size_t)q4_planes(dtype) * M * ((K + 127) / 128 * 128) * 2);
+    w.off_part = w.off_scale + (plain ? 0 : up((size_t)M * 4));
+    w.part_stride = (M * N + 3) / 4 * 4;
+    w.total = w.off_part + (d.split > 1 ? (size_t)d.split * w.part_stride * 4 : 0);
+    return w;
+}
+
+}  // namespace
+
+size_t q4_gemm_workspace(int64_t N, int64_t K, int64_t G, int64_t M, int dtype) {
+    const Deal d = deal(N, K, G, M, dtype);
+    return d.bm ? dense_ws(d, N, K, M, dtype).total : 0;
 }
 
 hipError_t launch_q4_gemm(const Q4View &v, const void *x, void *y, int64_t M, int dtype, void *ws, hipStream_t s) {
-    if (M >= kTiledRows) {
+    const Deal d = deal(v.N, v.K, v.G, M, dtype);
+    if (d.bm) {
+        const DenseWs w = dense_ws(d, v.N, v.K, M, dtype);
+        char *b = static_cast<char *>(ws);
         Q4TArgs a{};
-        a.w = v, a.y = y, a.M = M;
+        a.w = v, a.y = y, a.M = M, a.split = d.split;
         if (q4_plain_x(v.K, dtype)) {
             a.a = static_cast<const _Float16 *>(x), a.lda = v.K;
         } else {
             Q4Prep p{};
             p.x = x, p.rows = M, p.K = v.K;
             p.lda = (int64_t)v.ku * 128, p.plane = M * p.lda;
-            p.out = static_cast<_Float16 *>(ws);
-            p.rowscale = reinterpret_cast<float *>(p.out + q4_planes(dtype) * p.plane);
+            p.out = reinterpret_cast<_Float16 *>(b);
+            p.rowscale = reinterpret_cast<float *>(b + w.off_scale);
             const hipError_t e = launch_q4_prep(p, dtype, s);
             if (e != hipSuccess) return e;
             a.a = p.out, a.lda = p.lda, a.plane = p.plane, a.rowscale = p.rowscale;
         }
-        return launch_q4_tiled_dense(a, dtype, 128, s);
+        if (d.split > 1) a.part = reinterpret_cast<float *>(b + w.off_part), a.part_stride = w.part_stride;
+        const hipError_t e = launch_q4_tiled_dense(a, dtype, d.bm, s);
+        if (e != hipSuccess || d.split == 1) return e;
+        return launch_q4_join(a.part, a.part_stride, d.split, y, M * v.N, dtype, s);
     }
     Q4Args a{};
     a.w = v, a.x = x, a.y = y, a.M = M;

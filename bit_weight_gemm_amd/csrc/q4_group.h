@@ -161,7 +161,7 @@ __global__ __launch_bounds__(512, 4) void q4_group_kernel(Q4GroupArgs p) {
             for (int cb = 0; cb < CB; ++cb) acc[rb][cb] = f4{};
         auto compute = [&](int st, int u) {
             f4 part[RB][CB];
-            uint32_t c0w[CB], c1w[CB];
+            Q4Zero zero[CB];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bool first = (32 * j) % G == 0, last = (32 * (j + 1)) % G == 0;
@@ -175,8 +175,8 @@ __global__ __launch_bounds__(512, 4) void q4_group_kernel(Q4GroupArgs p) {
                             &xs[(q * ROWS + rb * 16 + r) * kp + u * 128 + (((4 * j + h) ^ r) << 3)]);
 #pragma unroll
                 for (int cb = 0; cb < CB; ++cb) {
-                    if (first) q4_zero_pairs((zreg[st][cb] >> (8 * g)) & 255u, c0w[cb], c1w[cb]);
-                    const h8 b = q4_word_f16(breg[st][cb][j], c0w[cb], c1w[cb], magic);
+                    if (first) zero[cb] = q4_zero((zreg[st][cb] >> (8 * g)) & 255u);
+                    const h8 b = q4_word_f16(breg[st][cb][j], zero[cb], magic);
                     const float s = half_bits((g & 2 ? sreg[st][cb].y : sreg[st][cb].x) >> (16 * (g & 1)));
 #pragma unroll
                     for (int rb = 0; rb < RB; ++rb) {
@@ -187,6 +187,7 @@ __global__ __launch_bounds__(512, 4) void q4_group_kernel(Q4GroupArgs p) {
                         if (last) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) acc[rb][cb][i] += s * part[rb][cb][i];
+                            q4_here(acc[rb][cb]);
                         }
                     }
                 }

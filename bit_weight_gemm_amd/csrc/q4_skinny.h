@@ -113,12 +113,13 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
         e = t.x, row0 = t.y, count = t.z;
     }
     const int wk = wave & ((1 << p.log_wk) - 1), wn = wave >> p.log_wk, cols = (8 >> p.log_wk) * NC;
-    // rows past the last repeat it (their results are not stored)
+    // rows past the last are zeros, not loaded (their results are not stored)
     int64_t xoff[RB];
+    bool live[RB];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
-        const int rr = rb * 16 + r < count ? rb * 16 + r : count - 1;
-        int64_t row = row0 + rr;
+        live[rb] = rb * 16 + r < count;
+        int64_t row = row0 + (live[rb] ? rb * 16 + r : 0);
         if constexpr (MODE == kGateUp) row = p.order[row] / p.topk;
         xoff[rb] = row * K + 8 * h;
     }
@@ -153,7 +154,7 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
         for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool in = u * 128 + 32 * j < K;  // K is a multiple of 32
+                const bool in = live[rb] && u * 128 + 32 * j < K;  // K is a multiple of 32
                 if constexpr (F32) {
                     const w4 *x = reinterpret_cast<const w4 *>(static_cast<const float *>(p.x) + xoff[rb] + u * 128 + 32 * j);
                     areg[st][rb][2 * j] = in ? x[0] : w4{};
@@ -210,8 +211,11 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             acc[rb][cb][i] += s * (EXACT ? part[rb][cb][i] : part[rb][cb][i] - zc * sum[rb][i]);
+#pragma unroll
+                    for (int rb = 0; rb < RB; ++rb) q4_here(acc[rb][cb]);  // not behind all products: registers
                 }
             }
+            if constexpr (RB > 1) __builtin_amdgcn_sched_barrier(0);
         }
     };
 
@@ -277,7 +281,7 @@ template <int XT, int G, int RB, int CB, int MODE>
 inline hipError_t run_q4_skinny(Q4Args a, int64_t grid_y, hipStream_t s) {
     constexpr int PERX = XT == kXF32x2 || XT == kXF32x3 ? 8 : 4;
     constexpr int REGS = 4 * (RB * PERX + CB);  // registers of one unit in flight
-    constexpr int D = REGS <= 20 ? 4 : REGS <= 48 ? 2 : 1;
+    constexpr int D = REGS <= 48 ? 2 : 1;  // (72 registers twice: 23 f32 rows 20.2 against 16.6 us)
     constexpr int NC = MODE == kGateUp ? CB / 2 : CB;
     const int64_t blocks = (a.w.nb + NC - 1) / NC;
     while (a.log_wk < 3 && (blocks * grid_y << a.log_wk) < kWavesWanted && (2 << a.log_wk) <= a.w.ku) ++a.log_wk;

@@ -29,6 +29,9 @@ struct Q4TArgs {
     const float *rowscale;   // [rows]: the power of two that each row was divided by (nullptr: 1)
     void *y;
     int64_t M;               // kTDense: rows
+    float *part;             // kTDense: the sums of each share of the units (nullptr: one share, y itself)
+    int64_t part_stride;
+    int split;               // shares
     int tiles_n;
     int topk;
     const int32_t *order;
@@ -42,24 +45,26 @@ struct Q4TArgs {
 
 __device__ __forceinline__ int q4_lds(int row, int chunk) { return row * 128 + ((chunk ^ (row & 15)) << 3); }
 
-// code - zero of a word's eight codes: the codes inserted into 1024 (or, four bits
-// higher, read as 1024 + 16 code and divided by 16), the zero point taken off; all exact.
-__device__ __forceinline__ h8 q4_word_f16(uint32_t w, uint32_t c0, uint32_t c1, uint32_t magic) {
-    constexpr uint32_t m0 = 0x000F000Fu, m1 = 0x00F000F0u;
-    const h2 k = {(_Float16)0.0625f, (_Float16)0.0625f};
-    const uint32_t v = w >> 8;
-    const h2 p0 = as_h2((w & m0) | (magic & ~m0)) + as_h2(c0);
-    const h2 p1 = __builtin_elementwise_fma(as_h2((w & m1) | (magic & ~m1)), k, as_h2(c1));
-    const h2 p2 = as_h2((v & m0) | (magic & ~m0)) + as_h2(c0);
-    const h2 p3 = __builtin_elementwise_fma(as_h2((v & m1) | (magic & ~m1)), k, as_h2(c1));
-    return h8{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+// -(1024 + zero) and -(64 + zero), exact in f16.
+struct Q4Zero {
+    _Float16 c0, c1;
+};
+__device__ __forceinline__ Q4Zero q4_zero(uint32_t zero) {
+    const _Float16 z = (_Float16)(uint16_t)zero;
+    return Q4Zero{(_Float16)-1024.0f - z, (_Float16)-64.0f - z};
 }
 
-// The pairs that q4_word_f16 adds: -(1024 + zero) and -(64 + zero), exact in f16.
-__device__ __forceinline__ void q4_zero_pairs(uint32_t zero, uint32_t &c0, uint32_t &c1) {
-    c0 = (0xE400u | zero) * 0x10001u;
-    const _Float16 f = (_Float16)(-64.0f - (float)zero);
-    c1 = (uint32_t)__builtin_bit_cast(uint16_t, f) * 0x10001u;
+// code - zero of a word's eight codes: the codes inserted into 1024 (or, four bits
+// higher, read as 1024 + 16 code and divided by 16), the zero point taken off; all exact.
+__device__ __forceinline__ h8 q4_word_f16(uint32_t w, Q4Zero z, uint32_t magic) {
+    constexpr uint32_t m0 = 0x000F000Fu, m1 = 0x00F000F0u;
+    const h2 k = {(_Float16)0.0625f, (_Float16)0.0625f}, c0 = {z.c0, z.c0}, c1 = {z.c1, z.c1};
+    const uint32_t v = w >> 8;
+    const h2 p0 = as_h2((w & m0) | (magic & ~m0)) + c0;
+    const h2 p1 = __builtin_elementwise_fma(as_h2((w & m1) | (magic & ~m1)), k, c1);
+    const h2 p2 = as_h2((v & m0) | (magic & ~m0)) + c0;
+    const h2 p3 = __builtin_elementwise_fma(as_h2((v & m1) | (magic & ~m1)), k, c1);
+    return h8{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
 }
 
 // The exponent by which a row with the largest finite value `most` is shifted to bring
@@ -86,6 +91,7 @@ __device__ __forceinline__ int q4_h_exp(int norm_exp, uint32_t gate_most, uint32
 template <int BM, int G, int P, int MODE, int DT>
 __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     constexpr int RB = BM / 16, GPU_ = 128 / G, NCB = 2;
+    constexpr int FRAG = P == 1;                  // fragments are read a row block ahead where registers allow
     constexpr int PPT = BM * 16 / 512;  // 16-byte pieces of a plane's tile per thread
     __shared__ __attribute__((aligned(16))) _Float16 As[2][P][BM * 128];
     __shared__ float rs[BM];
@@ -94,6 +100,9 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, h = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ku = p.w.ku;
+    // kTDense: the units are dealt to gridDim.y workgroups
+    const int u_begin = MODE == kTDense ? (int)((int64_t)ku * blockIdx.y / gridDim.y) : 0;
+    const int u_end = MODE == kTDense ? (int)((int64_t)ku * (blockIdx.y + 1) / gridDim.y) : ku;
     const uint32_t magic = f16_magic();
 
     // Workgroups go round the 8 XCDs: give each XCD a run of neighbouring tiles, N first.
@@ -185,55 +194,67 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
         for (int cb = 0; cb < NCB; ++cb) acc[rb][cb] = f4{};
     auto compute = [&](int buf, int st, auto &&hook) {
         h8 b[NCB][4];
-        float s[NCB][GPU_];
 #pragma unroll
         for (int cb = 0; cb < NCB; ++cb)
 #pragma unroll
-            for (int g = 0; g < GPU_; ++g) {
-                s[cb][g] = half_bits((g & 2 ? sreg[st][cb].y : sreg[st][cb].x) >> (16 * (g & 1)));
-                const uint32_t z = (zreg[st][cb] >> (8 * g)) & 255u;
-                uint32_t c0, c1;
-                q4_zero_pairs(z, c0, c1);
-#pragma unroll
-                for (int j = g * G / 32; j < (g + 1) * G / 32; ++j) b[cb][j] = q4_word_f16(breg[st][cb][j], c0, c1, magic);
-            }
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            h8 a[P][4];
+            for (int j = 0; j < 4; ++j)
+                b[cb][j] = q4_word_f16(breg[st][cb][j], q4_zero((zreg[st][cb] >> (8 * (32 * j / G))) & 255u), magic);
+        h8 a[1 + FRAG][P][4];
+        auto fragments = [&](int rb) {
 #pragma unroll
             for (int q = 0; q < P; ++q)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    a[q][j] = *reinterpret_cast<const h8 *>(&As[buf][q][q4_lds(rb * 16 + r, 4 * j + h)]);
+                    a[rb & FRAG][q][j] = *reinterpret_cast<const h8 *>(&As[buf][q][q4_lds(rb * 16 + r, 4 * j + h)]);
+        };
+        // Step t: column block t % NCB of row block t / NCB.  The previous step's parts are scaled
+        // while this one's products run, and no later: left free, the compiler puts all scaling
+        // behind all products, whose parts then go to scratch memory (G = 32, 1024 x 14336 x 4096: 1337
+        // against 170 us; G = 64, 2048 x 4096 x 4096: 132 against 74).  One part a step fits the registers
+        // as it is (G = 128: 79 us, held in place 84).
+        f4 part[2][GPU_];
+        auto scale = [&](int t) {
+            const int rb = t / NCB, cb = t % NCB;
 #pragma unroll
-            for (int cb = 0; cb < NCB; ++cb)
+            for (int g = 0; g < GPU_; ++g) {
+                const float s = half_bits((g & 2 ? sreg[st][cb].y : sreg[st][cb].x) >> (16 * (g & 1)));
 #pragma unroll
-                for (int g = 0; g < GPU_; ++g) {
-                    f4 part = {};
+                for (int i = 0; i < 4; ++i) acc[rb][cb][i] += s * part[t & 1][g][i];
+            }
+            if constexpr (GPU_ > 1 || P > 1) q4_here(acc[rb][cb]);
+        };
+        if (FRAG) fragments(0);
 #pragma unroll
-                    for (int q = P - 1; q >= 0; --q)
+        for (int t = 0; t < RB * NCB; ++t) {
+            const int rb = t / NCB, cb = t % NCB;
+            if (cb == 0 && rb + FRAG < RB) fragments(rb + FRAG);
 #pragma unroll
-                        for (int j = g * G / 32; j < (g + 1) * G / 32; ++j)
-                            part = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[q][j], b[cb][j], part, 0, 0, 0);
+            for (int g = 0; g < GPU_; ++g) {
+                part[t & 1][g] = f4{};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[rb][cb][i] += s[cb][g] * part[i];
-                }
-            if (rb == 0) hook();
+                for (int q = P - 1; q >= 0; --q)
+#pragma unroll
+                    for (int j = g * G / 32; j < (g + 1) * G / 32; ++j)
+                        part[t & 1][g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[rb & FRAG][q][j], b[cb][j], part[t & 1][g], 0, 0, 0);
+            }
+            if (t > 0) scale(t - 1);
+            if (t == NCB) hook();
         }
+        scale(RB * NCB - 1);
     };
 
-    auto last = [&](int u) { return u < ku ? u : ku - 1; };
-    load_a(0);
-    load_b(0, 0);
-    load_b(1, last(1));
+    auto last = [&](int u) { return u < u_end ? u : u_end - 1; };
+    load_a(u_begin);
+    load_b(0, u_begin);
+    load_b(1, last(u_begin + 1));
     store_a(0);
-    load_a(last(1));
+    load_a(last(u_begin + 1));
     __syncthreads();
-    for (int u0 = 0; u0 < ku; u0 += 2) {
+    for (int u0 = u_begin; u0 < u_end; u0 += 2) {
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
             const int u = u0 + st;
-            if (u < ku) {
+            if (u < u_end) {
                 compute(st, st, [&] {
                     store_a(st ^ 1);
                     load_a(last(u + 2));
@@ -269,7 +290,9 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
                     if (m >= count || n >= p.w.N) continue;
                     const float v = acc[rb][cb][i] * rs[m];
                     if constexpr (MODE == kTDense) {
-                        store_from_float<DT>(p.y, (row0 + m) * p.w.N + n, v);
+                        const int64_t at = (row0 + m) * p.w.N + n;
+                        if (p.part) p.part[blockIdx.y * p.part_stride + at] = v;
+                        else store_from_float<DT>(p.y, at, v);
                     } else {
                         static_cast<float *>(p.y)[(int64_t)hexp[m] * p.w.N + n] = v;
                     }
@@ -283,7 +306,8 @@ template <int BM, int G, int P, int MODE, int DT>
 inline hipError_t run_q4_tiled(Q4TArgs a, int64_t tiles_m, hipStream_t s) {
     a.tiles_n = MODE == kTGateUp ? (a.w.nb + 7) / 8 : (a.w.nb + 15) / 16;
     const int64_t grid = (tiles_m * a.tiles_n + 7) / 8 * 8;
-    q4_tiled_kernel<BM, G, P, MODE, DT><<<dim3((unsigned)grid), dim3(512), 0, s>>>(a);
+    const dim3 blocks((unsigned)grid, MODE == kTDense ? (unsigned)a.split : 1);
+    q4_tiled_kernel<BM, G, P, MODE, DT><<<blocks, dim3(512), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -302,6 +326,7 @@ hipError_t launch_q4_prep(const Q4Prep &p, int dtype, hipStream_t s);
 inline bool q4_plain_x(int64_t K, int dtype) { return dtype == kF16 && K % 128 == 0; }
 inline int q4_planes(int dtype) { return dtype == kF32 ? 2 : 1; }
 hipError_t launch_q4_tiled_dense(const Q4TArgs &a, int dtype, int bm, hipStream_t s);
+hipError_t launch_q4_join(const float *part, int64_t stride, int split, void *y, int64_t n, int dtype, hipStream_t s);
 hipError_t launch_q4_tiled_gate_up(const Q4TArgs &a, int planes, int bm, int64_t tiles, hipStream_t s);
 hipError_t launch_q4_tiled_down(const Q4TArgs &a, int planes, int bm, int64_t tiles, hipStream_t s);
 

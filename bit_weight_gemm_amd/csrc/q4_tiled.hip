@@ -105,6 +105,18 @@ __global__ __launch_bounds__(256) void q4_prep_kernel(Q4Prep p) {
     }
 }
 
+// y = the sum of the shares' sums, in their order.
+template <int DT>
+__global__ __launch_bounds__(256) void q4_join_kernel(const float *part, int64_t stride, int split, void *y, int64_t n) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    f4 v = *reinterpret_cast<const f4 *>(part + i);  // the stride leaves room for the last four
+    for (int q = 1; q < split; ++q) v += *reinterpret_cast<const f4 *>(part + q * stride + i);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (i + q < n) store_from_float<DT>(y, i + q, v[q]);
+}
+
 template <int G>
 hipError_t dense(const Q4TArgs &a, int dtype, int bm, hipStream_t s) {
     const int64_t t64 = (a.M + 63) / 64, t128 = (a.M + 127) / 128;
@@ -133,6 +145,14 @@ hipError_t launch_q4_tiled_dense(const Q4TArgs &a, int dtype, int bm, hipStream_
     if (a.w.G == 32) return dense<32>(a, dtype, bm, s);
     if (a.w.G == 64) return dense<64>(a, dtype, bm, s);
     return dense<128>(a, dtype, bm, s);
+}
+
+hipError_t launch_q4_join(const float *part, int64_t stride, int split, void *y, int64_t n, int dtype, hipStream_t s) {
+    const dim3 grid((unsigned)((n + 1023) / 1024)), block(256);
+    if (dtype == kF32) q4_join_kernel<kF32><<<grid, block, 0, s>>>(part, stride, split, y, n);
+    else if (dtype == kF16) q4_join_kernel<kF16><<<grid, block, 0, s>>>(part, stride, split, y, n);
+    else q4_join_kernel<kBF16><<<grid, block, 0, s>>>(part, stride, split, y, n);
+    return hipGetLastError();
 }
 
 hipError_t launch_q4_tiled_gate_up(const Q4TArgs &a, int planes, int bm, int64_t tiles, hipStream_t s) {
