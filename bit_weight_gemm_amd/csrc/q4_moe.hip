@@ -25,9 +25,16 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(const int32_t *idx, int 
     const int tid = threadIdx.x;
     for (int e = tid; e < E; e += 1024) cnt[e] = 0;
     __syncthreads();
-    for (int s = tid; s < slots; s += 1024) {
-        const int e = idx[s];
-        if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+    // sixteen slots of a thread at a time: their loads, then their atomics, wait together
+    // (16384 slots: 16 us one by one)
+    constexpr int kBatch = 16;
+    for (int s0 = tid; s0 < slots; s0 += 1024 * kBatch) {
+        int e[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) e[i] = s0 + 1024 * i < slots ? idx[s0 + 1024 * i] : -1;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (e[i] >= 0 && e[i] < E) atomicAdd(&cnt[e[i]], 1);
     }
     __syncthreads();
     // inclusive scans of the slots and of the tiles, in place
@@ -52,9 +59,15 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(const int32_t *idx, int 
     __syncthreads();
     if (tid < E) cnt[tid] = first;  // the next free place
     __syncthreads();
-    for (int s = tid; s < slots; s += 1024) {
-        const int e = idx[s];
-        if (e >= 0 && e < E) order[atomicAdd(&cnt[e], 1)] = s;
+    for (int s0 = tid; s0 < slots; s0 += 1024 * kBatch) {
+        int e[kBatch], at[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) e[i] = s0 + 1024 * i < slots ? idx[s0 + 1024 * i] : -1;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) at[i] = e[i] >= 0 && e[i] < E ? atomicAdd(&cnt[e[i]], 1) : -1;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (at[i] >= 0) order[at[i]] = s0 + 1024 * i;
     }
 }
 
@@ -74,17 +87,11 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(const float *part, const i
     for (int q = 0; q < 4; ++q) store_from_float<DT>(y, i + q, v[q]);
 }
 
-template <int XT, int G, int MODE>
-hipError_t product_rb(const MoePlan &p, const Q4Args &a, hipStream_t s) {
-    return p.tile_rows == 16 ? run_q4_skinny<XT, G, 1, 2, MODE>(a, p.max_tiles, s)
-                             : run_q4_skinny<XT, G, 2, 2, MODE>(a, p.max_tiles, s);
-}
-
 template <int XT, int MODE>
 hipError_t product(const MoePlan &p, const Q4Args &a, hipStream_t s) {
-    if (a.w.G == 32) return product_rb<XT, 32, MODE>(p, a, s);
-    if (a.w.G == 64) return product_rb<XT, 64, MODE>(p, a, s);
-    return product_rb<XT, 128, MODE>(p, a, s);
+    if (a.w.G == 32) return run_q4_skinny<XT, 32, 1, 2, MODE>(a, p.max_tiles, s);
+    if (a.w.G == 64) return run_q4_skinny<XT, 64, 1, 2, MODE>(a, p.max_tiles, s);
+    return run_q4_skinny<XT, 128, 1, 2, MODE>(a, p.max_tiles, s);
 }
 
 template <int XT, int PH>
@@ -147,7 +154,7 @@ hipError_t grouped(const MoePlan &p, const void *x, const int32_t *idx, const fl
     return sum(d.y, idx, y, T, k, gate.E, down.N, dtype, s);
 }
 
-// Few rows per expert: tiles of 16 or 32 rows, h in f32.
+// Few rows per expert: tiles of 16 rows, h in f32.
 hipError_t skinny(const MoePlan &p, const void *x, const float *weights, const Q4View &gate, const Q4View &up,
                   const Q4View &down, int64_t k, int dtype, char *b, hipStream_t s) {
     Q4Args g{};
@@ -204,6 +211,14 @@ hipError_t tiled(const MoePlan &p, const void *x, const float *weights, const Q4
 }  // namespace
 
 // Up to kDirectSlots slots, each reads its expert's weights for itself; their rows have to fit in LDS.
+// Beyond, by slots per expert (bf16; 64 experts of 8, 2048 x 1024: "large", 8 experts of 2, 1024 x 1024:
+// "small", which tiles of the gate product cannot fill the 256 compute units with):
+//   up to 8 (4 if small): workgroups find their slots (large, 33 tokens: 88 us, tiles of 64 rows
+//     106; small, 33 tokens: 30, rows of 16 24);
+//   up to 48, small: plan and blocks of 16 rows (128 tokens 39, tiles of 64 43, of 32-row blocks 36);
+//   then tiles of 64 rows (large, 100 tokens: 116, found slots 139; 256 tokens 135, rows of 32 240;
+//     small, 256 tokens 45, rows of 16 60);
+//   from 256 on tiles of 128 (large, 2048 tokens: 399, of 64 414; f32 629, of 64 591: not for f32).
 constexpr int64_t kDirectSlots = 32;
 constexpr size_t kDirectLds = 48 * 1024;
 
@@ -215,10 +230,12 @@ MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtyp
     p.ldx = (d + 127) / 128 * 128, p.ldh = (f + 127) / 128 * 128;
     p.direct = p.slots <= kDirectSlots && q4_row_lds(p.ldx / 128, f32 ? 3 : 1) <= kDirectLds &&
                q4_row_lds(k * (p.ldh / 128), f32 ? 3 : 2) <= kDirectLds;
-    p.grouped = !p.direct && p.slots <= kGroupMaxSlots && p.slots <= 24 * E && d <= kGroupMaxK && f <= kGroupMaxK &&
+    const bool fills = E * ((f + 127) / 128) >= 256;
+    const int64_t few = fills ? 8 * E : 4 * E;
+    p.grouped = !p.direct && p.slots <= kGroupMaxSlots && p.slots <= few && d <= kGroupMaxK && f <= kGroupMaxK &&
                 q4_group_lds(d > f ? d : f, q4_planes(dtype), 16) <= kGroupLds;
-    p.tiled = !p.direct && !p.grouped && p.slots > 32 * E;
-    p.tile_rows = p.tiled ? (p.slots > 96 * E ? 128 : 64) : p.slots <= 16 * E ? 16 : 32;
+    p.tiled = !p.direct && !p.grouped && p.slots > (fills ? 8 * E : 48 * E);
+    p.tile_rows = !p.tiled ? 16 : p.slots >= 256 * E && !f32 ? 128 : 64;
     p.max_tiles = p.slots / p.tile_rows + (E < p.slots ? E : p.slots);
     size_t at = 256;  // the first 256 bytes hold the number of tiles
     auto take = [&](size_t n) {
