@@ -475,6 +475,9 @@ hipError_t route_v(const RouteArgs &a, int log_lanes, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Tokens of one launch: a grid holds fewer than 2^32 work items, 64 a token.
+constexpr int64_t kMaxTokens = (int64_t)1 << 25;
+
 template <int DT>
 hipError_t route(RouteArgs a, hipStream_t s) {
     a.n = a.E / a.groups;
@@ -508,17 +511,32 @@ hipError_t backward(const void *l, const int32_t *idx, const float *dw, void *dl
 
 }  // namespace
 
-hipError_t launch_moe_route(const RouteArgs &a, hipStream_t s) {
-    if (a.dtype == kF32) return route<kF32>(a, s);
-    if (a.dtype == kF16) return route<kF16>(a, s);
-    return route<kBF16>(a, s);
+hipError_t launch_moe_route(const RouteArgs &all, hipStream_t s) {
+    hipError_t e = hipSuccess;
+    for (int64_t t = 0; t < all.T && e == hipSuccess; t += kMaxTokens) {
+        RouteArgs a = all;
+        a.logits = static_cast<const char *>(all.logits) + t * all.E * (all.dtype == kF32 ? 4 : 2);
+        a.idx += t * all.k, a.weights += t * all.k;
+        a.T = all.T - t < kMaxTokens ? all.T - t : kMaxTokens;
+        e = all.dtype == kF32 ? route<kF32>(a, s) : all.dtype == kF16 ? route<kF16>(a, s) : route<kBF16>(a, s);
+    }
+    return e;
 }
 
 hipError_t launch_moe_route_backward(const void *logits, const int32_t *idx, const float *dw, void *dlogits, int64_t T,
                                      int E, int k, int dtype, bool sigmoid, bool renorm, hipStream_t s) {
-    if (dtype == kF32) return backward<kF32>(logits, idx, dw, dlogits, T, E, k, sigmoid, renorm, s);
-    if (dtype == kF16) return backward<kF16>(logits, idx, dw, dlogits, T, E, k, sigmoid, renorm, s);
-    return backward<kBF16>(logits, idx, dw, dlogits, T, E, k, sigmoid, renorm, s);
+    hipError_t e = hipSuccess;
+    for (int64_t t = 0; t < T && e == hipSuccess; t += kMaxTokens) {
+        const int64_t n = T - t < kMaxTokens ? T - t : kMaxTokens, at = t * E * (dtype == kF32 ? 4 : 2);
+        const void *l = static_cast<const char *>(logits) + at;
+        void *dl = static_cast<char *>(dlogits) + at;
+        const int32_t *i = idx + t * k;
+        const float *d = dw + t * k;
+        if (dtype == kF32) e = backward<kF32>(l, i, d, dl, n, E, k, sigmoid, renorm, s);
+        else if (dtype == kF16) e = backward<kF16>(l, i, d, dl, n, E, k, sigmoid, renorm, s);
+        else e = backward<kBF16>(l, i, d, dl, n, E, k, sigmoid, renorm, s);
+    }
+    return e;
 }
 
 }  // namespace tq2

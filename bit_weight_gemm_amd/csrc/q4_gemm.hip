@@ -64,11 +64,12 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t *codes, cons
 }
 
 __global__ __launch_bounds__(256) void q4_dequant_kernel(Q4View v, float *out) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)v.E * v.N * v.K) return;
-    const int k = (int)(i % v.K);
-    const int64_t en = i / v.K;
-    out[i] = q4_weight_at(v, (int)(en / v.N), (int)(en % v.N), k);
+    const int64_t n = (int64_t)v.E * v.N * v.K, step = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+        const int k = (int)(i % v.K);
+        const int64_t en = i / v.K;
+        out[i] = q4_weight_at(v, (int)(en / v.N), (int)(en % v.N), k);
+    }
 }
 
 // Column blocks per wave: one while that gives each of the 256 compute units one workgroup
@@ -109,7 +110,8 @@ hipError_t launch_q4_pack(const uint8_t *codes, const uint16_t *scales, const ui
 
 hipError_t launch_q4_dequant(const Q4View &v, float *out, hipStream_t s) {
     const int64_t n = (int64_t)v.E * v.N * v.K;
-    q4_dequant_kernel<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s>>>(v, out);
+    const int64_t blocks = (n + 255) / 256, most = (int64_t)1 << 20;
+    q4_dequant_kernel<<<dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, s>>>(v, out);
     return hipGetLastError();
 }
 
@@ -135,8 +137,8 @@ Deal deal(int64_t N, int64_t K, int64_t G, int64_t M, int dtype) {
     const double nb = (double)((N + 15) / 16), ku = (double)((K + 127) / 128);
     auto up = [](double v) { return (double)(int64_t)(v + 0.999999); };
     Deal best{0, 1};
-    double least;
-    {
+    double least = 1e300;
+    if (M <= 65535 * 32) {  // a grid's second axis
         const double blocks = up(nb / 2), rows = (double)((M + 31) / 32);
         double wk = 1;
         while (wk < 8 && blocks * rows * wk < kWavesWanted && 2 * wk <= ku) wk *= 2;

@@ -1,10 +1,11 @@
 // Experts' gated products over 4-bit weights: for each token t and slot j with
 // expert e = idx[t][j],
 //   y[t] = sum_j weight[t][j] * down_e( silu(gate_e x_t) * (up_e x_t) ),
-// slots whose idx is outside 0 .. E-1 dropped.  Four launches: the plan (slots
-// sorted by expert, and the list of row tiles), the gate and up products with
-// silu(g) u in their epilogue, the down product times the slot's weight, and the
-// sum of each token's slots in slot order.
+// slots whose idx is outside 0 .. E-1 dropped.  With many slots four launches (and one
+// for x as f16 planes): the plan (slots sorted by expert, and the list of row tiles), the
+// gate and up products with silu(g) u in their epilogue, the down product times the
+// slot's weight, and the sum of each token's slots in slot order.  With fewer, three
+// without the plan, with a few two; moe_plan says when.
 #include "q4_group.h"
 #include "q4_row.h"
 #include "q4_tiled.h"
@@ -74,17 +75,18 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(const int32_t *idx, int 
 template <int DT>
 __global__ __launch_bounds__(256) void moe_sum_kernel(const float *part, const int32_t *idx, void *y, int64_t T, int k,
                                                       int E, int d) {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= T * d) return;
-    const int64_t t = i / d;
-    const int n = (int)(i % d);
-    f4 v = {};
-    for (int j = 0; j < k; ++j) {
-        const int e = idx[t * k + j];
-        if (e >= 0 && e < E) v += *reinterpret_cast<const f4 *>(part + (t * k + j) * d + n);
-    }
+    const int64_t step = (int64_t)gridDim.x * 1024;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < T * d; i += step) {
+        const int64_t t = i / d;
+        const int n = (int)(i % d);
+        f4 v = {};
+        for (int j = 0; j < k; ++j) {
+            const int e = idx[t * k + j];
+            if (e >= 0 && e < E) v += *reinterpret_cast<const f4 *>(part + (t * k + j) * d + n);
+        }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) store_from_float<DT>(y, i + q, v[q]);
+        for (int q = 0; q < 4; ++q) store_from_float<DT>(y, i + q, v[q]);
+    }
 }
 
 template <int XT, int MODE>
@@ -128,7 +130,8 @@ hipError_t direct(const MoePlan &p, const void *x, const int32_t *idx, const flo
 
 template <int DT>
 void launch_sum(const float *part, const int32_t *idx, void *y, int64_t T, int64_t k, int E, int d, hipStream_t s) {
-    moe_sum_kernel<DT><<<dim3((unsigned)((T * d / 4 + 255) / 256)), dim3(256), 0, s>>>(part, idx, y, T, (int)k, E, d);
+    const int64_t blocks = (T * d / 4 + 255) / 256, most = (int64_t)1 << 20;
+    moe_sum_kernel<DT><<<dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, s>>>(part, idx, y, T, (int)k, E, d);
 }
 
 hipError_t sum(const float *part, const int32_t *idx, void *y, int64_t T, int64_t k, int E, int d, int dtype, hipStream_t s) {

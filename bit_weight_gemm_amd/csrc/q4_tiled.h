@@ -314,14 +314,14 @@ inline hipError_t run_q4_tiled(Q4TArgs a, int64_t tiles_m, hipStream_t s) {
 // x as f16 planes (see q4_tiled.hip).
 struct Q4Prep {
     const void *x;
-    int64_t rows;
+    int64_t row0, rows;      // row0: of the launch
     int K;
     int64_t lda, plane;      // of the planes (elements)
     _Float16 *out;           // nullptr: only norm_exp (f16 x used as it is)
     float *rowscale;
     int32_t *norm_exp;       // or nullptr
 };
-hipError_t launch_q4_prep(const Q4Prep &p, int dtype, hipStream_t s);
+hipError_t launch_q4_prep(Q4Prep p, int dtype, hipStream_t s);
 // Whether x is read as it is: f16 rows of whole units.
 inline bool q4_plain_x(int64_t K, int dtype) { return dtype == kF16 && K % 128 == 0; }
 inline int q4_planes(int dtype) { return dtype == kF32 ? 2 : 1; }

@@ -13,7 +13,7 @@ namespace {
 template <int DT, int P>
 __global__ __launch_bounds__(256) void q4_prep_kernel(Q4Prep p) {
     const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t row = p.row0 + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (row >= p.rows) return;
     constexpr int V = DT == kF32 ? 4 : 8;  // elements of a 16-byte piece
     auto piece = [&](int i, float *v) {    // K is a multiple of 32: whole pieces
@@ -137,11 +137,15 @@ hipError_t grouped(const Q4TArgs &a, int planes, int bm, int64_t tiles, hipStrea
 
 }  // namespace
 
-hipError_t launch_q4_prep(const Q4Prep &p, int dtype, hipStream_t s) {
-    const dim3 grid((unsigned)((p.rows + 3) / 4)), block(256);
-    if (dtype == kF32) q4_prep_kernel<kF32, 2><<<grid, block, 0, s>>>(p);
-    else if (dtype == kF16) q4_prep_kernel<kF16, 1><<<grid, block, 0, s>>>(p);
-    else q4_prep_kernel<kBF16, 1><<<grid, block, 0, s>>>(p);
+hipError_t launch_q4_prep(Q4Prep p, int dtype, hipStream_t s) {
+    constexpr int64_t kMost = (int64_t)1 << 25;  // rows of one launch: fewer than 2^32 work items, 64 a row
+    for (p.row0 = 0; p.row0 < p.rows; p.row0 += kMost) {
+        const int64_t n = p.rows - p.row0 < kMost ? p.rows - p.row0 : kMost;
+        const dim3 grid((unsigned)((n + 3) / 4)), block(256);
+        if (dtype == kF32) q4_prep_kernel<kF32, 2><<<grid, block, 0, s>>>(p);
+        else if (dtype == kF16) q4_prep_kernel<kF16, 1><<<grid, block, 0, s>>>(p);
+        else q4_prep_kernel<kBF16, 1><<<grid, block, 0, s>>>(p);
+    }
     return hipGetLastError();
 }
 

@@ -35,14 +35,15 @@ size_t q4_packed_size(int64_t E, int64_t N, int64_t K, int64_t G, int zeros);
 /* Packs codes u8 [E][N][K/2] (element 2j in the low four bits of byte j, 2j+1 in the
  * high ones; 4-byte aligned), scales f16 [E][N][K/G] and zeros u8 [E][N][K/G] (NULL
  * exactly when w->zeros is 0), all in device memory, into w->data.  Scales are taken
- * as they are: an infinite or NaN one gives such weights. */
+ * as they are: an infinite or NaN one gives such weights, and products with them are
+ * infinite or NaN (which of the two may depend on the number of rows). */
 int q4_pack(const q4_weight *w, const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, void *stream);
 
 /* w_out[e][n][k] = (code - zero) * scale as f32, exact. */
 int q4_dequant(const q4_weight *w, float *w_out, void *stream);
 
 /* Bytes of device workspace that q4_gemm needs for these sizes (0: none, as for up to
- * 16 rows; also 0 on bad sizes). */
+ * 32 rows; also 0 on bad sizes). */
 size_t q4_gemm_workspace_size(const q4_weight *w, int64_t M, int dtype);
 
 /* y[m][n] = sum_k x[m][k] * W[n][k] for a weight with E == 1.  x [M][K] and y [M][N]
