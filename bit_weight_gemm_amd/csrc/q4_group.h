@@ -41,24 +41,6 @@ __global__ __launch_bounds__(512, 4) void q4_group_kernel(Q4GroupArgs p) {
     const int K = p.w.K, ku = p.w.ku, kp = ku * 128, e = blockIdx.y;
     const uint32_t magic = f16_magic();
 
-    // the expert's slots, in order
-    int count = 0;
-    for (int s0 = 0; s0 < p.slots; s0 += 512) {
-        const bool mine = s0 + tid < p.slots && p.idx[s0 + tid] == e;
-        const uint64_t who = __ballot(mine);
-        if (lane == 0) wcount[wave] = __popcll(who);
-        __syncthreads();
-        int at = count;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            if (q < wave) at += wcount[q];
-            count += wcount[q];
-        }
-        if (mine) list[at + __popcll(who & ((1ull << lane) - 1))] = (uint16_t)(s0 + tid);
-        __syncthreads();
-    }
-    if (count == 0) return;  // the whole workgroup
-
     const int step = 1 << p.log_wk, wk = wave & (step - 1), wn = wave >> p.log_wk, cols = (8 >> p.log_wk) * NC;
     const w4 *cp[CB];
     const uint16_t *sp[CB];
@@ -87,11 +69,35 @@ __global__ __launch_bounds__(512, 4) void q4_group_kernel(Q4GroupArgs p) {
     };
     const int n = (ku - wk + step - 1) >> p.log_wk;  // this wave's units: wk, wk + step, ...
 
-    for (int c0 = 0; c0 < count; c0 += ROWS) {
-        const int rows = count - c0 < ROWS ? count - c0 : ROWS;
+    // the first units' codes are on their way while the slots are found
+    auto first_units = [&] {
 #pragma unroll
         for (int st = 0; st < D; ++st)
             if (st < n) load(st, wk + step * st);
+    };
+    first_units();
+
+    // the expert's slots, in order
+    int count = 0;
+    for (int s0 = 0; s0 < p.slots; s0 += 512) {
+        const bool mine = s0 + tid < p.slots && p.idx[s0 + tid] == e;
+        const uint64_t who = __ballot(mine);
+        if (lane == 0) wcount[wave] = __popcll(who);
+        __syncthreads();
+        int at = count;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (q < wave) at += wcount[q];
+            count += wcount[q];
+        }
+        if (mine) list[at + __popcll(who & ((1ull << lane) - 1))] = (uint16_t)(s0 + tid);
+        __syncthreads();
+    }
+    if (count == 0) return;  // the whole workgroup
+
+    for (int c0 = 0; c0 < count; c0 += ROWS) {
+        const int rows = count - c0 < ROWS ? count - c0 : ROWS;
+        if (c0 > 0) first_units();
 
         // every wave brings its share of the rows to LDS; those past the last hold zeros
 #pragma unroll 1
