@@ -1,9 +1,10 @@
 // Experts' products with few rows each: a workgroup finds its expert's slots by itself.
 //
-// Workgroup (x, e) of eight waves looks through the T*k chosen experts for e, and takes
-// e's slots 16 rows at a time: it brings their rows to LDS as f16 planes (f16 rows as they are;
-// bfloat16 and f32 rows, whole in a wave's registers, under a power of two per row
-// as q4_prep_kernel makes them), and its waves multiply them with CB column blocks each.
+// Workgroup (x, e, z) of eight waves looks through the T*k chosen experts for e, and takes
+// e's slots 16 rows at a time, the z-th of them in turn: it brings their rows to LDS as f16
+// planes (f16 rows as they are; bfloat16 and f32 rows, whole in a wave's registers, under a
+// power of two per row as q4_prep_kernel makes them), and its waves multiply them with CB
+// column blocks each.
 // WK waves share a column block and take its units in turn; their sums are added in wave order.
 // Only codes and scales wait in registers, D units ahead: these products wait for
 // memory.  Codes are decoded to code - zero, exact in f16, and each group's sum is scaled in f32.
@@ -75,7 +76,7 @@ __global__ __launch_bounds__(512, 4) void q4_group_kernel(Q4GroupArgs p) {
         for (int st = 0; st < D; ++st)
             if (st < n) load(st, wk + step * st);
     };
-    first_units();
+    if (blockIdx.z == 0) first_units();
 
     // the expert's slots, in order
     int count = 0;
@@ -93,11 +94,11 @@ __global__ __launch_bounds__(512, 4) void q4_group_kernel(Q4GroupArgs p) {
         if (mine) list[at + __popcll(who & ((1ull << lane) - 1))] = (uint16_t)(s0 + tid);
         __syncthreads();
     }
-    if (count == 0) return;  // the whole workgroup
+    if (count <= (int)blockIdx.z * ROWS) return;  // the whole workgroup
 
-    for (int c0 = 0; c0 < count; c0 += ROWS) {
+    for (int c0 = blockIdx.z * ROWS; c0 < count; c0 += ROWS * gridDim.z) {
         const int rows = count - c0 < ROWS ? count - c0 : ROWS;
-        if (c0 > 0) first_units();
+        if (c0 > 0) first_units();  // (the first sixteen rows': above)
 
         // every wave brings its share of the rows to LDS; those past the last hold zeros
 #pragma unroll 1
@@ -264,8 +265,11 @@ inline hipError_t run_q4_group(Q4GroupArgs a, hipStream_t s) {
     const int64_t busy = a.w.E < a.slots ? a.w.E : a.slots;
     while (a.log_wk < 3 && (blocks * busy << a.log_wk) < 2048 && (2 << a.log_wk) <= a.w.ku) ++a.log_wk;
     const int64_t wn = 8 >> a.log_wk;
+    // popular experts' blocks of 16 rows go side by side (64 tokens of 32 experts, 4 each: 55 -> 42 us;
+    // 24 of 64, 8 each, the few blocks past the first do not pay for the workgroups: 77 -> 83)
+    const unsigned z = a.slots > 4 * a.w.E ? 3 : 1;
     q4_group_kernel<DT, P, G, CB, D, MODE>
-        <<<dim3((unsigned)((blocks + wn - 1) / wn), (unsigned)a.w.E), dim3(512), q4_group_lds(a.w.K, P, 16), s>>>(a);
+        <<<dim3((unsigned)((blocks + wn - 1) / wn), (unsigned)a.w.E, z), dim3(512), q4_group_lds(a.w.K, P, 16), s>>>(a);
     return hipGetLastError();
 }
 

@@ -213,16 +213,18 @@ hipError_t tiled(const MoePlan &p, const void *x, const float *weights, const Q4
 
 }  // namespace
 
-// Up to kDirectSlots slots, each reads its expert's weights for itself; their rows have to fit in LDS.
+// Up to kDirectSlots slots, or up to kDirectSpread while that is no more than one per expert, each reads its
+// expert's weights for itself; their rows have to fit in LDS.  (64 experts, 8 each, 2048 x 1024: 40 slots 39 us,
+// found by their expert's workgroups 50, 64 slots 55 and 65; of 8 experts, 48 slots 28 and 22.)
 // Beyond, by slots per expert (bf16; 64 experts of 8, 2048 x 1024: "large", 8 experts of 2, 1024 x 1024:
 // "small", which tiles of the gate product cannot fill the 256 compute units with):
-//   up to 8 (4 if small): workgroups find their slots (large, 33 tokens: 88 us, tiles of 64 rows
-//     106; small, 33 tokens: 30, rows of 16 24);
+//   up to 8 (4 if small): workgroups find their slots (large, 64 tokens: 101 us, tiles of 64 rows
+//     110; small, 33 tokens: 30, rows of 16 24);
 //   up to 48, small: plan and blocks of 16 rows (128 tokens 39, tiles of 64 43, of 32-row blocks 36);
 //   then tiles of 64 rows (large, 100 tokens: 116, found slots 139; 256 tokens 135, rows of 32 240;
 //     small, 256 tokens 45, rows of 16 60);
 //   from 256 on tiles of 128 (large, 2048 tokens: 399, of 64 414; f32 629, of 64 591: not for f32).
-constexpr int64_t kDirectSlots = 32;
+constexpr int64_t kDirectSlots = 32, kDirectSpread = 64;
 constexpr size_t kDirectLds = 48 * 1024;
 
 MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtype) {
@@ -231,7 +233,7 @@ MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtyp
     const bool plain = q4_plain_x(d, dtype), f32 = dtype == kF32;
     p.slots = T * k;
     p.ldx = (d + 127) / 128 * 128, p.ldh = (f + 127) / 128 * 128;
-    p.direct = p.slots <= kDirectSlots && q4_row_lds(p.ldx / 128, f32 ? 3 : 1) <= kDirectLds &&
+    p.direct = p.slots <= (E < kDirectSlots ? kDirectSlots : E < kDirectSpread ? E : kDirectSpread) && q4_row_lds(p.ldx / 128, f32 ? 3 : 1) <= kDirectLds &&
                q4_row_lds(k * (p.ldh / 128), f32 ? 3 : 2) <= kDirectLds;
     const bool fills = E * ((f + 127) / 128) >= 256;
     const int64_t few = fills ? 8 * E : 4 * E;
