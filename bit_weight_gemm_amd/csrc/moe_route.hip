@@ -23,6 +23,10 @@
 // its experts, so a group's best keys are found in its own lanes.  Keys are compared as
 // integers that order like them: a wave maximum is then six DPP instructions, and a pass
 // for one slot about thirty.
+//
+// Bound by instruction issue: 16384 tokens x 256 experts, 8 groups of which 4 stay, bias, 8 chosen:
+// 25 us of kernel (0.7 TB/s), some 600 vector instructions a token; one token 4.7 us, of which an
+// empty launch is two.  The gradient reads and writes its rows once: 8192 x 128 f32 4.4 us (2 TB/s).
 #include "q4.h"
 
 namespace tq2 {

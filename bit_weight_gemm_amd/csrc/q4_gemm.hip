@@ -15,6 +15,8 @@ __global__ __launch_bounds__(1024) void q4_head_kernel(uint32_t *head, int E) {
 // and hands word c to lane (r, c) as its word h; the first 16 lanes also bring their
 // row's scales and zeros.  The head collects each expert's largest |scale| (integer
 // maximum: the order does not matter), which a wave adds to only where it is larger.
+// Done once per weight, before its use: 4096 x 4096 13-21 us, 64 x 2048 x 1024 180 us, 0.8 TB/s
+// read and written: a lane's rows lie K/2 bytes apart, and scales come two bytes at a time.
 __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros,
                                                       Q4View v, w4 *oc, uint16_t *os, uint8_t *oz, uint32_t *head) {
     __shared__ uint32_t words[4][16][4][4 + 1];  // [wave][r][h of the reader][word]
