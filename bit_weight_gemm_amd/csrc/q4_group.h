@@ -3,7 +3,7 @@
 // Workgroup (x, e, z) of eight waves looks through the T*k chosen experts for e, and takes
 // e's slots 16 rows at a time, the z-th of them in turn: it brings their rows to LDS as f16
 // planes (f16 rows as they are; bfloat16 and f32 rows, whole in a wave's registers, under a
-// power of two per row as q4_prep_kernel makes them), and its waves multiply them with CB
+// power of two per row as q4_prep.h makes them), and its waves multiply them with CB
 // column blocks each.
 // WK waves share a column block and take its units in turn; their sums are added in wave order.
 // Only codes and scales wait in registers, D units ahead: these products wait for

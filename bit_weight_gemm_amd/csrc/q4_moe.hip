@@ -1,14 +1,14 @@
 // Experts' gated products over 4-bit weights: for each token t and slot j with
 // expert e = idx[t][j],
 //   y[t] = sum_j weight[t][j] * down_e( silu(gate_e x_t) * (up_e x_t) ),
-// slots whose idx is outside 0 .. E-1 dropped.  With many slots four launches (and one
-// for x as f16 planes): the plan (slots sorted by expert, and the list of row tiles), the
+// slots whose idx is outside 0 .. E-1 dropped.  With many slots four launches: the plan
+// (slots sorted by expert, and the list of row tiles; beside it x as f16 planes), the
 // gate and up products with silu(g) u in their epilogue, the down product times the
 // slot's weight, and the sum of each token's slots in slot order.  With fewer, three
 // without the plan, with a few two; moe_plan says when.
 #include "q4_group.h"
+#include "q4_prep.h"
 #include "q4_row.h"
-#include "q4_tiled.h"
 
 namespace tq2 {
 
@@ -21,8 +21,15 @@ constexpr int kMaxExperts = 1024;
 // within an expert may differ from call to call, but a slot's products do not
 // depend on its place, and the sum over slots goes by slot, so results are the
 // same bits.
+// The other workgroups bring x's rows to f16 planes meanwhile (sixteen rows each; none if x.rows is 0).
+template <int DT, int P>
 __global__ __launch_bounds__(1024) void moe_plan_kernel(const int32_t *idx, int slots, int E, int tile_rows,
-                                                        int32_t *order, int4 *tiles, int32_t *ntiles) {
+                                                        int32_t *order, int4 *tiles, int32_t *ntiles, Q4Prep x) {
+    if (blockIdx.x > 0) {
+        const int64_t row = (int64_t)(blockIdx.x - 1) * 16 + (threadIdx.x >> 6);
+        if (row < x.rows) q4_prep_row<DT, P>(x, row);
+        return;
+    }
     __shared__ int cnt[kMaxExperts], base[kMaxExperts], tbase[kMaxExperts];
     const int tid = threadIdx.x;
     for (int e = tid; e < E; e += 1024) cnt[e] = 0;
@@ -182,23 +189,16 @@ hipError_t skinny(const MoePlan &p, const void *x, const float *weights, const Q
 // row: half a step of f16 (2^-11) in front of a sum over f, as much as the result's own
 // rounding for f16 and an eighth of it for bfloat16; f32 h goes through f32 and two planes.
 hipError_t tiled(const MoePlan &p, const void *x, const float *weights, const Q4View &gate, const Q4View &up,
-                 const Q4View &down, int64_t T, int64_t k, int dtype, char *b, hipStream_t s) {
+                 const Q4View &down, const Q4Prep &px, int64_t k, int dtype, char *b, hipStream_t s) {
     const int planes = q4_planes(dtype), bm = (int)p.tile_rows;
     const bool plain = q4_plain_x(gate.K, dtype);
-    Q4Prep px{};
-    px.x = x, px.rows = T, px.K = gate.K, px.lda = p.ldx, px.plane = T * p.ldx;
-    px.out = plain ? nullptr : reinterpret_cast<_Float16 *>(b + p.off_x);
-    px.rowscale = reinterpret_cast<float *>(b + p.off_xscale);
-    px.norm_exp = reinterpret_cast<int32_t *>(b + p.off_xnorm);
-    hipError_t e = launch_q4_prep(px, dtype, s);
-    if (e != hipSuccess) return e;
     Q4TArgs g{};
     g.w = gate, g.w2 = up, g.topk = (int)k, g.weights = weights, g.y = b + p.off_h, g.ldh = p.ldh;
     g.ntiles = reinterpret_cast<const int32_t *>(b), g.order = reinterpret_cast<const int32_t *>(b + p.off_order);
     g.tiles = reinterpret_cast<const int4 *>(b + p.off_tiles);
     g.a = plain ? static_cast<const _Float16 *>(x) : px.out, g.lda = plain ? gate.K : px.lda, g.plane = px.plane;
     g.rowscale = px.rowscale, g.norm_exp = px.norm_exp, g.hscale = reinterpret_cast<float *>(b + p.off_hscale);
-    e = launch_q4_tiled_gate_up(g, planes, bm, p.max_tiles, s);
+    hipError_t e = launch_q4_tiled_gate_up(g, planes, bm, p.max_tiles, s);
     if (e != hipSuccess) return e;
     Q4TArgs d = g;
     d.w = down, d.y = b + p.off_part, d.rowscale = g.hscale, d.lda = p.ldh, d.plane = p.slots * p.ldh;
@@ -275,10 +275,21 @@ hipError_t launch_q4_moe(const MoePlan &p, const void *x, const int32_t *idx, co
     int32_t *ntiles = reinterpret_cast<int32_t *>(b), *order = reinterpret_cast<int32_t *>(b + p.off_order);
     int4 *tiles = reinterpret_cast<int4 *>(b + p.off_tiles);
     const float *part = reinterpret_cast<const float *>(b + p.off_part);
-    moe_plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(idx, (int)p.slots, gate.E, (int)p.tile_rows, order, tiles, ntiles);
+    Q4Prep px{};
+    if (p.tiled) {
+        px.x = x, px.rows = T, px.K = gate.K, px.lda = p.ldx, px.plane = T * p.ldx;
+        px.out = q4_plain_x(gate.K, dtype) ? nullptr : reinterpret_cast<_Float16 *>(b + p.off_x);
+        px.rowscale = reinterpret_cast<float *>(b + p.off_xscale);
+        px.norm_exp = reinterpret_cast<int32_t *>(b + p.off_xnorm);
+    }
+    const dim3 grid(1 + (unsigned)((px.rows + 15) / 16)), block(1024);
+    const int slots = (int)p.slots, rows = (int)p.tile_rows;
+    if (dtype == kF32) moe_plan_kernel<kF32, 2><<<grid, block, 0, s>>>(idx, slots, gate.E, rows, order, tiles, ntiles, px);
+    else if (dtype == kF16) moe_plan_kernel<kF16, 1><<<grid, block, 0, s>>>(idx, slots, gate.E, rows, order, tiles, ntiles, px);
+    else moe_plan_kernel<kBF16, 1><<<grid, block, 0, s>>>(idx, slots, gate.E, rows, order, tiles, ntiles, px);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    e = p.tiled ? tiled(p, x, weights, gate, up, down, T, k, dtype, b, s) : skinny(p, x, weights, gate, up, down, k, dtype, b, s);
+    e = p.tiled ? tiled(p, x, weights, gate, up, down, px, k, dtype, b, s) : skinny(p, x, weights, gate, up, down, k, dtype, b, s);
     if (e != hipSuccess) return e;
     return sum(part, idx, y, T, k, gate.E, down.N, dtype, s);
 }

@@ -10,7 +10,7 @@
 //
 // The codes are decoded to code - zero, exact in f16, and each group's sum is scaled in f32:
 // acc += scale * part.  Products are exact for f16 x.  bfloat16 rows are
-// brought to f16 by a power of two per row (their 8 bits fit; see q4_prep_kernel), and f32 rows
+// brought to f16 by a power of two per row (their 8 bits fit; see q4_prep.h), and f32 rows
 // to two f16 parts.
 //
 // Bound by the matrix unit and the waits around it: 2048 x 4096 x 4096, G = 128, bf16 takes 71-76
@@ -317,7 +317,7 @@ inline hipError_t run_q4_tiled(Q4TArgs a, int64_t tiles_m, hipStream_t s) {
     return hipGetLastError();
 }
 
-// x as f16 planes (see q4_tiled.hip).
+// x as f16 planes (see q4_prep.h).
 struct Q4Prep {
     const void *x;
     int64_t row0, rows;      // row0: of the launch

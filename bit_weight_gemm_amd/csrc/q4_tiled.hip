@@ -1,108 +1,14 @@
 // Launches of the tiled 4-bit products, and x as f16 planes for them.
-#include "q4_tiled.h"
+#include "q4_prep.h"
 
 namespace tq2 {
 
 namespace {
 
-// One wave per row.  bfloat16 and f32 rows are multiplied by the power of two that
-// brings their largest finite value into [2^14, 2^15): bfloat16's 8 bits are then exact
-// in f16 down to 2^-32 of the row's largest value, and below that the error is at most 2^-40 of
-// it, sixteen bits under the f32 sums' own (2048 x 4096 bf16: 7-9 us, 3.7-4.8 TB/s, as a copy).  f32 rows become hi + lo: 22 bits, the sum of
-// two f16 parts, with the same floor.  Past K up to whole units the planes hold zeros.
 template <int DT, int P>
 __global__ __launch_bounds__(256) void q4_prep_kernel(Q4Prep p) {
-    const int lane = threadIdx.x & 63;
     const int64_t row = p.row0 + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= p.rows) return;
-    constexpr int V = DT == kF32 ? 4 : 8;  // elements of a 16-byte piece
-    auto piece = [&](int i, float *v) {    // K is a multiple of 32: whole pieces
-        const int64_t at = row * p.K + (int64_t)i * V;
-        if constexpr (DT == kF32) {
-            const f4 x = *reinterpret_cast<const f4 *>(static_cast<const float *>(p.x) + at);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = x[q];
-        } else {
-            const w4 x = *reinterpret_cast<const w4 *>(static_cast<const uint16_t *>(p.x) + at);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if constexpr (DT == kBF16) {
-                    v[2 * q] = __builtin_bit_cast(float, x[q] << 16);
-                    v[2 * q + 1] = __builtin_bit_cast(float, x[q] & 0xffff0000u);
-                } else {
-                    v[2 * q] = half_bits(x[q]);
-                    v[2 * q + 1] = half_bits(x[q] >> 16);
-                }
-            }
-        }
-    };
-    const int pieces = p.K / V;
-    // the first kHold pieces of a lane stay in registers between the two passes
-    constexpr int kHold = 8;
-    float held[DT == kF16 ? 1 : kHold][V];
-    int shift = 0;
-    if constexpr (DT != kF16) {
-        float most = 0.0f;
-        auto look = [&](const float *v) {
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float a = __builtin_fabsf(v[q]);
-                most = a > most && a < __builtin_inff() ? a : most;
-            }
-        };
-#pragma unroll
-        for (int c = 0; c < kHold; ++c) {
-#pragma unroll
-            for (int q = 0; q < V; ++q) held[c][q] = 0.0f;
-            if (lane + 64 * c < pieces) piece(lane + 64 * c, held[c]);
-        }
-#pragma unroll
-        for (int c = 0; c < kHold; ++c) look(held[c]);
-        for (int i = lane + 64 * kHold; i < pieces; i += 64) {
-            float v[V];
-            piece(i, v);
-            look(v);
-        }
-        for (int o = 1; o < 64; o <<= 1) most = fmaxf(most, __shfl_xor(most, o));
-        shift = q4_row_shift(most);
-    }
-    float norm = 0.0f;
-    const int padded = (int)(p.lda / V);
-    auto put = [&](int i, const float *v) {
-        typedef _Float16 hv __attribute__((ext_vector_type(V)));
-        hv a, b;
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-            const float x = DT == kF16 ? v[q] : __builtin_ldexpf(v[q], shift);
-            norm += x * x;
-            a[q] = (_Float16)x;
-            if constexpr (P == 2) b[q] = __builtin_isfinite(x) ? (_Float16)(x - (float)a[q]) : (_Float16)0.0f;
-        }
-        if (!p.out) return;
-        *reinterpret_cast<hv *>(p.out + row * p.lda + (int64_t)i * V) = a;
-        if constexpr (P == 2) *reinterpret_cast<hv *>(p.out + p.plane + row * p.lda + (int64_t)i * V) = b;
-    };
-    constexpr int kFrom = DT == kF16 ? 0 : kHold;
-    if constexpr (DT != kF16) {
-#pragma unroll
-        for (int c = 0; c < kHold; ++c)
-            if (lane + 64 * c < padded) put(lane + 64 * c, held[c]);
-    }
-    for (int i = lane + 64 * kFrom; i < padded; i += 64) {
-        float v[V] = {};
-        if (i < pieces) piece(i, v);
-        put(i, v);
-    }
-    if (p.rowscale && lane == 0) p.rowscale[row] = __builtin_ldexpf(1.0f, -shift);
-    if (p.norm_exp) {
-        for (int o = 1; o < 64; o <<= 1) norm += __shfl_xor(norm, o);
-        int e = -200;
-        if (norm > 0.0f && norm < __builtin_inff()) {
-            (void)__builtin_frexpf(norm, &e);
-            e += 1 - 2 * shift;  // one more for the sum's own rounding
-        }
-        if (lane == 0) p.norm_exp[row] = e;
-    }
+    if (row < p.rows) q4_prep_row<DT, P>(p, row);
 }
 
 // y = the sum of the shares' sums, in their order.

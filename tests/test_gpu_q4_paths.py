@@ -56,6 +56,21 @@ def test_gemm_deals_infinities_stay_in_their_rows(m):
     assert (y[0] == float("inf")).all() and torch.isnan(y[m - 1]).all() and torch.isfinite(y[1: m - 1]).all()
 
 
+@pytest.mark.parametrize("m", [1, 20, 64, 260, 1200])
+def test_gemm_subnormal_activations_are_exact(m):
+    """f16 rows with one subnormal value each: every output is a small multiple of 2^-15, without any rounding."""
+    n, k = 1040, 1024
+    codes, scales, zeros = weight(39, (), n, k, 64, True)
+    scales = torch.full_like(scales, 512.0)
+    x = torch.zeros((m, k))
+    at = torch.arange(m) * 7 % k
+    x[torch.arange(m), at] = (1 + torch.arange(m) % 5) * 2.0 ** -24
+    note(f"[q4_gemm] subnormal x M={m}")
+    y = run(x.half().cuda(), (codes, scales, zeros), "f16")
+    want = x.double()[torch.arange(m), at][:, None] * dequant64(codes, scales, zeros).T[at]
+    assert torch.equal(y.cpu().double(), want)
+
+
 def test_gemm_rows_past_32_bits():
     """Rows whose byte offsets (x, and x as f16 planes) pass 2^32."""
     m, n, k = 66000, 64, 32768
@@ -73,7 +88,8 @@ def test_gemm_rows_past_32_bits():
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("t,e,k,d,f,group", [(50, 64, 8, 128, 512, 128), (70, 64, 8, 160, 512, 32), (300, 64, 8, 128, 512, 64),
-                                             (40, 8, 4, 2176, 128, 128), (30, 4, 1, 2048, 64, 64), (90, 3, 3, 96, 320, 32)])
+                                             (40, 8, 4, 2176, 128, 128), (25, 16, 2, 2048, 64, 64), (25, 16, 2, 64, 2048, 64),
+                                             (90, 3, 3, 96, 320, 32)])
 def test_moe_deals(t, e, k, d, f, group, dtype):
     """Slots that workgroups find, tiles of 64 and blocks of 16 rows; rows longer than a wave's registers."""
     check_moe(t, e, k, d, f, group, True, dtype, "deals", seed=90)
