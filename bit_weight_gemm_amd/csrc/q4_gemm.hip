@@ -6,26 +6,51 @@ namespace tq2 {
 
 namespace {
 
-__global__ __launch_bounds__(1024) void q4_head_kernel(uint32_t *head, int E) {
+__global__ __launch_bounds__(1024) void q4_zero_head_kernel(uint32_t *head, int E) {
     if ((int)threadIdx.x < E) head[threadIdx.x] = 0;
+}
+
+// The largest |scale| of each expert (blockIdx.y) over its packed scales, `eights` pieces of
+// eight, by gridDim.x workgroups.  Halves without their sign order as integers do.
+__global__ __launch_bounds__(1024) void q4_head_kernel(const uint16_t *scales, int64_t eights, uint32_t *head) {
+    __shared__ uint32_t red[16];
+    const w4 *p = reinterpret_cast<const w4 *>(scales) + blockIdx.y * eights;
+    uint32_t most = 0;
+    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < eights; i += (int64_t)gridDim.x * 1024) {
+        const w4 v = p[i];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t lo = v[q] & 0x7fffu, hi = (v[q] >> 16) & 0x7fffu, m = lo > hi ? lo : hi;
+            most = m > most ? m : most;
+        }
+    }
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t b = (uint32_t)__shfl_xor((int)most, o);
+        most = b > most ? b : most;
+    }
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = most;
+    __syncthreads();
+    if (threadIdx.x > 0) return;
+    for (int q = 1; q < 16; ++q) most = red[q] > most ? red[q] : most;
+    const uint32_t bits = __builtin_bit_cast(uint32_t, half_bits(most));
+    if (gridDim.x == 1) head[blockIdx.y] = bits;
+    else atomicMax(&head[blockIdx.y], bits);
 }
 
 // One workgroup per block of 16 rows of an expert, its four waves taking the units in
 // turn.  Lane (r, h) reads 16 bytes of row r (k = 128u + 32h .. +31), orders the nibbles
 // and hands word c to lane (r, c) as its word h; the first 16 lanes also bring their
-// row's scales and zeros.  The head collects each expert's largest |scale| (integer
-// maximum: the order does not matter), which a wave adds to only where it is larger.
-// Done once per weight, before its use: 4096 x 4096 13-21 us, 64 x 2048 x 1024 180 us, 0.8 TB/s
-// read and written: a lane's rows lie K/2 bytes apart, and scales come two bytes at a time.
+// row's scales and zeros.
+// Done once per weight, before its use: 4096 x 4096 11 us, 64 x 2048 x 1024 30 us, 4.6 TB/s
+// read and written, as a copy.
 __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros,
-                                                      Q4View v, w4 *oc, uint16_t *os, uint8_t *oz, uint32_t *head) {
+                                                      Q4View v, w4 *oc, uint16_t *os, uint8_t *oz) {
     __shared__ uint32_t words[4][16][4][4 + 1];  // [wave][r][h of the reader][word]
     const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4, wave = threadIdx.x >> 6;
     const int nb = blockIdx.x, e = blockIdx.y;
     const int n = nb * 16 + r;
     const int64_t row = (int64_t)e * v.N + n, unit0 = ((int64_t)e * v.nb + nb) * v.ku;
     const int gpu = 128 / v.G, kg = v.K / v.G;
-    uint32_t most = 0;
     for (int u0 = 0; u0 < v.ku; u0 += 4) {
         const int u = u0 + wave;
         const int k = u * 128 + 32 * h;  // K is a multiple of 32: whole pieces
@@ -49,20 +74,12 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t *codes, cons
                 for (int g = 0; g < gpu; ++g) {
                     const int at = u * gpu + g;
                     const bool has = n < v.N && at < kg;
-                    const uint16_t s = has ? scales[row * kg + at] : 0;
-                    os[((unit0 + u) * 16 + r) * gpu + g] = s;
+                    os[((unit0 + u) * 16 + r) * gpu + g] = has ? scales[row * kg + at] : 0;
                     if (oz) oz[((unit0 + u) * 16 + r) * gpu + g] = has ? zeros[row * kg + at] : 8;
-                    const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_fabsf(half_bits(s)));
-                    most = a > most ? a : most;
                 }
         }
         __syncthreads();
     }
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t b = (uint32_t)__shfl_xor((int)most, o);
-        most = b > most ? b : most;
-    }
-    if (lane == 0 && most > *const_cast<volatile uint32_t *>(&head[e])) atomicMax(&head[e], most);
 }
 
 __global__ __launch_bounds__(256) void q4_dequant_kernel(Q4View v, float *out) {
@@ -103,10 +120,14 @@ hipError_t dense_g(const Q4Args &a, hipStream_t s) {
 hipError_t launch_q4_pack(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, const Q4View &v,
                           hipStream_t s) {
     uint32_t *head = const_cast<uint32_t *>(v.head);
-    q4_head_kernel<<<dim3(1), dim3(1024), 0, s>>>(head, v.E);
     q4_pack_kernel<<<dim3((unsigned)v.nb, (unsigned)v.E), dim3(256), 0, s>>>(
         codes, scales, zeros, v, const_cast<w4 *>(v.codes), const_cast<uint16_t *>(v.scales),
-        const_cast<uint8_t *>(v.zeros), head);
+        const_cast<uint8_t *>(v.zeros));
+    // (an atomic of every workgroup of the packing took most of its time: 64 x 2048 x 1024 180-220 us)
+    const int64_t eights = (int64_t)v.nb * v.ku * 2 * (128 / v.G), shares = (eights + 16383) / 16384;
+    const unsigned x = (unsigned)(shares < 64 ? shares : 64);
+    if (x > 1) q4_zero_head_kernel<<<dim3(1), dim3(1024), 0, s>>>(head, v.E);
+    q4_head_kernel<<<dim3(x, (unsigned)v.E), dim3(1024), 0, s>>>(v.scales, eights, head);
     return hipGetLastError();
 }
 

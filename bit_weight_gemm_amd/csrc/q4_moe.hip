@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kMaxExperts = 1024;
 
-// One workgroup (16384 slots: 11.6 us, bound by its one compute unit's atomics and the two passes' latency).
+// One workgroup (16384 slots: 13 us beside the planes of 2048 rows, alone 11.6, bound by its one compute unit's atomics and the two passes' latency).
 // Counts and places come from LDS atomics: the order of slots
 // within an expert may differ from call to call, but a slot's products do not
 // depend on its place, and the sum over slots goes by slot, so results are the

@@ -13,9 +13,9 @@
 // brought to f16 by a power of two per row (their 8 bits fit; see q4_prep.h), and f32 rows
 // to two f16 parts.
 //
-// Bound by the matrix unit and the waits around it: 2048 x 4096 x 4096, G = 128, bf16 takes 71-76
-// us (0.9-0.97 PFLOP/s; 8 more for the planes), with the matrix unit busy 44% of the time, LDS 29%,
-// waves at a wait or barrier 36%.  Tried without gain: the next unit's codes decoded between
+// Bound by the matrix unit and the waits around it: 2048 x 4096 x 4096, G = 128 takes 69-72
+// us (0.95-1.0 PFLOP/s; bfloat16 8 more for the planes), with the matrix unit busy 44% of the time,
+// LDS 28%, waves at a wait or barrier 35%.  Tried without gain: the next unit's codes decoded between
 // this one's products (79.5 against 78 us for f16 x), workgroups of four waves, two to a compute unit
 // (94 against 79 us; with G = 32 it gains 9%), halves of a tile for an expert's last rows (scratch).
 #pragma once
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
         // Step t: column block t % NCB of row block t / NCB.  The previous step's parts are scaled
         // while this one's products run, and no later: left free, the compiler puts all scaling
         // behind all products, whose parts then go to scratch memory (G = 32, 1024 x 14336 x 4096: 1337
-        // against 170 us; G = 64, 2048 x 4096 x 4096: 132 against 74).  One part a step fits the registers
+        // against 170 us then; G = 64, 2048 x 4096 x 4096: 132 against 74).  One part a step fits the registers
         // as it is (G = 128: 79 us, held in place 84).
         f4 part[2][GPU_];
         auto scale = [&](int t) {
