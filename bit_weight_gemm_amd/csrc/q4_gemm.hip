@@ -105,6 +105,8 @@ hipError_t dense(const Q4Args &a, hipStream_t s) {
         }
         return run_q4_skinny<XT, G, 1, 2, kDense>(a, 1, s);
     }
+    // up to 32 rows as above (4096 x 4096, 17 rows 8.6 us, with two 9.7); the blocks of more rows fill the units
+    if (a.M <= 32 && nb <= 256) return run_q4_skinny<XT, G, 2, 1, kDense>(a, 1, s);
     return run_q4_skinny<XT, G, 2, 2, kDense>(a, (a.M + 31) / 32, s);
 }
 
@@ -149,7 +151,9 @@ struct Deal {
 // The shortest by an estimate in microseconds, whose constants were fitted to measured times
 // (M = 33 .. 2048; N x K = 4096 x 4096, 14336 x 4096, 5003 x 4000, 1024 x 1024 and 1000 x 8192;
 // all G and types).  A kernel takes as many rounds of the 256 compute units as its workgroups need,
-// and in each so many microseconds a unit of 128 k; shares are written and joined at 8 TB/s.
+// and in each so many microseconds a unit of 128 k (without LDS a last round counts half by its
+// workgroups); shares are written and joined at 8 TB/s, with more time for the launch and for rows
+// that are not aligned.
 // f16, 4096 x 4096, estimate against measured: 64 rows skinny 10.8 / 11.3, 128 rows in
 // 8 shares 17.6 / 17.3 (skinny 19.6), 256 rows in 4 shares 23 / 22.6 (skinny 35, one share 41), 512 rows in
 // 2 shares 34 / 35 (one 43), 2048 rows in tiles of 128 67 / 75 (of 64: 93).
@@ -165,7 +169,8 @@ Deal deal(int64_t N, int64_t K, int64_t G, int64_t M, int dtype) {
         const double blocks = up(nb / 2), rows = (double)((M + 31) / 32);
         double wk = 1;
         while (wk < 8 && blocks * rows * wk < kWavesWanted && 2 * wk <= ku) wk *= 2;
-        least = up(up(blocks * wk / 8) * rows / kCus) * (2.0 + up(ku / wk) * (f32 ? (fine ? 4.5 : 3.9) : (fine ? 2.6 : 2.2)));
+        const double full = up(blocks * wk / 8) * rows / kCus, share = full <= 1 ? 1 : (full + up(full)) / 2;
+        least = share * (2.0 + up(ku / wk) * (f32 ? (fine ? 4.5 : 3.9) : (fine ? 2.6 : 2.2)));
     }
     for (int bm = 64; bm <= 128; bm *= 2) {
         if (bm == 128 && f32 && fine) continue;  // its registers do not suffice
@@ -173,7 +178,7 @@ Deal deal(int64_t N, int64_t K, int64_t G, int64_t M, int dtype) {
         const double unit = f32 ? (bm == 64 ? (fine ? 2.4 : 2.0) : 3.4) : (bm == 64 ? (fine ? 1.6 : 1.35) : (fine ? 2.4 : 1.95));
         for (int split = 1; split <= 16 && split <= ku && (split == 1 || tiles * split <= kCus); ++split) {
             const double us = 5.5 + (q4_plain_x(K, dtype) ? 0.0 : 5.0) + up(tiles * split / kCus) * up(ku / split) * unit +
-                              (split == 1 ? 0.0 : 3.5 + (double)split * M * N * 1e-6);
+                              (split == 1 ? 0.0 : (N % 4 ? 6.5 : 3.5) + (double)split * M * N * 1e-6);
             if (us < least) least = us, best = Deal{bm, split};
         }
     }
