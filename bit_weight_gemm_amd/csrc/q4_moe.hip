@@ -106,18 +106,20 @@ hipError_t product(const MoePlan &p, const Q4Args &a, hipStream_t s) {
     return run_q4_skinny<XT, 128, 1, 2, MODE>(a, p.max_tiles, s);
 }
 
+// Two column blocks of each product to a workgroup (one token 14.3 us, with one 14.5; 64 slots 46 and 52); two
+// units of codes in flight in either launch.
 template <int XT, int PH>
 hipError_t row_gate_up(const Q4RowArgs &a, int64_t slots, hipStream_t s) {
-    if (a.w.G == 32) return run_q4_row<XT, 32, 2, 8, 2, kRowGateUp, PH, kF32>(a, slots, s);
-    if (a.w.G == 64) return run_q4_row<XT, 64, 2, 8, 2, kRowGateUp, PH, kF32>(a, slots, s);
-    return run_q4_row<XT, 128, 2, 8, 2, kRowGateUp, PH, kF32>(a, slots, s);
+    if (a.w.G == 32) return run_q4_row<XT, 32, 4, 8, 2, kRowGateUp, PH, kF32>(a, slots, s);
+    if (a.w.G == 64) return run_q4_row<XT, 64, 4, 8, 2, kRowGateUp, PH, kF32>(a, slots, s);
+    return run_q4_row<XT, 128, 4, 8, 2, kRowGateUp, PH, kF32>(a, slots, s);
 }
 
 template <int XT, int DT>
 hipError_t row_down_sum(const Q4RowArgs &a, int64_t T, hipStream_t s) {
-    if (a.w.G == 32) return run_q4_row<XT, 32, 1, 16, 4, kRowDownSum, 1, DT>(a, T, s);
-    if (a.w.G == 64) return run_q4_row<XT, 64, 1, 16, 4, kRowDownSum, 1, DT>(a, T, s);
-    return run_q4_row<XT, 128, 1, 16, 4, kRowDownSum, 1, DT>(a, T, s);
+    if (a.w.G == 32) return run_q4_row<XT, 32, 1, 16, 2, kRowDownSum, 1, DT>(a, T, s);
+    if (a.w.G == 64) return run_q4_row<XT, 64, 1, 16, 2, kRowDownSum, 1, DT>(a, T, s);
+    return run_q4_row<XT, 128, 1, 16, 2, kRowDownSum, 1, DT>(a, T, s);
 }
 
 // A few slots: two launches, every slot with its own expert's weights; h in two
@@ -217,8 +219,8 @@ hipError_t tiled(const MoePlan &p, const void *x, const float *weights, const Q4
 }  // namespace
 
 // Up to kDirectSlots slots, or up to kDirectSpread while that is no more than one per expert, each reads its
-// expert's weights for itself; their rows have to fit in LDS.  (64 experts, 8 each, 2048 x 1024: 40 slots 39 us,
-// found by their expert's workgroups 50, 64 slots 55 and 65; of 8 experts, 48 slots 28 and 22.)
+// expert's weights for itself; their rows have to fit in LDS.  (64 experts, 8 each, 2048 x 1024: 40 slots 33 us,
+// found by their expert's workgroups 50, 64 slots 46 and 65; of 8 experts, 48 slots 28 and 22.)
 // Beyond, by slots per expert (bf16; 64 experts of 8, 2048 x 1024: "large", 8 experts of 2, 1024 x 1024:
 // "small", which tiles of the gate product cannot fill the 256 compute units with):
 //   up to 8 (4 if small): workgroups find their slots (large, 64 tokens: 101 us, tiles of 64 rows
