@@ -468,12 +468,13 @@ def _calls():
 
 
 def _on(stream):
-    """The stream as a torch stream (a raw handle is wrapped), or None."""
+    """The stream as a torch stream (a raw handle is wrapped; 0 is the default stream's), or None."""
     if stream is None or hasattr(stream, "cuda_stream"):
         return stream
     import torch
 
-    return torch.cuda.ExternalStream(int(stream))
+    # a stream object made of the handle 0 would be a new stream of torch's pool
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
 
 
 class _Q4Struct(ctypes.Structure):
