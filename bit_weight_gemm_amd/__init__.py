@@ -477,6 +477,19 @@ def _on(stream):
     return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
 
 
+def _empty(shape, dtype, device, stream):
+    """New device memory for a call on `stream` (a torch stream, or None), which the caller's current stream may
+    use as well.  It comes from that stream's own pool: another's may hand out memory that work queued there still uses."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 class _Q4Struct(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("E", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("G", ctypes.c_int64), ("zeros", ctypes.c_int32), ("reserved", ctypes.c_int32)]
@@ -518,9 +531,9 @@ def q4_upload(codes, scales, zeros=None, stream=None) -> Q4Weight:
     ps = c.address(scales, "f16", (*lead, k // g), "scales", device)
     pz = None if zeros is None else c.address(zeros, "u8", (*lead, k // g), "zeros", device)
     raw = c.stream(stream, device)
-    w = Q4Weight(torch.empty(need, dtype=torch.uint8, device=codes.device), e, n, k, g, zeros is not None)
+    w = Q4Weight(_empty(need, torch.uint8, codes.device, stream), e, n, k, g, zeros is not None)
     if stream is not None:
-        for t in (w.data, codes, scales) + (() if zeros is None else (zeros,)):
+        for t in (codes, scales) + (() if zeros is None else (zeros,)):
             t.record_stream(stream)
     _check(lib().q4_pack(w.handle, pc, ps, pz, raw), "q4_pack")
     return w
@@ -534,9 +547,7 @@ def q4_dequant(w: Q4Weight, out=None, stream=None):
     shape = (w.N, w.K) if w.E is None else (w.E, w.N, w.K)
     raw = c.stream(stream, w.device)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=w.data.device)
-        if stream is not None:
-            out.record_stream(stream)
+        out = _empty(shape, torch.float32, w.data.device, stream)
     _check(lib().q4_dequant(w.handle, c.address(out, "f32", shape, "out", w.device), raw), "q4_dequant")
     return out
 

@@ -91,29 +91,35 @@ void *raw_stream(PyObject *stream, int device) {
     return p;
 }
 
-// A tensor of the current stream is kept from reuse until `stream` is done with it.
-void keep_for(const at::Tensor &t, PyObject *stream) {
-    if (stream == Py_None) return;
-    PyObject *o = THPVariable_Wrap(t), *done = o ? PyObject_CallMethod(o, "record_stream", "O", stream) : nullptr;
-    Py_XDECREF(o);
-    if (!done) throw Refused{};
-    Py_DECREF(done);
+// New device memory for a call on `stream`.  It comes from that stream's own pool: another
+// stream's may hand out memory that work queued there still uses.
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like, void *stream) {
+    const at::TensorOptions options = like.options().dtype(type).requires_grad(false);
+    const auto device = (c10::DeviceIndex)like.get_device();
+    const c10::hip::HIPStream current = c10::hip::getCurrentHIPStream(device);
+    if (current.stream() == stream) return at::empty(shape, options);
+    struct Restore {
+        const c10::hip::HIPStream &to;
+        ~Restore() { c10::hip::setCurrentHIPStream(to); }
+    } restore{current};
+    c10::hip::setCurrentHIPStream(c10::hip::getStreamFromExternal(static_cast<hipStream_t>(stream), device));
+    return at::empty(shape, options);
 }
 
-// The tensor o, or if that is None a new one.
+// The tensor o, or if that is None a new one.  A new one is given to the caller's current stream
+// as well, whose work on it has to end before its memory is used again.
 at::Tensor output(PyObject *o, at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like, const char *name,
-                  PyObject *stream) {
+                  void *stream) {
     if (o != Py_None) return tensor(o, name);
-    at::Tensor t = at::empty(shape, like.options().dtype(type));
-    keep_for(t, stream);
+    at::Tensor t = fresh(shape, type, like, stream);
+    const c10::hip::HIPStream current = c10::hip::getCurrentHIPStream((c10::DeviceIndex)like.get_device());
+    if (current.stream() != stream) t.record_stream(c10::Stream(c10::Stream::UNSAFE, t.device(), current.id()));
     return t;
 }
 
 // A temporary workspace.
-at::Tensor scratch(size_t need, const at::Tensor &like, PyObject *stream) {
-    at::Tensor ws = at::empty({(int64_t)need}, like.options().dtype(at::kByte));
-    keep_for(ws, stream);
-    return ws;
+at::Tensor scratch(size_t need, const at::Tensor &like, void *stream) {
+    return fresh({(int64_t)need}, at::kByte, like, stream);
 }
 
 int64_t number(PyObject *o) {
@@ -204,11 +210,11 @@ PyObject *py_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int code = type_code(x, "x");
         const void *px = address(x, x.scalar_type(), {m, w->K}, "x", device);
         void *stream = raw_stream(a[4], device);
-        const at::Tensor y = output(a[3], {m, w->N}, x.scalar_type(), x, "y", a[4]);
+        const at::Tensor y = output(a[3], {m, w->N}, x.scalar_type(), x, "y", stream);
         void *py = address(y, x.scalar_type(), {m, w->N}, "y", device);
         const size_t need = p_gemm_ws(w, m, code);
         at::Tensor ws;
-        if (need) ws = scratch(need, x, a[4]);
+        if (need) ws = scratch(need, x, stream);
         void *pw = need ? ws.data_ptr() : nullptr;
         return result(call([&] { return p_gemm(w, px, py, m, code, pw, need, stream); }), y);
     });
@@ -232,7 +238,8 @@ PyObject *py_route(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const void *pl = address(l, l.scalar_type(), {t, e}, "logits", device);
         const void *pb = a[2] == Py_None ? nullptr : address(tensor(a[2], "bias"), at::kFloat, {e}, "bias", device);
         void *stream = raw_stream(a[10], device);
-        const at::Tensor idx = output(a[8], {t, k}, at::kInt, l, "idx", a[10]), w = output(a[9], {t, k}, at::kFloat, l, "weights", a[10]);
+        const at::Tensor idx = output(a[8], {t, k}, at::kInt, l, "idx", stream);
+        const at::Tensor w = output(a[9], {t, k}, at::kFloat, l, "weights", stream);
         void *pi = address(idx, at::kInt, {t, k}, "idx", device), *pw = address(w, at::kFloat, {t, k}, "weights", device);
         const int st = call([&] {
             return p_route(pl, static_cast<const float *>(pb), static_cast<int32_t *>(pi), static_cast<float *>(pw), t, e, k,
@@ -257,7 +264,7 @@ PyObject *py_route_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const void *pl = address(l, l.scalar_type(), {t, e}, "logits", device);
         const void *pi = address(idx, at::kInt, {t, k}, "idx", device), *pw = address(dw, at::kFloat, {t, k}, "dw", device);
         void *stream = raw_stream(a[6], device);
-        const at::Tensor dl = output(a[5], {t, e}, l.scalar_type(), l, "dlogits", a[6]);
+        const at::Tensor dl = output(a[5], {t, e}, l.scalar_type(), l, "dlogits", stream);
         void *pd = address(dl, l.scalar_type(), {t, e}, "dlogits", device);
         return result(call([&] {
                           return p_route_backward(pl, static_cast<const int32_t *>(pi), static_cast<const float *>(pw), pd, t,
@@ -280,13 +287,13 @@ PyObject *py_moe(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const void *pi = address(idx, at::kInt, {t, k}, "idx", device);
         const void *pw = address(wts, at::kFloat, {t, k}, "weights", device);
         void *stream = raw_stream(a[8], device);
-        const at::Tensor y = output(a[7], {t, d}, x.scalar_type(), x, "y", a[8]);
+        const at::Tensor y = output(a[7], {t, d}, x.scalar_type(), x, "y", stream);
         void *py = address(y, x.scalar_type(), {t, d}, "y", device);
         const size_t need = p_moe_ws(t, k, e, d, f, code);
         if (need == 0)
             refuse(PyExc_ValueError, "no experts' products for T=%lld, k=%lld, E=%lld, d=%lld, f=%lld", (long long)t,
                    (long long)k, (long long)e, (long long)d, (long long)f);
-        const at::Tensor ws = scratch(need, x, a[8]);
+        const at::Tensor ws = scratch(need, x, stream);
         void *pws = ws.data_ptr();
         return result(call([&] {
                           return p_moe(px, static_cast<const int32_t *>(pi), static_cast<const float *>(pw), gate, up, down, py,

@@ -1,0 +1,135 @@
+"""Calls on a stream that is not the current one: whose memory their outputs and workspaces are.
+
+A call's kernels write its output and its workspace as soon as `stream` reaches them.  Memory of the current
+stream's pool may still be in use by work that is queued there, so both have to come from the pool of `stream`:
+every test looks at the allocator's own record of the segment that an address lies in.
+"""
+
+import pytest
+import torch
+
+import bit_weight_gemm_amd as bw
+from gpu_util import note
+from q4_util import cuda, gen, weight
+
+pytestmark = pytest.mark.gpu
+
+
+def pool_of(t):
+    """Handle of the stream whose pool the tensor's memory belongs to."""
+    at = t.data_ptr()
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= at < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("no segment holds the tensor")
+
+
+def pool_bytes(handle):
+    return sum(s["total_size"] for s in torch.cuda.memory_snapshot() if s["stream"] == handle)
+
+
+def side_stream():
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    return torch.cuda.Stream()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_new_calls_outputs_come_from_their_streams_pool(raw):
+    side = side_stream()
+    stream = side.cuda_stream if raw else side
+    codes, scales, zeros = (cuda(t) for t in weight(1, (4,), 128, 128, 64, True))
+    x = torch.randn((8, 128), generator=gen(2)).cuda()
+    idx = torch.randint(0, 4, (8, 2), generator=gen(3)).int().cuda()
+    wts = torch.rand((8, 2), generator=gen(4)).cuda()
+    logits = torch.randn((8, 4), generator=gen(5)).cuda()
+    torch.cuda.synchronize()
+    note(f"[streams] outputs raw={raw}")
+    w = bw.q4_upload(codes, scales, zeros, stream=stream)
+    dense = bw.q4_upload(codes[0], scales[0], zeros[0], stream=stream)
+    got = {"packed weight": w.data, "q4_dequant": bw.q4_dequant(w, stream=stream),
+           "q4_gemm": bw.q4_gemm(dense, x, stream=stream),
+           "q4_moe": bw.q4_moe(x, idx, wts, w, w, w, stream=stream),
+           "moe_route_backward": bw.moe_route_backward(logits, idx, wts, stream=stream)}
+    got["moe_route idx"], got["moe_route weights"] = bw.moe_route(logits, 2, stream=stream)
+    for what, t in got.items():
+        assert pool_of(t) == side.cuda_stream, what
+    side.synchronize()
+    assert torch.equal(got["q4_gemm"], bw.q4_gemm(dense, x)) and torch.equal(got["q4_moe"], bw.q4_moe(x, idx, wts, w, w, w))
+
+
+def test_new_calls_workspaces_come_from_their_streams_pool():
+    side = side_stream()
+    n, k, m = 4096, 4096, 300
+    w = bw.q4_upload(*(cuda(t) for t in weight(6, (), n, k, 128, False)))
+    x = torch.randn((m, k), generator=gen(7)).bfloat16().cuda()
+    y = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    need = bw.lib().q4_gemm_workspace_size(w.handle, m, bw.Q4_BF16)
+    assert need > 4 << 20
+    torch.cuda.synchronize()
+    note("[streams] workspace of q4_gemm")
+    bw.q4_gemm(w, x, y, stream=side)
+    assert pool_bytes(side.cuda_stream) >= need
+    side.synchronize()
+    assert torch.equal(y, bw.q4_gemm(w, x))
+
+    side = side_stream()
+    t, e, k, d, f = 512, 8, 2, 1024, 512
+    gate, up, down = (bw.q4_upload(*(cuda(t) for t in weight(8 + i, (e,), *s, 128, False)))
+                      for i, s in enumerate(((f, d), (f, d), (d, f))))
+    x = torch.randn((t, d), generator=gen(12)).bfloat16().cuda()
+    idx = torch.randint(0, e, (t, k), generator=gen(13)).int().cuda()
+    wts = torch.rand((t, k), generator=gen(14)).cuda()
+    y = torch.empty_like(x)
+    need = bw.lib().q4_moe_workspace_size(t, k, e, d, f, bw.Q4_BF16)
+    assert need > 4 << 20
+    torch.cuda.synchronize()
+    note("[streams] workspace of q4_moe")
+    bw.q4_moe(x, idx, wts, gate, up, down, y, stream=side)
+    assert pool_bytes(side.cuda_stream) >= need
+    side.synchronize()
+    assert torch.equal(y, bw.q4_moe(x, idx, wts, gate, up, down))
+
+
+def test_memory_that_the_current_stream_still_uses_is_left_alone():
+    """A tensor is read by work queued on the current stream, then freed; a call on another stream may not take its place."""
+    side = side_stream()
+    n, k, m = 4096, 4096, 300
+    w = bw.q4_upload(*(cuda(t) for t in weight(15, (), n, k, 128, False)))
+    x = torch.randn((m, k), generator=gen(16)).bfloat16().cuda()
+    want = bw.q4_gemm(w, x)
+    size = bw.lib().q4_gemm_workspace_size(w.handle, m, bw.Q4_BF16)
+    keep = torch.empty(size, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    note("[streams] memory in use by the current stream")
+    held = torch.full((size,), 7, dtype=torch.uint8, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(200_000_000)
+    torch.add(held, 0, out=keep)
+    del held
+    got = bw.q4_gemm(w, x, stream=side)
+    torch.cuda.synchronize()
+    assert (keep == 7).all() and torch.equal(got, want)
+
+
+def test_an_output_is_kept_for_the_callers_stream():
+    """The result is read by the current stream and dropped: its memory waits for that."""
+    side = side_stream()
+    n, k, m = 4096, 1024, 256
+    w = bw.q4_upload(*(cuda(t) for t in weight(17, (), n, k, 128, False)))
+    x = torch.randn((m, k), generator=gen(18)).half().cuda()
+    keep, minus, want = torch.empty((m, n), dtype=torch.float16, device="cuda"), -x, bw.q4_gemm(w, x)
+    torch.cuda.synchronize()
+    note("[streams] an output on the caller's stream")
+    got = bw.q4_gemm(w, x, stream=side)
+    at = got.data_ptr()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(200_000_000)
+    torch.neg(got, out=keep)
+    done = torch.cuda.Event()
+    done.record()
+    del got
+    other = bw.q4_gemm(w, minus, stream=side)
+    assert other.data_ptr() != at or done.query()
+    torch.cuda.synchronize()
+    assert torch.equal(-keep, want)
