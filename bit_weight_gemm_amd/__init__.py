@@ -136,6 +136,29 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _on(stream):
+    """The stream as a torch stream (a raw handle is wrapped; 0 is the default stream's), or None."""
+    if stream is None or hasattr(stream, "cuda_stream"):
+        return stream
+    import torch
+
+    # a stream object made of the handle 0 would be a new stream of torch's pool
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+
+
+def _empty(shape, dtype, device, stream):
+    """New device memory for a call on `stream` (a torch stream, or None), which the caller's current stream may
+    use as well.  It comes from that stream's own pool: another's may hand out memory that work queued there still uses."""
+    import torch
+
+    if stream is None or torch.device(device).type != "cuda":  # (another device is refused where the tensor is used)
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _dev(t, dtype, name):
     import torch
 
@@ -235,7 +258,7 @@ def tq2_gemm_path(w: Tq2Weight, x, y=None, path: int = TQ2_PATH_AUTO, stream=Non
         raise ValueError(f"x must be [M, {w.K}]")
     m = x.shape[0]
     if y is None:
-        y = torch.empty((m, w.N), dtype=torch.float32, device=x.device)
+        y = _empty((m, w.N), torch.float32, x.device, _on(stream))
     if y.shape != (m, w.N):
         raise ValueError(f"y must be [{m}, {w.N}]")
     _check(lib().tq2_gemm_path(w.handle, _dev(x, torch.float32, "x"), _dev(y, torch.float32, "y"), m, w.N, w.K,
@@ -251,7 +274,7 @@ def tq2_dequant(w: Tq2Weight, out=None, stream=None):
     import torch
 
     if out is None:
-        out = torch.empty((w.N, w.K), dtype=torch.float32, device="cuda")
+        out = _empty((w.N, w.K), torch.float32, "cuda", _on(stream))
     if tuple(out.shape) != (w.N, w.K):
         raise ValueError(f"out must be [{w.N}, {w.K}]")
     _check(lib().tq2_dequant(w.handle, _dev(out, torch.float32, "out"), _stream(stream)), "tq2_dequant")
@@ -296,9 +319,7 @@ def _workspace(workspace, need, like, stream, what):
     if need == 0:
         raise Tq2Error(TQ2_EINVAL, what)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-        if stream is not None and hasattr(stream, "cuda_stream"):
-            workspace.record_stream(stream)  # not reused before the work queued on `stream` is done
+        workspace = _empty(need, torch.uint8, like.device, _on(stream))
     if workspace.numel() < need:
         raise ValueError(f"workspace needs {need} bytes, got {workspace.numel()}")
     return workspace
@@ -309,7 +330,7 @@ def _blr_forward_call(bits_u, bits_v, h, l, g, x, y, stream, paths: bool, worksp
 
     npaths, m, d_in, d_out, r = _blr_sizes(bits_u, bits_v, h, l, g, x, paths)
     if y is None:
-        y = torch.empty((m, d_out), dtype=torch.float32, device=x.device)
+        y = _empty((m, d_out), torch.float32, x.device, _on(stream))
     _shape(y, (m, d_out), "y")
     args = [_dev(bits_u, torch.int32, "bits_u"), _dev(bits_v, torch.int32, "bits_v"), _dev(h, torch.float32, "h"),
             _dev(l, torch.float32, "l"), _dev(g, torch.float32, "g"), _dev(x, torch.float32, "x"),
@@ -366,13 +387,13 @@ def blr_forward_paths_save(bits_u, bits_v, h, l, g, x, y=None, saved=None, strea
 
     npaths, m, d_in, d_out, r = _blr_sizes(bits_u, bits_v, h, l, g, x, paths=True)
     if y is None:
-        y = torch.empty((m, d_out), dtype=torch.float32, device=x.device)
+        y = _empty((m, d_out), torch.float32, x.device, _on(stream))
     _shape(y, (m, d_out), "y")
     need = blr_saved_size(npaths, m, d_in, d_out, r)
     if need == 0:
         raise Tq2Error(TQ2_EINVAL, "blr_saved_size")
     if saved is None:
-        saved = torch.empty(need, dtype=torch.uint8, device=x.device)
+        saved = _empty(need, torch.uint8, x.device, _on(stream))
     if saved.dim() != 1 or saved.numel() < need:
         raise ValueError(f"saved must be a flat uint8 tensor of at least {need} bytes")
     _check(lib().blr_forward_paths_save(
@@ -417,7 +438,7 @@ def _blr_backward_call(bits_u, bits_v, h, l, g, x, dy, dh, dl, dg, dx, gscale, s
     _shape(dl, (npaths, r), "dl")
     _shape(dg, (npaths, d_in), "dg")
     if dx is None:
-        dx = torch.empty((m, d_in), dtype=torch.float32, device=x.device)
+        dx = _empty((m, d_in), torch.float32, x.device, _on(stream))
     _shape(dx, (m, d_in), "dx")
     args = [npaths, _dev(bits_u, torch.int32, "bits_u"), _dev(bits_v, torch.int32, "bits_v"),
             _dev(h, torch.float32, "h"), _dev(l, torch.float32, "l"), _dev(g, torch.float32, "g"),
@@ -465,29 +486,6 @@ def _calls():
     """The compiled calls, bound to the library's entry points."""
     lib()
     return _compiled
-
-
-def _on(stream):
-    """The stream as a torch stream (a raw handle is wrapped; 0 is the default stream's), or None."""
-    if stream is None or hasattr(stream, "cuda_stream"):
-        return stream
-    import torch
-
-    # a stream object made of the handle 0 would be a new stream of torch's pool
-    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-
-
-def _empty(shape, dtype, device, stream):
-    """New device memory for a call on `stream` (a torch stream, or None), which the caller's current stream may
-    use as well.  It comes from that stream's own pool: another's may hand out memory that work queued there still uses."""
-    import torch
-
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(t.device))
-    return t
 
 
 class _Q4Struct(ctypes.Structure):

@@ -9,7 +9,8 @@ import pytest
 import torch
 
 import bit_weight_gemm_amd as bw
-from gpu_util import note
+import workloads as wl
+from gpu_util import bits_dev, note, to_dev
 from q4_util import cuda, gen, weight
 
 pytestmark = pytest.mark.gpu
@@ -133,3 +134,54 @@ def test_an_output_is_kept_for_the_callers_stream():
     assert other.data_ptr() != at or done.query()
     torch.cuda.synchronize()
     assert torch.equal(-keep, want)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_ternary_and_blr_calls_memory_comes_from_their_streams_pool(raw):
+    side = side_stream()
+    stream = side.cuda_stream if raw else side
+    aos, n, k = wl.tiny_weight()
+    m, d_in, d_out, r = 64, 1024, 1024, 512
+    d = wl.blr_inputs(m=m, d_in=d_in, d_out=d_out, r=r, index=60)
+    one = [bits_dev(d["bits_u"]), bits_dev(d["bits_v"])] + [to_dev(d[v]) for v in ("h", "l", "g", "x")]
+    paths = [t[None].contiguous() for t in one[:5]] + one[5:]
+    x = to_dev(wl.tiny_x(5, k))
+    dy = 1e-3 * torch.randn((m, d_out), generator=gen(19)).cuda()
+    zero = lambda: [torch.zeros((1, v), device="cuda") for v in (d_out, r, d_in)]  # noqa: E731
+    grads = [zero() for _ in range(3)]
+    torch.cuda.synchronize()
+    note(f"[streams] ternary and BLR calls raw={raw}")
+    w = bw.tq2_upload(aos, n, k, stream=stream)
+    try:
+        got = {"tq2_gemm": bw.tq2_gemm(w, x, stream=stream), "tq2_dequant": bw.tq2_dequant(w, stream=stream)}
+        got["blr_forward_ws"] = bw.blr_forward_ws(*one, stream=stream)
+        got["blr_forward_paths"] = bw.blr_forward_paths(*paths, stream=stream)
+        y, saved = bw.blr_forward_paths_save(*paths, stream=stream)
+        got["blr_forward_paths_save y"], got["saved"] = y, saved
+        got["blr_backward_paths"] = bw.blr_backward_paths(*paths, dy, *grads[0], stream=stream)
+        got["blr_backward_paths_saved"] = bw.blr_backward_paths_saved(*paths, dy, *grads[1], saved, stream=stream)
+        got["blr_backward_paths_ws"] = bw.blr_backward_paths_ws(*paths, dy, *grads[2], stream=stream)
+        for what, t in got.items():
+            assert pool_of(t) == side.cuda_stream, what
+        side.synchronize()
+        assert torch.equal(got["tq2_gemm"], bw.tq2_gemm(w, x))
+        assert torch.equal(got["blr_forward_ws"], bw.blr_forward(*one))
+        assert torch.equal(got["blr_backward_paths"], got["blr_backward_paths_ws"])
+    finally:
+        torch.cuda.synchronize()
+        w.close()
+
+
+def test_a_workspace_of_blr_comes_from_its_streams_pool():
+    side = side_stream()
+    m, d_in, d_out, r = 256, 4096, 1024, 1024
+    d = wl.blr_inputs(m=m, d_in=d_in, d_out=d_out, r=r, index=61)
+    one = [bits_dev(d["bits_u"]), bits_dev(d["bits_v"])] + [to_dev(d[v]) for v in ("h", "l", "g", "x")]
+    y = torch.empty((m, d_out), device="cuda")
+    need = bw.blr_workspace_size(m, d_in, d_out, r)
+    torch.cuda.synchronize()
+    note("[streams] workspace of blr_forward_ws")
+    bw.blr_forward_ws(*one, y, stream=side)
+    assert need > 0 and pool_bytes(side.cuda_stream) >= need
+    side.synchronize()
+    assert torch.equal(y, bw.blr_forward(*one))
