@@ -488,6 +488,19 @@ def _calls():
     return _compiled
 
 
+def _for(stream, *tensors):
+    """The stream as a torch stream, or None; tensors that a call on it takes keep their memory until it is done with them."""
+    if stream is None:
+        return None
+    import torch
+
+    s = _on(stream)
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(s)
+    return s
+
+
 class _Q4Struct(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("E", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("G", ctypes.c_int64), ("zeros", ctypes.c_int32), ("reserved", ctypes.c_int32)]
@@ -510,7 +523,8 @@ class Q4Weight:
 def q4_upload(codes, scales, zeros=None, stream=None) -> Q4Weight:
     """Pack a 4-bit weight: codes uint8 [..., N, K/2] (element 2j in the low four bits of byte j), scales float16
     [..., N, K/G] with G 32, 64 or 128, zeros uint8 like scales (8 everywhere if None); W = (code - zero) * scale.
-    `...` is nothing, or one axis of experts.  The inputs may be freed once the work queued on the stream is done."""
+    `...` is nothing, or one axis of experts.  As in all calls below, `stream` is a torch stream or a raw handle (None: the
+    current stream); tensors given to a call may be freed at once, their memory stays until the stream is done with it."""
     import torch
 
     if codes.dim() not in (2, 3) or codes.numel() == 0:
@@ -523,16 +537,13 @@ def q4_upload(codes, scales, zeros=None, stream=None) -> Q4Weight:
     need = lib().q4_packed_size(e or 1, n, k, g, int(zeros is not None))
     if need == 0:
         raise ValueError(f"no packed form for E={e}, N={n}, K={k}, G={g}: G is 32, 64 or 128 and divides K")
-    c, lead, stream = _calls(), codes.shape[:-1], _on(stream)
+    c, lead, stream = _calls(), codes.shape[:-1], _for(stream, codes, scales, zeros)
     pc = c.address(codes, "u8", codes.shape, "codes", None)
     device = codes.get_device()
     ps = c.address(scales, "f16", (*lead, k // g), "scales", device)
     pz = None if zeros is None else c.address(zeros, "u8", (*lead, k // g), "zeros", device)
     raw = c.stream(stream, device)
     w = Q4Weight(_empty(need, torch.uint8, codes.device, stream), e, n, k, g, zeros is not None)
-    if stream is not None:
-        for t in (codes, scales) + (() if zeros is None else (zeros,)):
-            t.record_stream(stream)
     _check(lib().q4_pack(w.handle, pc, ps, pz, raw), "q4_pack")
     return w
 
@@ -541,7 +552,7 @@ def q4_dequant(w: Q4Weight, out=None, stream=None):
     """(code - zero) * scale as float32, exact: [N, K] or [E, N, K]."""
     import torch
 
-    c, stream = _calls(), _on(stream)
+    c, stream = _calls(), _for(stream, w.data, out)
     shape = (w.N, w.K) if w.E is None else (w.E, w.N, w.K)
     raw = c.stream(stream, w.device)
     if out is None:
@@ -554,7 +565,7 @@ def q4_gemm(w: Q4Weight, x, y=None, stream=None):
     """y[M][N] = x[M][K] @ W^T in x's type (float32, float16 or bfloat16); returns y (allocated if None)."""
     if w.E is not None:
         raise ValueError("q4_gemm takes a weight without an axis of experts")
-    out = (_compiled or _calls()).gemm(w.handle, w.device, x, y, stream if stream is None else _on(stream))
+    out = (_compiled or _calls()).gemm(w.handle, w.device, x, y, stream if stream is None else _for(stream, w.data, x, y))
     if out.__class__ is int:
         _check(out, "q4_gemm")
     return out
@@ -573,7 +584,7 @@ def moe_route(logits, k, bias=None, score="softmax", groups=1, keep=1, group_top
     equal groups whose `group_top` best keys add up to most; equal keys go to the lower index.  The weights are the scores,
     divided by their sum if renorm.  Slots that find no expert (logits of -inf) get idx -1 and weight 0."""
     out = (_compiled or _calls()).route(logits, k, bias, _score(score), groups, keep, group_top, renorm, idx, weights,
-                                       stream if stream is None else _on(stream))
+                                       stream if stream is None else _for(stream, logits, bias, idx, weights))
     if out.__class__ is int:
         _check(out, "moe_route")
     return out
@@ -583,7 +594,7 @@ def moe_route_backward(logits, idx, dw, score="softmax", renorm=False, dlogits=N
     """Gradient of moe_route's weights: dlogits [T][E] (logits' type, overwritten; allocated if None) from dw
     float32 [T][k] and the idx that moe_route gave, the choice held fixed."""
     out = (_compiled or _calls()).route_backward(logits, idx, dw, _score(score), renorm, dlogits,
-                                                stream if stream is None else _on(stream))
+                                                stream if stream is None else _for(stream, logits, idx, dw, dlogits))
     if out.__class__ is int:
         _check(out, "moe_route_backward")
     return out
@@ -600,7 +611,8 @@ def q4_moe(x, idx, weights, gate: Q4Weight, up: Q4Weight, down: Q4Weight, y=None
     if up.device != gate.device or down.device != gate.device:
         raise ValueError("the weights are on different devices")
     out = (_compiled or _calls()).moe(x, idx, weights, gate.handle, up.handle, down.handle, gate.device, y,
-                                     stream if stream is None else _on(stream))
+                                     stream if stream is None else
+                                     _for(stream, x, idx, weights, gate.data, up.data, down.data, y))
     if out.__class__ is int:
         _check(out, "q4_moe")
     return out

@@ -136,6 +136,45 @@ def test_an_output_is_kept_for_the_callers_stream():
     assert torch.equal(-keep, want)
 
 
+def new_calls():
+    """Each 4-bit or mixture call on a stream, as (name, call(stream, tensors), tensors of its arguments)."""
+    codes, scales, zeros = (cuda(t) for t in weight(20, (4,), 128, 128, 64, True))
+    w = lambda: bw.q4_upload(codes, scales, zeros)  # noqa: E731
+    dense = lambda: bw.q4_upload(codes[0], scales[0], zeros[0])  # noqa: E731
+    x = lambda: torch.randn((300, 128), generator=gen(21)).cuda()  # noqa: E731
+    idx = lambda: torch.randint(0, 4, (300, 2), generator=gen(22)).int().cuda()  # noqa: E731
+    wts = lambda: torch.rand((300, 2), generator=gen(23)).cuda()  # noqa: E731
+    logits = lambda: torch.randn((300, 4), generator=gen(24)).cuda()  # noqa: E731
+    return [("q4_upload", lambda s, a: bw.q4_upload(*a, stream=s), [codes.clone(), scales.clone(), zeros.clone()]),
+            ("q4_dequant", lambda s, a: bw.q4_dequant(a[0], stream=s), [w()]),
+            ("q4_gemm", lambda s, a: bw.q4_gemm(*a, stream=s), [dense(), x()]),
+            ("moe_route", lambda s, a: bw.moe_route(a[0], 2, bias=a[1], stream=s), [logits(), torch.zeros(4, device="cuda")]),
+            ("moe_route_backward", lambda s, a: bw.moe_route_backward(*a, stream=s), [logits(), idx(), wts()]),
+            ("q4_moe", lambda s, a: bw.q4_moe(*a, stream=s), [x(), idx(), wts(), w(), w(), w()])]
+
+
+def test_arguments_may_be_freed_at_once():
+    """Memory of a call's arguments is not handed out again before its stream is done with it."""
+    side = side_stream()
+    calls = new_calls()
+    torch.cuda.synchronize()
+    for what, call, args in calls:
+        note(f"[streams] arguments of {what}")
+        data = [a.data if isinstance(a, bw.Q4Weight) else a for a in args]
+        places = [(t.data_ptr(), t.numel() * t.element_size()) for t in data]
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+        out = call(side, args)
+        done = torch.cuda.Event()
+        done.record(side)
+        del data
+        args.clear()
+        again = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in places]
+        assert not {at for at, _ in places} & {t.data_ptr() for t in again} or done.query(), what
+        side.synchronize()
+        del out
+
+
 @pytest.mark.parametrize("raw", [False, True])
 def test_ternary_and_blr_calls_memory_comes_from_their_streams_pool(raw):
     side = side_stream()
