@@ -100,7 +100,7 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     constexpr int FRAG = P == 1;                  // fragments are read a row block ahead where registers allow
     constexpr int PPT = BM * 16 / 512;  // 16-byte pieces of a plane's tile per thread
     __shared__ __attribute__((aligned(16))) _Float16 As[2][P][BM * 128];
-    __shared__ float rs[BM];
+    __shared__ float rs[BM], slot_weight[MODE == kTDown ? BM : 1];
     __shared__ int hexp[BM];   // kTGateUp: exponent of the row's h; kTDown: its slot
 
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, h = lane >> 4;
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
         if constexpr (MODE == kTDown) {
             const int slot = p.order[s];
             hexp[tid] = slot;
-            rs[tid] *= p.weights[slot];
+            slot_weight[tid] = p.weights[slot];  // (its product with the row's power of two may leave f32's range)
         }
         if constexpr (MODE == kTGateUp && P == 1) {
             const int ex = q4_h_exp(p.norm_exp[s], p.w.head[e], p.w2.head[e], p.w.K, p.w.zeros != nullptr);
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
                         if (p.part) p.part[blockIdx.y * p.part_stride + at] = v;
                         else store_from_float<DT>(p.y, at, v);
                     } else {
-                        static_cast<float *>(p.y)[(int64_t)hexp[m] * p.w.N + n] = v;
+                        static_cast<float *>(p.y)[(int64_t)hexp[m] * p.w.N + n] = slot_weight[m] * v;
                     }
                 }
             }
