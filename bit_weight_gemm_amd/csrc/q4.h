@@ -30,7 +30,7 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
 enum Q4Type { kF32 = 0, kF16 = 1, kBF16 = 2 };
 
-// Bytes before the codes: each expert's largest |scale| (f32 bits).
+// Bytes before the codes, which nothing reads.
 inline size_t q4_head_bytes(int64_t E) { return (size_t)(E * 4 + 255) / 256 * 256; }
 
 struct Q4Layout {
@@ -56,7 +56,6 @@ struct Q4View {
     const w4 *codes;
     const uint16_t *scales;
     const uint8_t *zeros;    // nullptr: every zero point is 8
-    const uint32_t *head;
     int E, N, K, G, nb, ku;
 };
 
@@ -64,7 +63,6 @@ inline Q4View q4_view(const void *data, int64_t E, int64_t N, int64_t K, int64_t
     const Q4Layout L = q4_layout(E, N, K, G, zeros);
     const char *b = static_cast<const char *>(data);
     Q4View v{};
-    v.head = reinterpret_cast<const uint32_t *>(b);
     v.codes = reinterpret_cast<const w4 *>(b + L.codes_off);
     v.scales = reinterpret_cast<const uint16_t *>(b + L.scales_off);
     v.zeros = zeros ? reinterpret_cast<const uint8_t *>(b + L.zeros_off) : nullptr;
@@ -172,7 +170,7 @@ struct MoePlan {
     bool tiled;                      // many rows per expert: the tiled products
     int64_t tile_rows, max_tiles;    // rows per tile of the grouped products, and the most tiles there can be
     int64_t ldx, ldh;                // tiled: rows of x and of h in whole units of 128
-    size_t off_order, off_tiles, off_h, off_part, off_x, off_xscale, off_xnorm, off_hscale, off_hplanes, total;
+    size_t off_order, off_tiles, off_h, off_part, off_x, off_xscale, off_hexp, off_hscale, off_hplanes, total;
 };
 MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtype);
 hipError_t launch_q4_moe(const MoePlan &p, const void *x, const int32_t *idx, const float *weights, const Q4View &gate,

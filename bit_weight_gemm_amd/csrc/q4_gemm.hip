@@ -6,37 +6,6 @@ namespace tq2 {
 
 namespace {
 
-__global__ __launch_bounds__(1024) void q4_zero_head_kernel(uint32_t *head, int E) {
-    if ((int)threadIdx.x < E) head[threadIdx.x] = 0;
-}
-
-// The largest |scale| of each expert (blockIdx.y) over its packed scales, `eights` pieces of
-// eight, by gridDim.x workgroups.  Halves without their sign order as integers do.
-__global__ __launch_bounds__(1024) void q4_head_kernel(const uint16_t *scales, int64_t eights, uint32_t *head) {
-    __shared__ uint32_t red[16];
-    const w4 *p = reinterpret_cast<const w4 *>(scales) + blockIdx.y * eights;
-    uint32_t most = 0;
-    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < eights; i += (int64_t)gridDim.x * 1024) {
-        const w4 v = p[i];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t lo = v[q] & 0x7fffu, hi = (v[q] >> 16) & 0x7fffu, m = lo > hi ? lo : hi;
-            most = m > most ? m : most;
-        }
-    }
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t b = (uint32_t)__shfl_xor((int)most, o);
-        most = b > most ? b : most;
-    }
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = most;
-    __syncthreads();
-    if (threadIdx.x > 0) return;
-    for (int q = 1; q < 16; ++q) most = red[q] > most ? red[q] : most;
-    const uint32_t bits = __builtin_bit_cast(uint32_t, half_bits(most));
-    if (gridDim.x == 1) head[blockIdx.y] = bits;
-    else atomicMax(&head[blockIdx.y], bits);
-}
-
 // One workgroup per block of 16 rows of an expert, its four waves taking the units in
 // turn.  Lane (r, h) reads 16 bytes of row r (k = 128u + 32h .. +31), orders the nibbles
 // and hands word c to lane (r, c) as its word h; the first 16 lanes also bring their
@@ -121,15 +90,9 @@ hipError_t dense_g(const Q4Args &a, hipStream_t s) {
 
 hipError_t launch_q4_pack(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, const Q4View &v,
                           hipStream_t s) {
-    uint32_t *head = const_cast<uint32_t *>(v.head);
     q4_pack_kernel<<<dim3((unsigned)v.nb, (unsigned)v.E), dim3(256), 0, s>>>(
         codes, scales, zeros, v, const_cast<w4 *>(v.codes), const_cast<uint16_t *>(v.scales),
         const_cast<uint8_t *>(v.zeros));
-    // (an atomic of every workgroup of the packing took most of its time: 64 x 2048 x 1024 180-220 us)
-    const int64_t eights = (int64_t)v.nb * v.ku * 2 * (128 / v.G), shares = (eights + 16383) / 16384;
-    const unsigned x = (unsigned)(shares < 64 ? shares : 64);
-    if (x > 1) q4_zero_head_kernel<<<dim3(1), dim3(1024), 0, s>>>(head, v.E);
-    q4_head_kernel<<<dim3(x, (unsigned)v.E), dim3(1024), 0, s>>>(v.scales, eights, head);
     return hipGetLastError();
 }
 

@@ -187,9 +187,10 @@ hipError_t skinny(const MoePlan &p, const void *x, const float *weights, const Q
     return dtype == kF32 ? product<kXF32x3, kDown>(p, d, s) : product<kXF32x2, kDown>(p, d, s);
 }
 
-// Many rows per expert.  For 16-bit types h is rounded to f16 under a power of two per
-// row: half a step of f16 (2^-11) in front of a sum over f, as much as the result's own
-// rounding for f16 and an eighth of it for bfloat16; f32 h goes through f32 and two planes.
+// Many rows per expert.  For 16-bit types h is rounded to f16 under a power of two per row and
+// unit of 128, from its largest value there: half a step of f16 (2^-11 of each value down to 2^-29 of the
+// unit's largest) in front of a sum over f, as much as the result's own rounding for f16 and an
+// eighth of it for bfloat16; f32 h goes through f32 and two planes.
 hipError_t tiled(const MoePlan &p, const void *x, const float *weights, const Q4View &gate, const Q4View &up,
                  const Q4View &down, const Q4Prep &px, int64_t k, int dtype, char *b, hipStream_t s) {
     const int planes = q4_planes(dtype), bm = (int)p.tile_rows;
@@ -199,19 +200,19 @@ hipError_t tiled(const MoePlan &p, const void *x, const float *weights, const Q4
     g.ntiles = reinterpret_cast<const int32_t *>(b), g.order = reinterpret_cast<const int32_t *>(b + p.off_order);
     g.tiles = reinterpret_cast<const int4 *>(b + p.off_tiles);
     g.a = plain ? static_cast<const _Float16 *>(x) : px.out, g.lda = plain ? gate.K : px.lda, g.plane = px.plane;
-    g.rowscale = px.rowscale, g.norm_exp = px.norm_exp, g.hscale = reinterpret_cast<float *>(b + p.off_hscale);
+    g.rowscale = px.rowscale, g.hexp = reinterpret_cast<int16_t *>(b + p.off_hexp);
     hipError_t e = launch_q4_tiled_gate_up(g, planes, bm, p.max_tiles, s);
     if (e != hipSuccess) return e;
     Q4TArgs d = g;
-    d.w = down, d.y = b + p.off_part, d.rowscale = g.hscale, d.lda = p.ldh, d.plane = p.slots * p.ldh;
+    d.w = down, d.y = b + p.off_part, d.rowscale = nullptr, d.lda = p.ldh, d.plane = p.slots * p.ldh;
     d.a = reinterpret_cast<const _Float16 *>(b + p.off_h);
     if (dtype == kF32) {
         Q4Prep ph{};
         ph.x = g.y, ph.rows = p.slots, ph.K = gate.N, ph.lda = p.ldh, ph.plane = d.plane;
-        ph.out = reinterpret_cast<_Float16 *>(b + p.off_hplanes), ph.rowscale = g.hscale;
+        ph.out = reinterpret_cast<_Float16 *>(b + p.off_hplanes), ph.rowscale = reinterpret_cast<float *>(b + p.off_hscale);
         e = launch_q4_prep(ph, kF32, s);
         if (e != hipSuccess) return e;
-        d.a = ph.out;
+        d.a = ph.out, d.rowscale = ph.rowscale;
     }
     return launch_q4_tiled_down(d, planes, bm, p.max_tiles, s);
 }
@@ -259,9 +260,9 @@ MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtyp
     p.off_part = take((size_t)p.slots * d * 4);
     if (p.tiled) {
         p.off_x = take(plain ? 0 : (size_t)q4_planes(dtype) * T * p.ldx * 2);
-        p.off_xscale = take((size_t)T * 4);
-        p.off_xnorm = take((size_t)T * 4);
-        p.off_hscale = take((size_t)p.slots * 4);
+        p.off_xscale = take(plain ? 0 : (size_t)T * 4);
+        p.off_hexp = take(f32 ? 0 : (size_t)p.slots * (p.ldh / 128) * 2);
+        p.off_hscale = take(f32 ? (size_t)p.slots * 4 : 0);
         p.off_hplanes = take(f32 ? (size_t)2 * p.slots * p.ldh * 2 : 0);
     }
     p.total = at;
@@ -278,11 +279,10 @@ hipError_t launch_q4_moe(const MoePlan &p, const void *x, const int32_t *idx, co
     int4 *tiles = reinterpret_cast<int4 *>(b + p.off_tiles);
     const float *part = reinterpret_cast<const float *>(b + p.off_part);
     Q4Prep px{};
-    if (p.tiled) {
+    if (p.tiled && !q4_plain_x(gate.K, dtype)) {
         px.x = x, px.rows = T, px.K = gate.K, px.lda = p.ldx, px.plane = T * p.ldx;
-        px.out = q4_plain_x(gate.K, dtype) ? nullptr : reinterpret_cast<_Float16 *>(b + p.off_x);
+        px.out = reinterpret_cast<_Float16 *>(b + p.off_x);
         px.rowscale = reinterpret_cast<float *>(b + p.off_xscale);
-        px.norm_exp = reinterpret_cast<int32_t *>(b + p.off_xnorm);
     }
     const dim3 grid(1 + (unsigned)((px.rows + 15) / 16)), block(1024);
     const int slots = (int)p.slots, rows = (int)p.tile_rows;

@@ -65,7 +65,6 @@ __device__ void q4_prep_row(const Q4Prep &p, int64_t row) {
         for (int o = 1; o < 64; o <<= 1) most = fmaxf(most, __shfl_xor(most, o));
         shift = q4_row_shift(most);
     }
-    float norm = 0.0f;
     const int padded = (int)(p.lda / V);
     auto put = [&](int i, const float *v) {
         typedef _Float16 hv __attribute__((ext_vector_type(V)));
@@ -73,11 +72,9 @@ __device__ void q4_prep_row(const Q4Prep &p, int64_t row) {
 #pragma unroll
         for (int q = 0; q < V; ++q) {
             const float x = DT == kF16 ? v[q] : __builtin_ldexpf(v[q], shift);
-            norm += x * x;
             a[q] = (_Float16)x;
             if constexpr (P == 2) b[q] = __builtin_isfinite(x) ? (_Float16)(x - (float)a[q]) : (_Float16)0.0f;
         }
-        if (!p.out) return;
         *reinterpret_cast<hv *>(p.out + row * p.lda + (int64_t)i * V) = a;
         if constexpr (P == 2) *reinterpret_cast<hv *>(p.out + p.plane + row * p.lda + (int64_t)i * V) = b;
     };
@@ -92,16 +89,7 @@ __device__ void q4_prep_row(const Q4Prep &p, int64_t row) {
         if (i < pieces) piece(i, v);
         put(i, v);
     }
-    if (p.rowscale && lane == 0) p.rowscale[row] = __builtin_ldexpf(1.0f, -shift);
-    if (p.norm_exp) {
-        for (int o = 1; o < 64; o <<= 1) norm += __shfl_xor(norm, o);
-        int e = -200;
-        if (norm > 0.0f && norm < __builtin_inff()) {
-            (void)__builtin_frexpf(norm, &e);
-            e += 1 - 2 * shift;  // one more for the sum's own rounding
-        }
-        if (lane == 0) p.norm_exp[row] = e;
-    }
+    if (lane == 0) p.rowscale[row] = __builtin_ldexpf(1.0f, -shift);
 }
 
 }  // namespace tq2

@@ -20,6 +20,8 @@
 // (94 against 79 us; with G = 32 it gains 9%), halves of a tile for an expert's last rows (scratch).
 #pragma once
 
+#include <type_traits>
+
 #include "q4.h"
 
 namespace tq2 {
@@ -44,8 +46,7 @@ struct Q4TArgs {
     const int4 *tiles;
     const int32_t *ntiles;
     const float *weights;
-    const int32_t *norm_exp; // kTGateUp, f16 h: exponent above each token's squared norm
-    float *hscale;           // kTGateUp, f16 h: the power of two that each place's row was divided by
+    int16_t *hexp;           // f16 h: q4_h_exp of each place's row and unit of 128 columns, [places][units]
     int64_t ldh;             // kTGateUp, f16 h: row length, whole units of 128 (zeros past N)
 };
 
@@ -81,17 +82,34 @@ __device__ __forceinline__ int q4_row_shift(float most) {
     return 15 - e > 126 ? 126 : 15 - e;
 }
 
-// The power of two by which a row's silu(g) u is divided before it is rounded to f16,
-// so that it stays below 2^15 whatever the weights: |g| <= |x| |w| and |w| <= sqrt(K)
-// most |scale|, likewise u.  The bound lies some 2^14 above typical values, below which
-// f16 has 14 more binades with all its bits.  norm_exp: 2^norm_exp >= |x|^2.
-__device__ __forceinline__ int q4_h_exp(int norm_exp, uint32_t gate_most, uint32_t up_most, int K, bool zeros) {
-    int eg, eu;
-    (void)__builtin_frexpf(__builtin_bit_cast(float, gate_most), &eg);
-    (void)__builtin_frexpf(__builtin_bit_cast(float, up_most), &eu);
-    const int ek = 32 - __builtin_clz(K) + (zeros ? 8 : 6);  // 2^ek >= K most^2, most = 15 (stored zero points) or 8
-    const int e = norm_exp + eg + eu + ek - 15;
-    return e < -100 ? -100 : e > 100 ? 100 : e;
+// The exponent of the power of two by which 128 columns of a row's silu(g) u are divided before they
+// are rounded to f16, from the bits of the largest magnitude among them, which comes to [2^14, 2^15).
+// (Beside an infinity or NaN finite values only have to stay finite: 114.)
+__device__ __forceinline__ int q4_h_exp(uint32_t most) {
+    const int e = (int)(most >> 23) - 141;
+    return e < -126 ? -126 : e;
+}
+
+// The two factors, as halves, that bring such values under a row's power of two, 2^down times as large
+// as theirs (down >= 0).  Two, because one would end at 2^-24: what falls below f16 with both is less than
+// 2^-39 of the row's largest value.
+__device__ __forceinline__ uint32_t q4_h_factors(int down) {
+    down = down < 48 ? down : 48;
+    const int half = down >> 1;
+    const h2 f = {(_Float16)__builtin_ldexpf(1.0f, -half), (_Float16)__builtin_ldexpf(1.0f, half - down)};
+    return __builtin_bit_cast(uint32_t, f);
+}
+__device__ __forceinline__ w4 q4_h_lower(w4 v, uint32_t factors) {
+    const h2 f = as_h2(factors), a = {f.x, f.x}, b = {f.y, f.y};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = __builtin_bit_cast(uint32_t, as_h2(v[q]) * a * b);
+    return v;
+}
+
+// silu(g) u for a consumer that rounds to f16: e^-g and the quotient from the hardware's exp2 and
+// reciprocal, relative error below 2^-17 (of it |g| 2^-24 from the rounded exponent).
+__device__ __forceinline__ float q4_silu_f16(float g, float u) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
 }
 
 template <int BM, int G, int P, int MODE, int DT>
@@ -100,8 +118,13 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     constexpr int FRAG = P == 1;                  // fragments are read a row block ahead where registers allow
     constexpr int PPT = BM * 16 / 512;  // 16-byte pieces of a plane's tile per thread
     __shared__ __attribute__((aligned(16))) _Float16 As[2][P][BM * 128];
-    __shared__ float rs[BM], slot_weight[MODE == kTDown ? BM : 1];
-    __shared__ int hexp[BM];   // kTGateUp: exponent of the row's h; kTDown: its slot
+    constexpr bool H16 = P == 1 && MODE != kTDense;   // h in f16 under powers of two
+    __shared__ __attribute__((aligned(16))) float rs[BM], slot_weight[MODE == kTDown ? BM : 4];
+    __shared__ __attribute__((aligned(16))) int slots[MODE == kTDown ? BM : 4];
+    // kTGateUp: bits of the largest magnitude of the row's h in this tile
+    __shared__ __attribute__((aligned(16))) int hmost[H16 && MODE == kTGateUp ? BM : 4];
+    constexpr int TU = 64;  // kTDown: units whose factors are at hand
+    __shared__ uint32_t factors[H16 && MODE == kTDown ? TU * BM : 1];
 
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, h = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -133,17 +156,31 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     };
     if (tid < BM) {
         const int64_t s = source(tid);
-        rs[tid] = p.rowscale ? p.rowscale[s] : 1.0f;
+        if constexpr (!(H16 && MODE == kTDown)) rs[tid] = p.rowscale ? p.rowscale[s] : 1.0f;
         if constexpr (MODE == kTDown) {
             const int slot = p.order[s];
-            hexp[tid] = slot;
+            slots[tid] = slot;
             slot_weight[tid] = p.weights[slot];  // (its product with the row's power of two may leave f32's range)
         }
-        if constexpr (MODE == kTGateUp && P == 1) {
-            const int ex = q4_h_exp(p.norm_exp[s], p.w.head[e], p.w2.head[e], p.w.K, p.w.zeros != nullptr);
-            hexp[tid] = ex;
-            if (tn == 0 && tid < count) p.hscale[row0 + tid] = __builtin_ldexpf(1.0f, ex);
+        if constexpr (H16 && MODE == kTGateUp) hmost[tid] = 0;
+    }
+    // A row's power of two is the largest of its units'; 512/BM neighbouring threads serve a row.
+    constexpr int LANES = 512 / BM;
+    const int16_t *units_exp = nullptr;
+    int row_exp = -126;
+    auto fill_factors = [&](int u0) {
+        for (int u = u0 + tid % LANES; u < ku && u < u0 + TU; u += LANES)
+            factors[(u - u0) * BM + tid / LANES] = q4_h_factors(row_exp - units_exp[u]);
+    };
+    if constexpr (H16 && MODE == kTDown) {
+        units_exp = p.hexp + source(tid / LANES) * ku;
+        for (int u = tid % LANES; u < ku; u += LANES) row_exp = units_exp[u] > row_exp ? units_exp[u] : row_exp;
+        for (int o = 1; o < LANES; o <<= 1) {
+            const int b = __shfl_xor(row_exp, o);
+            row_exp = b > row_exp ? b : row_exp;
         }
+        if (tid % LANES == 0) rs[tid / LANES] = __builtin_ldexpf(1.0f, row_exp);
+        fill_factors(0);
     }
     const _Float16 *ap[PPT];
     int al[PPT];
@@ -175,7 +212,11 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
 #pragma unroll
             for (int c = 0; c < PPT; ++c) areg[q][c] = *reinterpret_cast<const w4 *>(ap[c] + q * p.plane + (int64_t)u * 128);
     };
-    auto store_a = [&](int buf) {
+    auto store_a = [&](int buf, int u) {  // unit u
+        if constexpr (H16 && MODE == kTDown)
+#pragma unroll
+            for (int c = 0; c < PPT; ++c)
+                areg[0][c] = q4_h_lower(areg[0][c], factors[(u % TU) * BM + (tid >> 4) + 32 * c]);
 #pragma unroll
         for (int q = 0; q < P; ++q)
 #pragma unroll
@@ -264,7 +305,8 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     load_a(u_begin);
     load_b(0, u_begin);
     load_b(1, last(u_begin + 1));
-    store_a(0);
+    if constexpr (H16 && MODE == kTDown) __syncthreads();  // the factors
+    store_a(0, u_begin);
     load_a(last(u_begin + 1));
     if (late) decode(0);
     __syncthreads();
@@ -274,15 +316,71 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
             const int u = u0 + st;
             if (u < u_end) {
                 compute(st, st, [&] {
-                    store_a(st ^ 1);
+                    store_a(st ^ 1, u + 1);
                     load_a(last(u + 2));
                 });
                 load_b(st, last(u + 2));
                 __syncthreads();
+                if constexpr (H16 && MODE == kTDown)
+                    if ((u + 2) % TU == 0) {  // the next unit that is stored is the first of others
+                        fill_factors(u + 2);
+                        __syncthreads();
+                    }
             }
         }
     }
 
+    if constexpr (MODE == kTGateUp && H16) {  // a tile covers a whole unit of h
+        const int n = nb[0] * 16 + r;
+        uint32_t most[RB * 4];
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float scale = rs[rb * 16 + 4 * h + i];
+                const float v = n < p.w.N ? q4_silu_f16(acc[rb][0][i] * scale, acc[rb][1][i] * scale) : 0.0f;
+                acc[rb][0][i] = v;
+                most[rb * 4 + i] = __builtin_bit_cast(uint32_t, v) & 0x7fffffffu;  // (of the vector's element it would be element 0's)
+            }
+        // the largest of each row: every exchange halves the rows that a lane keeps
+        int first = 0;  // its first row, counted as rb * 4 + i
+        auto halve = [&](auto exchange, int bit, int keep) {
+            const bool upper = (r & bit) != 0;
+            first += upper ? keep : 0;
+#pragma unroll
+            for (int j = 0; j < keep; ++j) {
+                const uint32_t mine = upper ? most[j + keep] : most[j], other = upper ? most[j] : most[j + keep];
+                const uint32_t got = exchange(other);
+                most[j] = mine > got ? mine : got;
+            }
+        };
+        auto swapped = [](auto ctrl) {
+            return [](uint32_t v) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, decltype(ctrl)::value, 0xF, 0xF, false); };
+        };
+        halve(swapped(std::integral_constant<int, 0xB1>{}), 1, RB * 2);   // lane ^ 1
+        halve(swapped(std::integral_constant<int, 0x4E>{}), 2, RB);       // lane ^ 2
+        halve(swapped(std::integral_constant<int, 0x124>{}), 4, RB / 2);  // lane - 4 of the sixteen
+        halve(swapped(std::integral_constant<int, 0x128>{}), 8, RB / 4);  // lane ^ 8
+#pragma unroll
+        for (int j = 0; j < RB / 4; ++j) {
+            const int at = first + j;
+            atomicMax(&hmost[(at >> 2) * 16 + 4 * h + (at & 3)], (int)most[j]);
+        }
+        __syncthreads();
+        if (tid < count) p.hexp[(row0 + tid) * p.tiles_n + tn] = (int16_t)q4_h_exp(hmost[tid]);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            const int4 bits = *reinterpret_cast<const int4 *>(&hmost[rb * 16 + 4 * h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = rb * 16 + 4 * h + i;
+                if (m >= count) continue;
+                const int e = q4_h_exp(i == 0 ? bits.x : i == 1 ? bits.y : i == 2 ? bits.z : bits.w);
+                static_cast<_Float16 *>(p.y)[(row0 + m) * p.ldh + n] = (_Float16)__builtin_ldexpf(acc[rb][0][i], -e);
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         if constexpr (MODE == kTGateUp) {
@@ -290,13 +388,24 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int m = rb * 16 + 4 * h + i;
-                if (m >= count) continue;
+                if (m >= count || n >= p.w.N) continue;
                 const float g = acc[rb][0][i] * rs[m], u = acc[rb][1][i] * rs[m];
-                const float v = n < p.w.N ? g / (1.0f + expf(-g)) * u : 0.0f;
-                if constexpr (P == 1)  // a tile covers a whole unit of h
-                    static_cast<_Float16 *>(p.y)[(row0 + m) * p.ldh + n] = (_Float16)__builtin_ldexpf(v, -hexp[m]);
-                else if (n < p.w.N)
-                    static_cast<float *>(p.y)[(row0 + m) * p.w.N + n] = v;
+                static_cast<float *>(p.y)[(row0 + m) * p.w.N + n] = g / (1.0f + expf(-g)) * u;
+            }
+        } else if constexpr (MODE == kTDown) {
+            const int m = rb * 16 + 4 * h;
+            const f4 scale = *reinterpret_cast<const f4 *>(&rs[m]), weight = *reinterpret_cast<const f4 *>(&slot_weight[m]);
+            const int4 s4 = *reinterpret_cast<const int4 *>(&slots[m]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (m + i >= count) continue;
+                const int slot = i == 0 ? s4.x : i == 1 ? s4.y : i == 2 ? s4.z : s4.w;
+                float *out = static_cast<float *>(p.y) + (int64_t)slot * p.w.N;
+#pragma unroll
+                for (int cb = 0; cb < NCB; ++cb) {
+                    const int n = nb[cb] * 16 + r;
+                    if (n < p.w.N) out[n] = weight[i] * (acc[rb][cb][i] * scale[i]);
+                }
             }
         } else {
 #pragma unroll
@@ -307,13 +416,9 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
                     const int m = rb * 16 + 4 * h + i;
                     if (m >= count || n >= p.w.N) continue;
                     const float v = acc[rb][cb][i] * rs[m];
-                    if constexpr (MODE == kTDense) {
-                        const int64_t at = (row0 + m) * p.w.N + n;
-                        if (p.part) p.part[blockIdx.y * p.part_stride + at] = v;
-                        else store_from_float<DT>(p.y, at, v);
-                    } else {
-                        static_cast<float *>(p.y)[(int64_t)hexp[m] * p.w.N + n] = slot_weight[m] * v;
-                    }
+                    const int64_t at = (row0 + m) * p.w.N + n;
+                    if (p.part) p.part[blockIdx.y * p.part_stride + at] = v;
+                    else store_from_float<DT>(p.y, at, v);
                 }
             }
         }
@@ -335,9 +440,8 @@ struct Q4Prep {
     int64_t row0, rows;      // row0: of the launch
     int K;
     int64_t lda, plane;      // of the planes (elements)
-    _Float16 *out;           // nullptr: only norm_exp (f16 x used as it is)
+    _Float16 *out;
     float *rowscale;
-    int32_t *norm_exp;       // or nullptr
 };
 hipError_t launch_q4_prep(Q4Prep p, int dtype, hipStream_t s);
 // Whether x is read as it is: f16 rows of whole units.

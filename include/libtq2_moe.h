@@ -33,8 +33,8 @@ typedef struct q4_weight {
 size_t q4_packed_size(int64_t E, int64_t N, int64_t K, int64_t G, int zeros);
 
 /* Packs codes u8 [E][N][K/2] (element 2j in the low four bits of byte j, 2j+1 in the
- * high ones; 4-byte aligned), scales f16 [E][N][K/G] and zeros u8 [E][N][K/G] (NULL
- * exactly when w->zeros is 0), all in device memory, into w->data.  Scales are taken
+ * high ones; 4-byte aligned), scales f16 [E][N][K/G] and zeros u8 [E][N][K/G] (any byte;
+ * NULL exactly when w->zeros is 0), all in device memory, into w->data.  Scales are taken
  * as they are: an infinite or NaN one gives such weights, and products with them are
  * infinite or NaN (which of the two may depend on the number of rows). */
 int q4_pack(const q4_weight *w, const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, void *stream);
