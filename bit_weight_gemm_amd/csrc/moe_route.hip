@@ -338,8 +338,9 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p, int log
                 const float m = sc + __builtin_fabsf(key[i]);
                 if (l[i] != kNone && m < __builtin_inff()) mag = fmaxf(mag, m);
             }
-            // exp, sum, quotient and sum with the bias: below eight steps of 2^-24 each
-            error = 0x1p-21f * wave_max(mag);
+            // exp, sum, quotient and sum with the bias: below eight steps of 2^-24 each.  Scores below
+            // f32's normal range are flushed or held at e^-88: at most 2^-126 each.
+            error = 0x1p-21f * wave_max(mag) + 0x1p-125f;
         }
     }
 #pragma unroll

@@ -1,0 +1,50 @@
+"""The router and its gradient where f32 scores decide wrongly, saturate, underflow or are not finite.
+
+Indices are whole numbers, compared with the definition in f64.  Gradients are compared element by element in
+relative terms.  Renormalised, w_j = c_j / sum c by exponents relative to the largest chosen logit: an argument is off by half
+a step of the chosen logits' span S (S 2^-24), exp, sum, quotient and the factor 1 - p by at most 12 steps of 2^-24 more, for
+w_j and again for each w_i of the sum; so (2 S + 32) 2^-24 of w_j (|dw_j| + sum w_i |dw_i|).  Sigmoid without
+renormalising: dw p (1 - p), each factor a few steps: 16 2^-24 of the value.  Results below the normal range: 2^-126 2^-22.
+"""
+
+import math
+
+import pytest
+import torch
+
+import bit_weight_gemm_amd as bw
+from gpu_util import note
+from q4_util import cuda, gen, route64
+
+pytestmark = pytest.mark.gpu
+INF, NAN = math.inf, math.nan
+
+
+def check(logits, k, what, bias=None, score="sigmoid", groups=1, keep=1, group_top=1):
+    note(f"[moe_route] {what}")
+    idx, w = bw.moe_route(logits.cuda(), k, bias=cuda(bias), score=score, groups=groups, keep=keep, group_top=group_top)
+    want, want_w = route64(logits, k, bias, score, groups, keep, group_top, False)
+    assert torch.equal(idx.cpu(), want), what
+    fin = logits[torch.isfinite(logits)].double()
+    # as test_gpu_moe's: (L + 12) 2^-23 of the weight
+    tol = (float(fin.abs().max()) + 12) * 2.0 ** -23 * want_w + 2.0 ** -149
+    assert ((w.cpu().double() - want_w).abs() <= tol).all(), what
+
+
+def test_sigmoid_scores_below_f32s_normal_range():
+    """Sums of scores near 2^-126: e^-87 + e^-300 against twice e^-87.5."""
+    check(torch.tensor([[-87.0, -300.0, -87.5, -87.5]]), 2, "sums near 2^-126", groups=2, keep=1, group_top=2)
+    logits = -85 - 25 * torch.rand((300, 64), generator=gen(1))
+    check(logits, 6, "all scores small", groups=8, keep=3, group_top=2)
+    bias = torch.randint(0, 4, (64,), generator=gen(2)) * 2.0 ** -127
+    check(logits, 6, "small biases too", bias, groups=8, keep=3, group_top=2)
+    check(logits, 6, "without groups", bias)
+
+
+def test_softmax_scores_below_f32s_normal_range():
+    logits = -85 - 25 * torch.rand((300, 64), generator=gen(3))
+    logits[:, 5] = 0
+    bias = torch.zeros(64)
+    bias[5] = -INF
+    check(logits, 6, "softmax, all but one small", bias, "softmax")
+    check(logits, 6, "softmax groups", bias, "softmax", groups=8, keep=3, group_top=2)
