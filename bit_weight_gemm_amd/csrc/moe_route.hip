@@ -3,7 +3,7 @@
 //
 // Score p_e = softmax(l)_e or sigmoid(l_e); an expert's key is its logit (no bias and
 // no sum of several keys per group: softmax and sigmoid are monotonic), else p_e +
-// bias_e.  A group's key is the sum of its group_top best keys; the `keep` best groups
+// bias_e in f64.  A group's key is the sum of its group_top best keys; the `keep` best groups
 // stay.  Among what is left the k largest keys are chosen, the first at slot 0; equal
 // keys go to the lower index.  weights[j] = p of slot j's expert, divided by the sum
 // over the slots if renorm.
@@ -16,8 +16,8 @@
 // 256 experts f32 scores swap a pair every few calls, so such keys count in f64.  They
 // are formed in f32 first, with a bound on their error; a token whose decisions (the
 // order of its first k + 1 keys, and which groups stay) all have more than that
-// between them is done, the others, a few in a thousand, are done again in f64.
-// Without a bias the order inside groups is the logits' own, which has no error.
+// between them is done, the others, a few in a thousand, are done again in f64.  (The
+// logits' own order would not do inside groups either: different logits may have equal scores.)
 //
 // One wave per token.  A group has 2^log_lanes lanes, each with every 2^log_lanes-th of
 // its experts, so a group's best keys are found in its own lanes.  Keys are compared as
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p, int log
     at.own = at.group < p.groups && i0 < n ? (n - i0 + at.lanes - 1) >> log_lanes : 0;
 
     float l[V], key[V];
-    int order[V];  // decides among experts: the logit where there is no bias, else the key
+    int order[V];  // of the keys: decides among experts
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = i < at.own ? at.first + i * at.lanes : 0;
@@ -347,16 +347,14 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p, int log
     for (int i = 0; i < V; ++i) {
         order[i] = order_of(l[i]);
         if constexpr (KEYS) {
-            const int o = order[i] == kNoneOrder ? kNoneOrder : order_of(key[i]);
-            key[i] = __builtin_bit_cast(float, o);  // the key's order, for the groups
-            if (p.bias || o == kNoneOrder) order[i] = o;
+            order[i] = order[i] == kNoneOrder ? kNoneOrder : order_of(key[i]);
         }
     }
     bool close = false;  // some decision within the keys' error
     if (p.groups > 1) {
         int a = kNoneOrder, b = kNoneOrder;
 #pragma unroll
-        for (int i = 0; i < V; ++i) merge2(a, b, KEYS ? __builtin_bit_cast(int, key[i]) : order[i], kNoneOrder);
+        for (int i = 0; i < V; ++i) merge2(a, b, order[i], kNoneOrder);
         best_two(a, b, log_lanes);
         if (p.group_top > 1 && b > kNoneOrder) a = order_of(value_of(a) + value_of(b));
         const bool in = stays(p, a, at, log_lanes);
@@ -372,14 +370,13 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p, int log
 
     int mine = -1, from[V];
     sort_keys<V>(order, from);
-    const bool fuzzy = KEYS && p.bias;          // the order is that of keys with an error
-    const int passes = fuzzy ? p.k + 1 : p.k;  // one more key, to see how near it comes
+    const int passes = KEYS ? p.k + 1 : p.k;  // one more key, to see how near it comes
     float before = 0.0f;
     for (int j = 0; j < passes; ++j) {
         int best;
         const int e = take_best<V, int>(order, from, at, lane, kNoneOrder, kGone, best);
         if (e < 0) break;
-        if (fuzzy) {
+        if constexpr (KEYS) {
             if (j && before - value_of(best) <= 2.0f * error) close = true;
             before = value_of(best);
         }

@@ -57,7 +57,7 @@ int q4_gemm(const q4_weight *w, const void *x, void *y, int64_t M, int dtype, vo
 
 /* A mixture's router.  Per token t of T: scores p = softmax or sigmoid of logits
  * [T][E]; keys p + bias[e] (bias f32 [E] or NULL), or the logits themselves, which
- * order the same, where there is no bias and group_top is 1.  The experts lie in `groups`
+ * order the same, where there is no bias and group_top or groups is 1.  The experts lie in `groups`
  * equal groups; a group's key is the sum of its group_top (1 or 2) largest keys, and the
  * experts of the `keep` best groups stay.  idx [T][k] (int32) are the experts with
  * the k largest keys, in that order, equal keys by the lower index; weights [T][k] (f32)

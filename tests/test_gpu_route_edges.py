@@ -48,3 +48,13 @@ def test_softmax_scores_below_f32s_normal_range():
     bias[5] = -INF
     check(logits, 6, "softmax, all but one small", bias, "softmax")
     check(logits, 6, "softmax groups", bias, "softmax", groups=8, keep=3, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_saturated_scores_tie_as_in_the_definition(score):
+    """Two best keys to a group: the keys are scores, and sigmoid(40) = sigmoid(50) = 1 in f64."""
+    check(torch.tensor([[40.0, 50.0, 0.0, 0.0]]), 2, f"saturated {score}", None, score, 2, 1, 2)
+    logits = torch.randint(20, 60, (300, 64), generator=gen(4)).float()
+    check(logits, 8, f"saturated rows {score}", None, score, 8, 3, 2)
+    logits = torch.randint(0, 3, (300, 64), generator=gen(5)) * 1e-20
+    check(logits, 8, f"scores that agree {score}", None, score, 8, 3, 2)
