@@ -321,11 +321,15 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p, int log
     if constexpr (KEYS || !SIGMOID) {
         float score[V];
         if constexpr (!SIGMOID) {
-            total = 0.0f;
+            float sum[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) total += score[i] = l[i] == kNone ? 0.0f : KEYS ? exp_of(l[i] - most) : expf(l[i] - most);
+            for (int i = 0; i < V; ++i) sum[i] = score[i] = l[i] == kNone ? 0.0f : KEYS ? exp_of(l[i] - most) : expf(l[i] - most);
+#pragma unroll
+            for (int o = 1; o < V; o <<= 1)  // pairs of pairs: log2(V) roundings, not V - 1
+#pragma unroll
+                for (int i = 0; i < V; i += 2 * o) sum[i] += sum[i + o];
             // one lane's sum for all: the lanes' orders of addition differ
-            total = uniform(wave_sum(total), 0);
+            total = uniform(wave_sum(sum[0]), 0);
         }
         if constexpr (KEYS) {
             float mag = 0.0f;
@@ -338,9 +342,13 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p, int log
                 const float m = sc + __builtin_fabsf(key[i]);
                 if (l[i] != kNone && m < __builtin_inff()) mag = fmaxf(mag, m);
             }
-            // exp, sum, quotient and sum with the bias: below eight steps of 2^-24 each.  Scores below
-            // f32's normal range are flushed or held at e^-88: at most 2^-126 each.
-            error = 0x1p-21f * wave_max(mag) + 0x1p-125f;
+            // In steps of 2^-24 of the score, and one of the key for its sum with the bias.  exp_of: 3.2.
+            // Sigmoid: the sum with 1 one more, the reciprocal two: 8 with that of a group's two keys.
+            // Softmax: the rounded argument 0.4 of the largest score, and 5 of the total (the mean of
+            // x e^-x over 1024 terms at most); the total's log2(V) and 6 additions; its terms 3.2; quotient
+            // and product two: log2(V) + 22 likewise.  Scores below f32's normal range are flushed or held at
+            // e^-88: at most 2^-126 each.
+            error = (SIGMOID ? 8 : 22 + __builtin_ctz(V)) * 0x1p-24f * wave_max(mag) + 0x1p-125f;
         }
     }
 #pragma unroll

@@ -58,3 +58,18 @@ def test_saturated_scores_tie_as_in_the_definition(score):
     check(logits, 8, f"saturated rows {score}", None, score, 8, 3, 2)
     logits = torch.randint(0, 3, (300, 64), generator=gen(5)) * 1e-20
     check(logits, 8, f"scores that agree {score}", None, score, 8, 3, 2)
+
+
+def test_long_sums_of_a_softmax_do_not_decide():
+    """33 groups of 31: each lane adds 30 terms that f32 loses, 1.8e-6 of the sum, and a bias puts two keys within that."""
+    groups, n = 33, 31
+    logits = torch.full((1, groups, n), -16.65)
+    logits[:, :, 0] = 0
+    p = float(torch.softmax(logits.double().flatten(), 0)[0])
+    bias = torch.full((groups, n), -INF)
+    bias[0, 0] = -1 / 33
+    true_key = p + float(bias[0, 0])
+    other = float(torch.softmax(logits.double().flatten(), 0)[n + 1])
+    bias[1, 1] = true_key + 1.2e-8 - other
+    check(logits.view(1, -1), 2, "long sums", bias.flatten(), "softmax", groups, groups, 1)
+    check(logits.view(1, -1), 2, "long sums, one group", bias.flatten(), "softmax")
