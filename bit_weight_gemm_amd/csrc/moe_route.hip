@@ -10,7 +10,7 @@
 //
 // A logit of -inf masks its expert (so does a bias of -inf, or a dropped group):
 // it is never chosen, and slots that find no expert get idx -1 and weight 0, which
-// the experts' products skip.  A NaN logit ranks first, so that it shows.
+// the experts' products skip.  A NaN key ranks first, so that it shows.
 //
 // Keys that are sums of scores decide whole numbers in near ties: over 16384 tokens of
 // 256 experts f32 scores swap a pair every few calls, so such keys count in f64.  They
@@ -135,13 +135,13 @@ __device__ __forceinline__ double score64(float l, float most, double total) {
 }
 
 // exp of v to about two steps of f32 (v limited to +-88, where it is next to 0 or 2^127):
-// the product with log2(e) in two parts around the hardware's exp2.
-__device__ __forceinline__ float exp_of(float v) {
-    v = __builtin_amdgcn_fmed3f(v, -88.0f, 88.0f);
+// the product with log2(e) in two parts around the hardware's exp2.  NaN stays (the limits would drop it).
+__device__ __forceinline__ float exp_of(float x) {
+    const float v = __builtin_amdgcn_fmed3f(x, -88.0f, 88.0f);
     const float t = v * 1.44269504f;
     const float rest = __builtin_fmaf(v, 1.92596299e-8f, __builtin_fmaf(v, 1.44269504f, -t));
     const float e = __builtin_amdgcn_exp2f(t);
-    return __builtin_fmaf(e, rest * 0.69314718f, e);
+    return x != x ? x : __builtin_fmaf(e, rest * 0.69314718f, e);
 }
 
 // (a, b) and (c, d), each the best two of a set, to the best two of both.
@@ -338,7 +338,6 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p, int log
             for (int i = 0; i < V; ++i) {
                 const float sc = SIGMOID ? __builtin_amdgcn_rcpf(1.0f + exp_of(-l[i])) : score[i] * inv;
                 key[i] += sc;
-                if (l[i] != l[i]) key[i] = l[i];
                 const float m = sc + __builtin_fabsf(key[i]);
                 if (l[i] != kNone && m < __builtin_inff()) mag = fmaxf(mag, m);
             }

@@ -64,7 +64,8 @@ int q4_gemm(const q4_weight *w, const void *x, void *y, int64_t M, int dtype, vo
  * their scores, divided by their sum if renorm is not 0.  Keys are formed and compared
  * in f64.
  * A logit (or bias) of -inf masks its expert: it is never chosen, and slots that find
- * no expert get idx -1 and weight 0.  A NaN key ranks first.
+ * no expert get idx -1 and weight 0.  A NaN key ranks first.  A logit of NaN or +inf makes
+ * every softmax score of its row NaN.
  * 1 <= E <= 1024, 1 <= k <= min(64, E), 1 <= groups <= 64, E % groups == 0,
  * 1 <= keep <= groups; logits, idx and weights aligned to their elements; outputs do
  * not overlap each other or the inputs.  T == 0 is a no-op; T < 2^31. */

@@ -73,3 +73,17 @@ def test_long_sums_of_a_softmax_do_not_decide():
     bias[1, 1] = true_key + 1.2e-8 - other
     check(logits.view(1, -1), 2, "long sums", bias.flatten(), "softmax", groups, groups, 1)
     check(logits.view(1, -1), 2, "long sums, one group", bias.flatten(), "softmax")
+
+
+@pytest.mark.parametrize("groups,keep,group_top,bias", [(1, 1, 1, True), (4, 2, 2, False), (4, 2, 1, True)])
+def test_softmax_of_rows_that_are_not_finite(groups, keep, group_top, bias):
+    """A NaN logit, and one of +inf, make every score NaN: all weights show it, whatever the keys are."""
+    logits = torch.randn((4, 32), generator=gen(6))
+    logits[1, 9], logits[2, 20] = NAN, INF
+    b = 0.1 * torch.randn(32, generator=gen(7)) if bias else None
+    note(f"[moe_route] rows that are not finite groups={groups} top={group_top} bias={bias}")
+    for renorm in (False, True):
+        idx, w = (v.cpu() for v in bw.moe_route(logits.cuda(), 4, bias=cuda(b), groups=groups, keep=keep,
+                                                group_top=group_top, renorm=renorm))
+        assert w[[1, 2]].isnan().all() and torch.isfinite(w[[0, 3]]).all()
+        assert ((idx >= 0) & (idx < 32)).all()
