@@ -405,9 +405,11 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteArgs p, int log
     }
 }
 
-// dlogits of one token: with c_j the chosen scores, dc_j = dw_j, or with renorm
-// (dw_j - sum_i dw_i c_i / sum c) / sum c; then dp scattered to the experts and
-// through softmax dl = p (dp - sum dp p), or sigmoid dl = dp p (1 - p).
+// dlogits of one token from its chosen experts' d(weights) dw_j, with p the scores.  Without renorm
+// dp = dw scattered to the experts, then through softmax dl = p (dp - sum dp p), or sigmoid dl = dp p (1 - p).
+// With renorm w_j = p_j / sum p over the slots, and the scores themselves cancel: dw/dl is softmax's among the
+// chosen, w_j (dw_j - sum w_i dw_i), for sigmoid times 1 - p_j, and 0 for the others.  w is formed from exponents
+// relative to the largest chosen logit, so that scores below f32's range have their gradient.
 template <int DT, int V, bool SIGMOID>
 __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(const void *logits, const int32_t *idx, const float *dw,
                                                                      void *dlogits, int64_t T, int E, int k, int renorm) {
@@ -416,7 +418,7 @@ __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(const void 
     const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
     if (t >= T) return;
     int e = -1;
-    float dc = 0.0f, c = 0.0f;
+    float dc = 0.0f, c = kNone;  // of the lane's slot: d(weight), then what goes to its expert; its logit
     if (lane < k) {
         e = idx[t * k + lane];
         if (e < 0 || e >= E) e = -1;
@@ -426,7 +428,7 @@ __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(const void 
         }
     }
     float l[V], pr[V];
-    float most = kNone;
+    float most = kNone, total = 1.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int x = lane + 64 * i;
@@ -436,24 +438,29 @@ __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(const void 
     if constexpr (SIGMOID) {
 #pragma unroll
         for (int i = 0; i < V; ++i) pr[i] = 1.0f / (1.0f + expf(-l[i]));
-        c = 1.0f / (1.0f + expf(-c));
     } else {
         most = wave_max(most);
-        float total = 0.0f;
+        total = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) total += pr[i] = l[i] == kNone ? 0.0f : expf(l[i] - most);
         total = wave_sum(total);
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // 0: every logit is -inf
 #pragma unroll
         for (int i = 0; i < V; ++i) pr[i] *= inv;
-        c = c == kNone ? 0.0f : expf(c - most) * inv;
     }
-    if (e < 0) c = 0.0f;
-    float dot = wave_sum(dc * c);
+    float dot = 0.0f;
     if (renorm) {
-        const float total = wave_sum(c);
-        dc = e < 0 || total == 0.0f ? 0.0f : (dc - dot / total) / total;
-        dot = wave_sum(dc * c);
+        const float top = wave_max(c), from = SIGMOID ? fminf(top, 0.0f) : top;
+        float w = c == kNone ? 0.0f : expf(c - from);
+        if constexpr (SIGMOID) w = c >= 0.0f ? 1.0f / (1.0f + expf(-c)) : w / (1.0f + expf(c));
+        bool none = top == kNone;
+        if (!none && (SIGMOID ? top : top - most) < -700.0f)  // the forward's weights are 0 where the f64 scores are
+            none = !__any(e >= 0 && score64<SIGMOID>(c, most, (double)total) > 0.0);
+        const float sum = wave_sum(w);
+        w = none || e < 0 ? 0.0f : w / sum;
+        dc = w * (dc - wave_sum(w * dc));
+    } else if constexpr (!SIGMOID) {
+        dot = wave_sum(c == kNone ? 0.0f : dc * expf(c - most) / total);
     }
     float dp[V];
 #pragma unroll
@@ -468,7 +475,9 @@ __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(const void 
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int x = lane + 64 * i;
-        const float v = SIGMOID ? dp[i] * pr[i] * (1.0f - pr[i]) : pr[i] * (dp[i] - dot);
+        float v;
+        if constexpr (SIGMOID) v = dp[i] * (renorm ? 1.0f : pr[i]) * (1.0f - pr[i]);
+        else v = renorm ? dp[i] + 0.0f * pr[i] : pr[i] * (dp[i] - dot);  // (the row's NaN shows)
         if (x < E) store_from_float<DT>(dlogits, t * E + x, v);
     }
 }

@@ -75,8 +75,8 @@ int moe_route(const void *logits, const float *bias, int32_t *idx, float *weight
 /* Gradient of moe_route's weights with respect to the logits, the choice held fixed:
  * dlogits [T][E] (of the logits' type, overwritten) from dw = d(weights) f32 [T][k] and
  * the idx that moe_route gave (entries outside 0 .. E-1 have no weight and add nothing; an expert
- * that a row names twice gets both contributions).  f32 sums.  Where a renormalised
- * row's scores add up to 0, its gradient is 0. */
+ * that a row names twice gets both contributions).  f32 sums.  Renormalised, only
+ * the chosen experts' logits have a gradient; where a row's scores (in f64) add up to 0, it is 0. */
 int moe_route_backward(const void *logits, const int32_t *idx, const float *dw, void *dlogits, int64_t T, int64_t E,
                        int64_t k, int score, int renorm, int dtype, void *stream);
 

@@ -87,3 +87,73 @@ def test_softmax_of_rows_that_are_not_finite(groups, keep, group_top, bias):
                                                 group_top=group_top, renorm=renorm))
         assert w[[1, 2]].isnan().all() and torch.isfinite(w[[0, 3]]).all()
         assert ((idx >= 0) & (idx < 32)).all()
+
+
+def gradient64(logits, idx, dw, score, renorm):
+    """dlogits from the closed forms in f64, with 1 - p formed without cancelling; and the terms' magnitudes."""
+    l, dw = logits.double(), dw.double()
+    on = (idx >= 0) & (idx < l.shape[1])
+    at = idx.long().clamp(0, l.shape[1] - 1)
+    c = torch.where(on, l.gather(1, at), -INF)
+    p = torch.sigmoid(c) if score == "sigmoid" else None
+    q = torch.sigmoid(-c) if score == "sigmoid" else torch.ones_like(c)
+    if renorm:
+        most = c.max(1, keepdim=True).values
+        w = torch.exp(c - most) * (q / torch.sigmoid(-most) if score == "sigmoid" else 1)  # p_j over the largest p
+        w = torch.where(on, w, 0.0)
+        w = w / w.sum(1, keepdim=True)
+        dw = torch.where(on, dw, 0.0)
+        mean, size = (w * dw).sum(1, keepdim=True), (w * dw.abs()).sum(1, keepdim=True)
+        v, mag = w * (dw - mean) * q, w * (dw.abs() + size) * q
+    else:
+        v = torch.where(on, dw * p * q, 0.0)
+        mag = v.abs()
+    out = torch.zeros_like(l).scatter_add(1, at, torch.where(on, v, 0.0))
+    return out, torch.zeros_like(l).scatter_add(1, at, torch.where(on, mag, 0.0))
+
+
+def check_gradient(logits, idx, dw, score, renorm, what):
+    note(f"[moe_route_backward] {what} {score} renorm={renorm}")
+    got = bw.moe_route_backward(logits.cuda(), idx.cuda(), dw.cuda(), score=score, renorm=renorm).cpu().double()
+    want, mag = gradient64(logits, idx, dw, score, renorm)
+    c = logits.double().gather(1, idx.long())
+    span = (c.max(1).values - c.min(1).values)[:, None]
+    tol = ((2 * span + 32) if renorm else 16) * 2.0 ** -24 * mag + 2.0 ** -148
+    assert torch.isfinite(got).all(), what
+    assert ((got - want).abs() <= tol).all(), (what, float(((got - want).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("below", [0, 60, 88, 95, 103, 300, 600])
+def test_renormalised_softmax_gradient_far_below_the_maximum(below):
+    """Chosen experts whose scores are small beside the row's largest, which a bias or a dropped group keeps out."""
+    t, e, k = 20, 40, 5
+    logits = torch.randn((t, e), generator=gen(8))
+    idx = torch.stack([torch.randperm(e - 1, generator=gen(20 + i))[:k] for i in range(t)]).int()
+    logits[:, e - 1] = below
+    dw = torch.randn((t, k), generator=gen(9))
+    check_gradient(logits, idx, dw, "softmax", True, f"{below} below")
+
+
+@pytest.mark.parametrize("at", [-600, -300, -100, -88, -60, -20, 0])
+def test_renormalised_sigmoid_gradient_of_large_logits(at):
+    t, e, k = 20, 40, 5
+    logits = torch.randn((t, e), generator=gen(10)) + at
+    idx = torch.topk(logits, k, dim=1).indices.int()
+    check_gradient(logits, idx, torch.randn((t, k), generator=gen(11)), "sigmoid", True, f"logits near {at}")
+
+
+def test_renormalised_gradient_of_rows_that_leave_nothing():
+    """Chosen logits of -inf have no weight: their rows' gradients are 0, and other slots' as if they were dropped."""
+    logits = torch.randn((3, 16), generator=gen(16))
+    logits[0] = -INF
+    logits[1, :4] = -INF
+    idx = torch.tensor([[0, 1, 2], [0, 5, 6], [7, 8, 9]], dtype=torch.int32)
+    dw = torch.randn((3, 3), generator=gen(17))
+    note("[moe_route_backward] rows that leave nothing")
+    for score in ("softmax", "sigmoid"):
+        got = bw.moe_route_backward(logits.cuda(), idx.cuda(), dw.cuda(), score=score, renorm=True).cpu()
+        assert (got[0] == 0).all() and (got[1, :4] == 0).all() and torch.isfinite(got).all()
+        dropped = idx.clone()
+        dropped[1, 0] = -1
+        want, mag = gradient64(logits, dropped, dw, score, True)
+        assert ((got[1:].double() - want[1:]).abs() <= 64 * 2.0 ** -24 * mag[1:]).all()
