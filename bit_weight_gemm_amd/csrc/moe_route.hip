@@ -427,8 +427,8 @@ __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(const void 
             c = load_as_float<DT>(logits, t * E + e);
         }
     }
-    float l[V], pr[V];
-    float most = kNone, total = 1.0f;
+    float l[V], pr[V];  // pr: softmax's scores, or sigmoid's factors
+    float most = kNone, total = 1.0f, inv = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int x = lane + 64 * i;
@@ -437,22 +437,25 @@ __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(const void 
     }
     if constexpr (SIGMOID) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) pr[i] = 1.0f / (1.0f + expf(-l[i]));
+        for (int i = 0; i < V; ++i) {  // p (1 - p), or with renorm 1 - p: from e^-|l|, where 1 - p would cancel
+            const float a = expf(-__builtin_fabsf(l[i])), b = 1.0f / (1.0f + a);
+            pr[i] = renorm ? (l[i] > 0.0f ? a * b : b) : a * b * b;
+        }
     } else {
         most = wave_max(most);
         total = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) total += pr[i] = l[i] == kNone ? 0.0f : expf(l[i] - most);
         total = wave_sum(total);
-        const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // 0: every logit is -inf
+        inv = total == 0.0f ? 0.0f : 1.0f / total;  // 0: every logit is -inf
 #pragma unroll
         for (int i = 0; i < V; ++i) pr[i] *= inv;
     }
     float dot = 0.0f;
     if (renorm) {
         const float top = wave_max(c), from = SIGMOID ? fminf(top, 0.0f) : top;
-        float w = c == kNone ? 0.0f : expf(c - from);
-        if constexpr (SIGMOID) w = c >= 0.0f ? 1.0f / (1.0f + expf(-c)) : w / (1.0f + expf(c));
+        float w = c == kNone ? 0.0f : SIGMOID && c >= 0.0f ? 1.0f : expf(c - from);
+        if constexpr (SIGMOID) w /= 1.0f + expf(-__builtin_fabsf(c));
         bool none = top == kNone;
         if (!none && (SIGMOID ? top : top - most) < -700.0f)  // the forward's weights are 0 where the f64 scores are
             none = !__any(e >= 0 && score64<SIGMOID>(c, most, (double)total) > 0.0);
@@ -460,7 +463,7 @@ __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(const void 
         w = none || e < 0 ? 0.0f : w / sum;
         dc = w * (dc - wave_sum(w * dc));
     } else if constexpr (!SIGMOID) {
-        dot = wave_sum(c == kNone ? 0.0f : dc * expf(c - most) / total);
+        dot = wave_sum(c == kNone ? 0.0f : dc * expf(c - most) * inv);
     }
     float dp[V];
 #pragma unroll
@@ -472,14 +475,16 @@ __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(const void 
         for (int i = 0; i < V; ++i)
             if (ej == lane + 64 * i) dp[i] += dj;
     }
+    auto store = [&](auto value) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int x = lane + 64 * i;
-        float v;
-        if constexpr (SIGMOID) v = dp[i] * (renorm ? 1.0f : pr[i]) * (1.0f - pr[i]);
-        else v = renorm ? dp[i] + 0.0f * pr[i] : pr[i] * (dp[i] - dot);  // (the row's NaN shows)
-        if (x < E) store_from_float<DT>(dlogits, t * E + x, v);
-    }
+        for (int i = 0; i < V; ++i) {
+            const int x = lane + 64 * i;
+            if (x < E) store_from_float<DT>(dlogits, t * E + x, value(i));
+        }
+    };
+    if constexpr (SIGMOID) store([&](int i) { return dp[i] * pr[i]; });
+    else if (renorm) store([&](int i) { return dp[i] + 0.0f * pr[i]; });  // (the row's NaN shows)
+    else store([&](int i) { return pr[i] * (dp[i] - dot); });
 }
 
 template <int DT, int V>

@@ -134,12 +134,27 @@ def test_renormalised_softmax_gradient_far_below_the_maximum(below):
     check_gradient(logits, idx, dw, "softmax", True, f"{below} below")
 
 
-@pytest.mark.parametrize("at", [-600, -300, -100, -88, -60, -20, 0])
+@pytest.mark.parametrize("at", [-600, -300, -100, -88, -60, -20, 0, 20, 60, 300])
 def test_renormalised_sigmoid_gradient_of_large_logits(at):
     t, e, k = 20, 40, 5
     logits = torch.randn((t, e), generator=gen(10)) + at
     idx = torch.topk(logits, k, dim=1).indices.int()
     check_gradient(logits, idx, torch.randn((t, k), generator=gen(11)), "sigmoid", True, f"logits near {at}")
+
+
+def test_renormalised_sigmoid_gradient_of_mixed_signs():
+    t, e, k = 50, 64, 6
+    logits = 30 * torch.randn((t, e), generator=gen(12))
+    idx = torch.topk(logits, k, dim=1).indices.int()
+    check_gradient(logits, idx, torch.randn((t, k), generator=gen(13)), "sigmoid", True, "mixed signs")
+
+
+@pytest.mark.parametrize("at", [-60, -20, 0, 5, 10, 16, 20, 60])
+def test_sigmoid_gradient_of_large_logits(at):
+    t, e, k = 20, 40, 5
+    logits = torch.randn((t, e), generator=gen(14)) + at
+    idx = torch.topk(logits, k, dim=1).indices.int()
+    check_gradient(logits, idx, torch.randn((t, k), generator=gen(15)), "sigmoid", False, f"logits near {at}")
 
 
 def test_renormalised_gradient_of_rows_that_leave_nothing():
