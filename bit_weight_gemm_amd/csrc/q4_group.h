@@ -23,12 +23,13 @@ constexpr int kGroupMaxK = 2048;      // a row in a wave's registers: 32 values 
 constexpr int kGroupMaxSlots = 2048;
 
 struct Q4GroupArgs {
-    Q4View w, w2;            // kGroupGateUp: gate and up
+    Q4View w;                // kGroupGateUp: gate
     const void *x;           // kGroupGateUp: x [T][K]; kGroupDown: h [slots][K], f32
     float *y;
     const int32_t *idx;
     const float *weights;
     int slots, topk, log_wk;
+    Q4View w2;               // kGroupGateUp: up
 };
 
 template <int DT, int P, int G, int CB, int D, int MODE>

@@ -20,13 +20,14 @@ namespace tq2 {
 enum Q4RowMode { kRowGateUp = 0, kRowDownSum = 1 };
 
 struct Q4RowArgs {
-    Q4View w, w2;            // kRowGateUp: gate and up
+    Q4View w;                // kRowGateUp: gate
     const void *x;           // kRowGateUp: x [T][K]; kRowDownSum: h in bfloat16 parts [slots][P][ldh]
     void *y;                 // kRowGateUp: h in bfloat16 parts [slots][PH][ldh]; kRowDownSum: y [T][N]
     const int32_t *idx;      // [T][topk]
     const float *weights;    // [T][topk]
-    int topk;
     int64_t ldh;
+    int topk;
+    Q4View w2;               // kRowGateUp: up
 };
 
 // v as P bfloat16 parts (bits) that add up to it, the last of two rounded.

@@ -31,7 +31,7 @@ namespace tq2 {
 enum Q4TMode { kTDense = 0, kTGateUp = 1, kTDown = 2 };
 
 struct Q4TArgs {
-    Q4View w, w2;
+    Q4View w;
     const _Float16 *a;       // [planes][rows][lda]
     int64_t plane, lda;      // elements
     const float *rowscale;   // [rows]: the power of two that each row was divided by (nullptr: 1)
@@ -48,6 +48,7 @@ struct Q4TArgs {
     const float *weights;
     int16_t *hexp;           // f16 h: q4_h_exp of each place's row and unit of 128 columns, [places][units]
     int64_t ldh;             // kTGateUp, f16 h: row length, whole units of 128 (zeros past N)
+    Q4View w2;               // kTGateUp: up
 };
 
 __device__ __forceinline__ int q4_lds(int row, int chunk) { return row * 128 + ((chunk ^ (row & 15)) << 3); }
