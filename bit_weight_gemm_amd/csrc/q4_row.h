@@ -187,8 +187,8 @@ __global__ __launch_bounds__(WAVES * 64) void q4_row_kernel(Q4RowArgs p) {
         float g = total(at), u = total(at + 16);
         if (!__builtin_isfinite(g) || !__builtin_isfinite(u)) {
             const int e = p.idx[slot0];
-            g = q4_slow_dot<XT>(p.x, row / p.topk, p.w, e, nn);
-            u = q4_slow_dot<XT>(p.x, row / p.topk, p.w2, e, nn);
+            g = q4_slow_row<XT>(p.x, row / p.topk, p.w, e, nn);
+            u = q4_slow_row<XT>(p.x, row / p.topk, p.w2, e, nn);
         }
         uint16_t part[PH];
         q4_parts<PH>(g / (1.0f + expf(-g)) * u, part);
@@ -203,15 +203,17 @@ __global__ __launch_bounds__(WAVES * 64) void q4_row_kernel(Q4RowArgs p) {
             for (int j = 0; j < p.topk; ++j) {
                 const int e = p.idx[slot0 + j];
                 if (e < 0 || e >= p.w.E) continue;
-                float dot = 0.0f;
-#pragma unroll 1
-                for (int k = 0; k < K; ++k) {
-                    float x = 0.0f;
+                const uint16_t *x = static_cast<const uint16_t *>(p.x) + (int64_t)(slot0 + j) * P * p.ldh;
+                const float dot = q4_slow_dot(p.w, e, nn, [&](int k, float (&v8)[8]) {
+                    q4_x8<kXBF16>(x, k, v8);
 #pragma unroll
-                    for (int q = 0; q < P; ++q)
-                        x += load_as_float<kBF16>(p.x, ((int64_t)(slot0 + j) * P + q) * p.ldh + k);
-                    dot += x * q4_weight_at(p.w, e, nn, k);
-                }
+                    for (int q = 1; q < P; ++q) {
+                        float part[8];
+                        q4_x8<kXBF16>(x, q * p.ldh + k, part);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v8[i] += part[i];
+                    }
+                });
                 v += p.weights[slot0 + j] * dot;
             }
         }
