@@ -128,7 +128,18 @@ int64_t number(PyObject *o) {
     return v;
 }
 
-const q4_weight *weight(PyObject *handle) { return static_cast<const q4_weight *>(PyLong_AsVoidPtr(handle)); }
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused{};
+    return v != 0;
+}
+
+const q4_weight *weight(PyObject *handle) {
+    void *p = PyLong_AsVoidPtr(handle);
+    if (PyErr_Occurred()) throw Refused{};
+    if (!p) refuse(PyExc_ValueError, "no weight%s", "");
+    return static_cast<const q4_weight *>(p);
+}
 
 // The entry point's status as a number, or the output tensors.
 template <typename F>
@@ -185,6 +196,7 @@ PyObject *py_address(PyObject *, PyObject *const *a, Py_ssize_t n) {
         for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(s); ++i)
             shape.push_back(PyLong_AsLongLong(PySequence_Fast_GET_ITEM(s, i)));
         Py_DECREF(s);
+        if (PyErr_Occurred()) throw Refused{};
         const int device = a[4] == Py_None ? gpu_of(tensor(a[0], name), name) : (int)number(a[4]);
         return PyLong_FromVoidPtr(address(tensor(a[0], name), t, shape, name, device));
     });
@@ -227,7 +239,7 @@ PyObject *py_route(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor &l = tensor(a[0], "logits");
         if (l.dim() != 2) refuse(PyExc_ValueError, "logits must be [T, E]%s", "");
         const int64_t t = l.size(0), e = l.size(1), k = number(a[1]);
-        const int code = type_code(l, "logits"), score = (int)number(a[3]), renorm = PyObject_IsTrue(a[7]);
+        const int code = type_code(l, "logits"), score = (int)number(a[3]), renorm = truth(a[7]);
         const int64_t groups = number(a[4]), keep = number(a[5]), group_top = number(a[6]);
         if (k < 1 || k > e || k > 64)
             refuse(PyExc_ValueError, "k must lie between 1 and %lld, got %lld", (long long)(e < 64 ? e : 64), (long long)k);
@@ -257,7 +269,7 @@ PyObject *py_route_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor &l = tensor(a[0], "logits"), &idx = tensor(a[1], "idx"), &dw = tensor(a[2], "dw");
         if (l.dim() != 2 || idx.dim() != 2) refuse(PyExc_ValueError, "logits must be [T, E] and idx [T, k]%s", "");
         const int64_t t = l.size(0), e = l.size(1), k = idx.size(1);
-        const int code = type_code(l, "logits"), score = (int)number(a[3]), renorm = PyObject_IsTrue(a[4]);
+        const int code = type_code(l, "logits"), score = (int)number(a[3]), renorm = truth(a[4]);
         if (k < 1 || k > 64 || e < 1 || e > 1024)
             refuse(PyExc_ValueError, "no routing of k=%lld out of E=%lld", (long long)k, (long long)e);
         const int device = gpu_of(l, "logits");
