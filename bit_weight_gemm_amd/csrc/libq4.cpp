@@ -2,6 +2,8 @@
 // and launches.  Declarations and the contract live in include/libtq2_moe.h.
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "../../include/libtq2_moe.h"
 #include "internal.h"
 #include "q4.h"
@@ -28,9 +30,17 @@ tq2::Q4View view(const q4_weight *w) { return tq2::q4_view(w->data, w->E, w->N, 
 
 size_t bytes(const q4_weight *w) { return q4_packed_size(w->E, w->N, w->K, w->G, w->zeros); }
 
-// A caller's workspace: large enough, 256-byte aligned, clear of the output.
-bool workspace_bad(const void *ws, size_t ws_bytes, size_t need, const void *out, size_t out_bytes) {
-    return !ws || ws_bytes < need || !aligned(ws, 256) || overlap(ws, need, out, out_bytes);
+struct Range {
+    const void *at;
+    size_t bytes;
+};
+
+// A caller's workspace: large enough, 256-byte aligned, clear of the call's other arguments.
+bool workspace_bad(const void *ws, size_t ws_bytes, size_t need, std::initializer_list<Range> others) {
+    if (!ws || ws_bytes < need || !aligned(ws, 256)) return true;
+    for (const Range &r : others)
+        if (overlap(ws, need, r.at, r.bytes)) return true;
+    return false;
 }
 
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
@@ -76,8 +86,10 @@ int q4_gemm(const q4_weight *w, const void *x, void *y, int64_t M, int dtype, vo
     if (M == 0) return tq2::current_device(nullptr);
     if (!x || !y || !aligned(x, 16) || !aligned(y, 16)) return TQ2_EINVAL;
     const size_t ybytes = (size_t)M * w->N * size_of(dtype), need = q4_gemm_workspace_size(w, M, dtype);
-    if (overlap(y, ybytes, x, (size_t)M * w->K * size_of(dtype)) || overlap(y, ybytes, w->data, bytes(w))) return TQ2_EINVAL;
-    if (need && workspace_bad(workspace, workspace_bytes, need, y, ybytes)) return TQ2_EINVAL;
+    const size_t xbytes = (size_t)M * w->K * size_of(dtype);
+    if (overlap(y, ybytes, x, xbytes) || overlap(y, ybytes, w->data, bytes(w))) return TQ2_EINVAL;
+    if (need && workspace_bad(workspace, workspace_bytes, need, {{y, ybytes}, {x, xbytes}, {w->data, bytes(w)}}))
+        return TQ2_EINVAL;
     const int st = tq2::current_device(nullptr);
     if (st) return st;
     return tq2::status_of(tq2::launch_q4_gemm(view(w), x, y, M, dtype, workspace, static_cast<hipStream_t>(stream)));
@@ -146,7 +158,10 @@ int q4_moe(const void *x, const int32_t *idx, const float *weights, const q4_wei
     if (overlap(y, n, x, n) || overlap(y, n, idx, m) || overlap(y, n, weights, m) || overlap(y, n, gate->data, bytes(gate)) ||
         overlap(y, n, up->data, bytes(up)) || overlap(y, n, down->data, bytes(down)))
         return TQ2_EINVAL;
-    if (workspace_bad(workspace, workspace_bytes, need, y, n)) return TQ2_EINVAL;
+    if (workspace_bad(workspace, workspace_bytes, need,
+                      {{y, n}, {x, n}, {idx, m}, {weights, m}, {gate->data, bytes(gate)}, {up->data, bytes(up)},
+                       {down->data, bytes(down)}}))
+        return TQ2_EINVAL;
     const int st = tq2::current_device(nullptr);
     if (st) return st;
     const tq2::MoePlan p = tq2::moe_plan(T, k, E, d, f, dtype);

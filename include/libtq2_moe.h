@@ -50,8 +50,8 @@ size_t q4_gemm_workspace_size(const q4_weight *w, int64_t M, int dtype);
  * have the type `dtype`, are row-major and 16-byte aligned and do not overlap; y is
  * overwritten, its values rounded once from f32 sums (nearest even).  Results are
  * deterministic.  M == 0 is a no-op; M < 2^31.  workspace: q4_gemm_workspace_size bytes,
- * 256-byte aligned, clear of y (NULL where that is 0); calls that share one must not
- * overlap in time. */
+ * 256-byte aligned, clear of x, y and the weight (NULL where that is 0); calls that share
+ * one must not overlap in time. */
 int q4_gemm(const q4_weight *w, const void *x, void *y, int64_t M, int dtype, void *workspace, size_t workspace_bytes,
             void *stream);
 
@@ -90,7 +90,7 @@ size_t q4_moe_workspace_size(int64_t T, int64_t k, int64_t E, int64_t d, int64_t
  * gate and up [E][f][d] with equal G and both or neither with zero points, down [E][d][f].
  * Sums are f32, in an order that does not depend on timing: results are deterministic.
  * x and y 16-byte aligned, not overlapping; 1 <= k <= 64; T * k < 2^24; T == 0 is a no-op.
- * workspace: q4_moe_workspace_size bytes, 256-byte aligned, clear of y; its contents are
+ * workspace: q4_moe_workspace_size bytes, 256-byte aligned, clear of all else; its contents are
  * scratch, and calls that share one must not overlap in time. */
 int q4_moe(const void *x, const int32_t *idx, const float *weights, const q4_weight *gate, const q4_weight *up,
            const q4_weight *down, void *y, int64_t T, int64_t k, int dtype, void *workspace, size_t workspace_bytes,
