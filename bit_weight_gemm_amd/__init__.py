@@ -18,6 +18,8 @@ moe_route_backward and q4_moe.  The last three and q4_gemm go through a compiled
 module (csrc/binding.cpp): beside their kernels' few microseconds, checks and
 conversions in Python would be the larger part.
 
+No call records anything for autograd: gradients come from the backward calls.
+
 Every tensor's shape is checked here against the sizes the call derives from x,
 h and l before anything reaches the library: the C ABI takes raw device
 pointers and cannot see buffer sizes.

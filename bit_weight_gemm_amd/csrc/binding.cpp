@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -89,6 +90,12 @@ void *raw_stream(PyObject *stream, int device) {
     Py_DECREF(handle);
     if (PyErr_Occurred()) throw Refused{};
     return p;
+}
+
+// The calls record nothing for autograd.  Where it would want a gradient, they say so.
+void no_gradient(const at::Tensor &t, const char *what) {
+    if (!t.requires_grad() || !at::GradMode::is_enabled()) return;
+    if (PyErr_WarnEx(PyExc_UserWarning, what, 2)) throw Refused{};
 }
 
 // New device memory for a call on `stream`.  It comes from that stream's own pool: another
@@ -221,6 +228,7 @@ PyObject *py_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t m = x.size(0);
         const int code = type_code(x, "x");
         const void *px = address(x, x.scalar_type(), {m, w->K}, "x", device);
+        no_gradient(x, "q4_gemm forms no gradient, but x requires one (detach it, or call under torch.no_grad())");
         void *stream = raw_stream(a[4], device);
         const at::Tensor y = output(a[3], {m, w->N}, x.scalar_type(), x, "y", stream);
         void *py = address(y, x.scalar_type(), {m, w->N}, "y", device);
@@ -248,6 +256,8 @@ PyObject *py_route(PyObject *, PyObject *const *a, Py_ssize_t n) {
                    (long long)groups, (long long)keep, (long long)group_top);
         const int device = gpu_of(l, "logits");
         const void *pl = address(l, l.scalar_type(), {t, e}, "logits", device);
+        no_gradient(l, "moe_route records no gradient, but logits require one: it comes from moe_route_backward (call moe_route "
+                       "under torch.no_grad())");
         const void *pb = a[2] == Py_None ? nullptr : address(tensor(a[2], "bias"), at::kFloat, {e}, "bias", device);
         void *stream = raw_stream(a[10], device);
         const at::Tensor idx = output(a[8], {t, k}, at::kInt, l, "idx", stream);
@@ -298,6 +308,8 @@ PyObject *py_moe(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const void *px = address(x, x.scalar_type(), {t, d}, "x", device);
         const void *pi = address(idx, at::kInt, {t, k}, "idx", device);
         const void *pw = address(wts, at::kFloat, {t, k}, "weights", device);
+        no_gradient(x, "q4_moe forms no gradients, but x requires one (detach it, or call under torch.no_grad())");
+        no_gradient(wts, "q4_moe forms no gradients, but weights require one (detach them, or call under torch.no_grad())");
         void *stream = raw_stream(a[8], device);
         const at::Tensor y = output(a[7], {t, d}, x.scalar_type(), x, "y", stream);
         void *py = address(y, x.scalar_type(), {t, d}, "y", device);
