@@ -167,22 +167,11 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     }
     // A row's power of two is the largest of its units'; 512/BM neighbouring threads serve a row.
     constexpr int LANES = 512 / BM;
-    const int16_t *units_exp = nullptr;
-    int row_exp = -126;
-    auto fill_factors = [&](int u0) {
+    auto fill_factors = [&](int u0, int row_exp) {
+        const int16_t *ex = p.hexp + source(tid / LANES) * ku;
         for (int u = u0 + tid % LANES; u < ku && u < u0 + TU; u += LANES)
-            factors[(u - u0) * BM + tid / LANES] = q4_h_factors(row_exp - units_exp[u]);
+            factors[(u - u0) * BM + tid / LANES] = q4_h_factors(row_exp - ex[u]);
     };
-    if constexpr (H16 && MODE == kTDown) {
-        units_exp = p.hexp + source(tid / LANES) * ku;
-        for (int u = tid % LANES; u < ku; u += LANES) row_exp = units_exp[u] > row_exp ? units_exp[u] : row_exp;
-        for (int o = 1; o < LANES; o <<= 1) {
-            const int b = __shfl_xor(row_exp, o);
-            row_exp = b > row_exp ? b : row_exp;
-        }
-        if (tid % LANES == 0) rs[tid / LANES] = __builtin_ldexpf(1.0f, row_exp);
-        fill_factors(0);
-    }
     const _Float16 *ap[PPT];
     int al[PPT];
 #pragma unroll
@@ -305,8 +294,19 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     auto last = [&](int u) { return u < u_end ? u : u_end - 1; };
     load_a(u_begin);
     load_b(0, u_begin);
+    if constexpr (H16 && MODE == kTDown) {  // behind the first loads, on their way
+        const int16_t *ex = p.hexp + source(tid / LANES) * ku;
+        int row_exp = -126;
+        for (int u = tid % LANES; u < ku; u += LANES) row_exp = ex[u] > row_exp ? ex[u] : row_exp;
+        for (int o = 1; o < LANES; o <<= 1) {
+            const int b = __shfl_xor(row_exp, o);
+            row_exp = b > row_exp ? b : row_exp;
+        }
+        if (tid % LANES == 0) rs[tid / LANES] = __builtin_ldexpf(1.0f, row_exp);
+        fill_factors(0, row_exp);
+        __syncthreads();
+    }
     load_b(1, last(u_begin + 1));
-    if constexpr (H16 && MODE == kTDown) __syncthreads();  // the factors
     store_a(0, u_begin);
     load_a(last(u_begin + 1));
     if (late) decode(0);
@@ -324,7 +324,8 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
                 __syncthreads();
                 if constexpr (H16 && MODE == kTDown)
                     if ((u + 2) % TU == 0) {  // the next unit that is stored is the first of others
-                        fill_factors(u + 2);
+                        const float scale = rs[tid / LANES];
+                        fill_factors(u + 2, (int)(__builtin_bit_cast(uint32_t, scale) >> 23) - 127);
                         __syncthreads();
                     }
             }
@@ -335,7 +336,10 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
         const int n = nb[0] * 16 + r;
         uint32_t most[RB * 4];
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
+        for (int rb = 0; rb < RB; ++rb) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) most[rb * 4 + i] = 0;
+            if (rb * 16 >= count) continue;  // the whole wave
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float scale = rs[rb * 16 + 4 * h + i];
@@ -343,6 +347,7 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
                 acc[rb][0][i] = v;
                 most[rb * 4 + i] = __builtin_bit_cast(uint32_t, v) & 0x7fffffffu;  // (of the vector's element it would be element 0's)
             }
+        }
         // the largest of each row: every exchange halves the rows that a lane keeps
         int first = 0;  // its first row, counted as rb * 4 + i
         auto halve = [&](auto exchange, int bit, int keep) {
@@ -371,6 +376,7 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
         if (tid < count) p.hexp[(row0 + tid) * p.tiles_n + tn] = (int16_t)q4_h_exp(hmost[tid]);
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
+            if (rb * 16 >= count) break;
             const int4 bits = *reinterpret_cast<const int4 *>(&hmost[rb * 16 + 4 * h]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
