@@ -1,7 +1,7 @@
 // Python calls of the 4-bit weights and the mixture-of-experts operators.
 //
 // A small kernel takes a few microseconds, as long as a call whose dozen arguments are
-// checked and converted in Python (6.0-7.1 us of host time for one launch; from here 3.2-3.5).
+// checked and converted in Python (6.0-7.1 us of host time for one launch; from here 3.0-3.9).
 // This module checks the tensors of a call, allocates what the caller left out and calls
 // the C entry points, whose addresses `bind` gets from the binding.  Host code only.
 #include <Python.h>

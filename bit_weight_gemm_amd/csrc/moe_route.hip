@@ -25,8 +25,8 @@
 // for one slot about thirty.
 //
 // Bound by instruction issue: 16384 tokens x 256 experts, 8 groups of which 4 stay, bias, 8 chosen:
-// 25 us of kernel (0.7 TB/s), some 600 vector instructions a token; one token 4.7 us, of which an
-// empty launch is two.  The gradient reads and writes its rows once: 8192 x 128 f32 4.4 us (2 TB/s).
+// 24-26 us of kernel (0.7 TB/s), some 600 vector instructions a token; one token 4.4-4.8 us, of which an
+// empty launch is two.  The gradient reads and writes its rows once: 8192 x 128 f32 4.6-5.6 us (2 TB/s).
 #include "q4.h"
 
 namespace tq2 {

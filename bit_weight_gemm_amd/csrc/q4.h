@@ -30,7 +30,7 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
 enum Q4Type { kF32 = 0, kF16 = 1, kBF16 = 2 };
 
-// Bytes before the codes, which nothing reads.
+// Bytes before the codes: unused, kept so that packed weights that a program stored keep their layout.
 inline size_t q4_head_bytes(int64_t E) { return (size_t)(E * 4 + 255) / 256 * 256; }
 
 struct Q4Layout {

@@ -61,9 +61,9 @@ __global__ __launch_bounds__(256) void q4_dequant_kernel(Q4View v, float *out) {
 }
 
 // Column blocks per wave: one while that gives each of the 256 compute units one workgroup
-// at most (N = K = 4096, one row: 5.0 us, with two 5.9), two beyond (N = 5003, sixteen rows: 7.6
+// at most (N = K = 4096, one row: 4.4 us, with two 6.0), two beyond (N = 5003, sixteen rows: 7.5
 // us, with one 8.8), so that x is read less often; four for f32 x beyond two workgroups each (x is
-// split for all columns at once; N = 14336, K = 4096, one row 16.5, with two 20.3 us).
+// split for all columns at once; N = 14336, K = 4096, one row 15.7, with two 20.7 us).
 template <int XT, int G>
 hipError_t dense(const Q4Args &a, hipStream_t s) {
     const int64_t nb = a.w.nb;
@@ -74,7 +74,7 @@ hipError_t dense(const Q4Args &a, hipStream_t s) {
         }
         return run_q4_skinny<XT, G, 1, 2, kDense>(a, 1, s);
     }
-    // up to 32 rows as above (4096 x 4096, 17 rows 8.6 us, with two 9.7); the blocks of more rows fill the units
+    // up to 32 rows as above (4096 x 4096, 17 rows 8.1 us, with two 9.4); the blocks of more rows fill the units
     if (a.M <= 32 && nb <= 256) return run_q4_skinny<XT, G, 2, 1, kDense>(a, 1, s);
     return run_q4_skinny<XT, G, 2, 2, kDense>(a, (a.M + 31) / 32, s);
 }
@@ -117,11 +117,11 @@ struct Deal {
 // and in each so many microseconds a unit of 128 k (without LDS a last round counts half by its
 // workgroups); shares are written and joined at 8 TB/s, with more time for the launch and for rows
 // that are not aligned.
-// f16, 4096 x 4096, estimate against measured: 64 rows skinny 10.8 / 11.3, 128 rows in
-// 8 shares 17.6 / 17.3 (skinny 19.6), 256 rows in 4 shares 23 / 22.6 (skinny 35, one share 41), 512 rows in
-// 2 shares 34 / 35 (one 43), 2048 rows in tiles of 128 67 / 75 (of 64: 93).
+// f16, 4096 x 4096, estimate against measured: 64 rows skinny 10.8 / 11.2, 128 rows in
+// 8 shares 17.6 / 16.7 (skinny 19.5), 256 rows in 4 shares 23 / 21.5 (skinny 35, one share 39), 512 rows in
+// 2 shares 34 / 32 (one 40), 2048 rows in tiles of 128 67 / 72 (of 64: 84).
 Deal deal(int64_t N, int64_t K, int64_t G, int64_t M, int dtype) {
-    if (M <= 32) return Deal{0, 1};  // 4096 x 4096: 11 us, in tiles at least 14
+    if (M <= 32) return Deal{0, 1};  // 4096 x 4096: 10 us, in tiles at least 14
     constexpr double kCus = 256;
     const bool f32 = dtype == kF32, fine = G == 32;
     const double nb = (double)((N + 15) / 16), ku = (double)((K + 127) / 128);

@@ -8,7 +8,7 @@
 // WK waves share a column block and take its units in turn; their sums are added in wave order.
 // Only codes and scales wait in registers, D units ahead: these products wait for
 // memory.  Codes are decoded to code - zero, exact in f16, and each group's sum is scaled in f32.
-// 33 tokens of 32 experts, 4 each, 1024 x 1536, f16: gate and up 15 us (3.6 TB/s of codes and
+// 33 tokens of 32 experts, 4 each, 1024 x 1536, f16: gate and up 15-17 us (3.2-3.6 TB/s of codes and
 // scales), down 12 (2.3 TB/s); a plan, tiles and f32 rows through the skinny kernel took 46 in all.
 // 128 registers let two workgroups share a compute unit, for up to 84 bytes a lane in scratch memory.
 #pragma once

@@ -106,7 +106,7 @@ hipError_t product(const MoePlan &p, const Q4Args &a, hipStream_t s) {
     return run_q4_skinny<XT, 128, 1, 2, MODE>(a, p.max_tiles, s);
 }
 
-// Two column blocks of each product to a workgroup (one token 14.3 us, with one 14.5; 64 slots 46 and 52); two
+// Two column blocks of each product to a workgroup (one token 13.8 us, with one 14.5; 64 slots 45 and 52); two
 // units of codes in flight in either launch.
 template <int XT, int PH>
 hipError_t row_gate_up(const Q4RowArgs &a, int64_t slots, hipStream_t s) {
@@ -220,16 +220,17 @@ hipError_t tiled(const MoePlan &p, const void *x, const float *weights, const Q4
 }  // namespace
 
 // Up to kDirectSlots slots, or up to kDirectSpread while that is no more than one per expert, each reads its
-// expert's weights for itself; their rows have to fit in LDS.  (64 experts, 8 each, 2048 x 1024: 40 slots 33 us,
-// found by their expert's workgroups 50, 64 slots 46 and 65; of 8 experts, 48 slots 28 and 22.)
+// expert's weights for itself; their rows have to fit in LDS.  (64 experts, 8 each, 2048 x 1024: 40 slots 32 us,
+// found by their expert's workgroups 50, 64 slots 45 and 63; of 8 experts, 48 slots 21 and 17.)
 // Beyond, by slots per expert (bf16; 64 experts of 8, 2048 x 1024: "large", 8 experts of 2, 1024 x 1024:
 // "small", which tiles of the gate product cannot fill the 256 compute units with):
-//   up to 8 (4 if small): workgroups find their slots (large, 64 tokens: 101 us, tiles of 64 rows
-//     110; small, 33 tokens: 30, rows of 16 24);
-//   up to 48, small: plan and blocks of 16 rows (128 tokens 39, tiles of 64 43, of 32-row blocks 36);
-//   then tiles of 64 rows (large, 100 tokens: 116, found slots 139; 256 tokens 135, rows of 32 240;
-//     small, 256 tokens 45, rows of 16 60);
-//   from 256 on tiles of 128 (large, 2048 tokens: 399, of 64 414; f32 629, of 64 591: not for f32).
+//   up to 8 (4 if small): workgroups find their slots (large, 64 tokens: 93 us, tiles of 64 rows
+//     122; small, 33 tokens: 22, rows of 16 20);
+//   up to 48, small: plan and blocks of 16 rows (33 tokens 20, tiles of 64 35; 128 tokens 35 and 36);
+//   then tiles of 64 rows (large, 128 tokens: 122, found slots 145; 256 tokens 126, rows of 16 207;
+//     small, 256 tokens 37, rows of 16 54);
+//   from 256 on tiles of 128 (large, 2048 tokens: 392, of 64 408; 1024 tokens 259 and 244).  f32, 598, has
+//     tiles of 64 only: its two planes were slower in tiles of 128 (629 against 591).
 constexpr int64_t kDirectSlots = 32, kDirectSpread = 64;
 constexpr size_t kDirectLds = 48 * 1024;
 

@@ -9,8 +9,8 @@
 // codes in flight: these products wait for memory, not for the matrix unit.
 // Decode, correction and the treatment of infinities are q4_skinny.h's.
 //
-// Bound by latency: 8 of 64 experts for one token, 2048 x 1024, 6.5 us for gate and up (16.8 MB of
-// codes, 2.6 TB/s) and 6.5 for down, of which an empty launch is about two each.
+// Bound by latency: 8 of 64 experts for one token, 2048 x 1024, 6.4-7.5 us for gate and up (16.8 MB of
+// codes, 2.2-2.6 TB/s) and 6.0-7.1 for down, of which an empty launch is about two each.
 #pragma once
 
 #include "q4_skinny.h"

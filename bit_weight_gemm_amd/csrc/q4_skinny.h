@@ -28,9 +28,9 @@
 // (q4_slow_dot): the correction makes Inf - Inf of an infinite x, where the sum itself
 // may be an infinity of one sign.
 //
-// Bound by the loads' latency and their number in flight: one row, 4096 x 4096, bf16, 4.4 us of
-// kernel (2.0 TB/s; a copy of gigabytes reaches 4.8), eight rows, 14336 x 4096, G = 32, f16, 10.9 us
-// (3.2 TB/s); 23 f32 rows, 5003 x 4000, 17 us, where the split of x and the exact decode
+// Bound by the loads' latency and their number in flight: one row, 4096 x 4096, bf16, 3.7-4.8 us of
+// kernel (2 TB/s; a copy of gigabytes reaches 4.8), eight rows, 14336 x 4096, G = 32, f16, 11-12 us
+// (3.1 TB/s); 23 f32 rows, 5003 x 4000, 17 us, where the split of x and the exact decode
 // count.  Rows that M does not have are not loaded (eight rows 12.5 -> 11.3 us).
 #pragma once
 

@@ -11,13 +11,16 @@
 // The codes are decoded to code - zero, exact in f16, and each group's sum is scaled in f32:
 // acc += scale * part.  Products are exact for f16 x.  bfloat16 rows are
 // brought to f16 by a power of two per row (their 8 bits fit; see q4_prep.h), and f32 rows
-// to two f16 parts.
+// to two f16 parts.  silu(g) u of 16-bit rows is held in f16 under a power of two per row and 128
+// columns, from its largest value there; the down product brings a row's parts under one power of two.
 //
-// Bound by the matrix unit and the waits around it: 2048 x 4096 x 4096, G = 128 takes 69-72
-// us (0.95-1.0 PFLOP/s; bfloat16 8 more for the planes), with the matrix unit busy 44% of the time,
-// LDS 28%, waves at a wait or barrier 35%.  Tried without gain: the next unit's codes decoded between
-// this one's products (79.5 against 78 us for f16 x), workgroups of four waves, two to a compute unit
-// (94 against 79 us; with G = 32 it gains 9%), halves of a tile for an expert's last rows (scratch).
+// Bound by the matrix unit and the waits around it: 2048 x 4096 x 4096, G = 128 takes 69-76
+// us (0.9-1.0 PFLOP/s; bfloat16 8 more for the planes), with the matrix unit busy 44% of the time,
+// LDS 28%, waves at a wait or barrier 35%.  64 experts of 8, 2048 tokens, 2048 x 1024: gate and up 214-224 us (busy
+// 40%), down 137-140 (31%; eight units to a tile, and some 5 us for the rows' powers of two).
+// Tried without gain: the next unit's codes decoded between this one's products (79.5 against 78 us for
+// f16 x), workgroups of four waves, two to a compute unit (94 against 79 us; with G = 32 it gains 9%), halves of
+// a tile for an expert's last rows (scratch).
 #pragma once
 
 #include <type_traits>
