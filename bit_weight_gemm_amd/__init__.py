@@ -14,9 +14,10 @@ blr_saved_size, blr_workspace_size,
 blr_backward_workspace_size, tq2_workspace_allocs, tq2_select_path,
 tq2_set_path, tq2_set_m_small, tq2_strerror, tq2_version; and in include/libtq2_moe.h:
 q4_upload (packs into memory of its own), q4_gemm, q4_dequant, moe_route,
-moe_route_backward and q4_moe.  The last three and q4_gemm go through a compiled
-module (csrc/binding.cpp): beside their kernels' few microseconds, checks and
-conversions in Python would be the larger part.
+moe_route_backward and q4_moe; and in include/libtq2_block.h: q4_linear, moe_layer,
+block_norm and block_norm_backward.  These and the last three and q4_gemm go through
+a compiled module (csrc/binding.cpp): beside their kernels' few microseconds, checks
+and conversions in Python would be the larger part.
 
 No call records anything for autograd: gradients come from the backward calls.
 
@@ -112,6 +113,12 @@ def lib():
         "moe_route_backward": ([p, p, p, p, i64, i64, i64, i32, i32, i32, p], i32),
         "q4_moe_workspace_size": ([i64, i64, i64, i64, i64, i32], sz),
         "q4_moe": ([p, p, p, p, p, p, p, i64, i64, i32, p, sz, p], i32),
+        "q4_linear": ([p, p, p, i32, i32, p, p, i64, i32, p, sz, p], i32),
+        "moe_layer_workspace_size": ([i64, i64, i64, i64, i64, i32, i32], sz),
+        "moe_layer": ([p, p, sz, p], i32),
+        "block_norm": ([p, p], i32),
+        "block_norm_backward_workspace_size": ([i64, i64, i64, i32], sz),
+        "block_norm_backward": ([p, p, sz, p], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -120,7 +127,9 @@ def lib():
     from . import _binding as calls
 
     calls.bind(*(ctypes.cast(f, p).value for f in (L.q4_gemm_workspace_size, L.q4_gemm, L.moe_route, L.moe_route_backward,
-                                                   L.q4_moe_workspace_size, L.q4_moe)))
+                                                   L.q4_moe_workspace_size, L.q4_moe, L.q4_linear,
+                                                   L.moe_layer_workspace_size, L.moe_layer, L.block_norm,
+                                                   L.block_norm_backward_workspace_size, L.block_norm_backward)))
     _lib, _compiled = L, calls
     return L
 
@@ -573,6 +582,24 @@ def q4_gemm(w: Q4Weight, x, y=None, stream=None):
     return out
 
 
+_ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def q4_linear(w: Q4Weight, x, bias=None, activation=None, residual=None, y=None, stream=None):
+    """y = act(x @ W^T + bias) + residual in x's type (float32, float16 or bfloat16), rounded once: x [M][K], bias [N]
+    (float32 or x's type), activation None, "relu", "gelu", "gelu_tanh" or "silu", residual [M][N] in x's type; returns
+    y [M][N] (allocated if None; it may be the residual itself)."""
+    if w.E is not None:
+        raise ValueError("q4_linear takes a weight without an axis of experts")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None, 'relu', 'gelu', 'gelu_tanh' or 'silu', got {activation!r}")
+    out = (_compiled or _calls()).linear(w.handle, w.device, x, bias, _ACTIVATIONS[activation], residual, y,
+                                        stream if stream is None else _for(stream, w.data, x, bias, residual, y))
+    if out.__class__ is int:
+        _check(out, "q4_linear")
+    return out
+
+
 def _score(score):
     if score not in _SCORES:
         raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
@@ -602,19 +629,82 @@ def moe_route_backward(logits, idx, dw, score="softmax", renorm=False, dlogits=N
     return out
 
 
-def q4_moe(x, idx, weights, gate: Q4Weight, up: Q4Weight, down: Q4Weight, y=None, stream=None):
-    """Experts' gated products, y[t] = sum_j weights[t][j] * down_e(silu(gate_e x_t) * (up_e x_t)) with e = idx[t][j]:
-    x [T][d] (float32, float16 or bfloat16), idx int32 [T][k] (entries outside 0 .. E-1 are dropped), weights float32
-    [T][k], gate and up [E][f][d], down [E][d][f]; returns y [T][d] in x's type (allocated if None)."""
+def _experts(gate, up, down, what):
+    """The three weights of a mixture's experts fit each other."""
     if gate.E is None or up.E is None or down.E is None:
-        raise ValueError("q4_moe takes weights with an axis of experts")
+        raise ValueError(f"{what} takes weights with an axis of experts")
     if up.like != gate.like or (down.E, down.N, down.K) != (gate.E, gate.K, gate.N):
         raise ValueError(f"gate and up must be alike and down [{gate.E}, {gate.K}, {gate.N}]")
     if up.device != gate.device or down.device != gate.device:
         raise ValueError("the weights are on different devices")
+
+
+def q4_moe(x, idx, weights, gate: Q4Weight, up: Q4Weight, down: Q4Weight, y=None, stream=None):
+    """Experts' gated products, y[t] = sum_j weights[t][j] * down_e(silu(gate_e x_t) * (up_e x_t)) with e = idx[t][j]:
+    x [T][d] (float32, float16 or bfloat16), idx int32 [T][k] (entries outside 0 .. E-1 are dropped), weights float32
+    [T][k], gate and up [E][f][d], down [E][d][f]; returns y [T][d] in x's type (allocated if None)."""
+    _experts(gate, up, down, "q4_moe")
     out = (_compiled or _calls()).moe(x, idx, weights, gate.handle, up.handle, down.handle, gate.device, y,
                                      stream if stream is None else
                                      _for(stream, x, idx, weights, gate.data, up.data, down.data, y))
     if out.__class__ is int:
         _check(out, "q4_moe")
+    return out
+
+
+def moe_layer(x, router, gate: Q4Weight, up: Q4Weight, down: Q4Weight, k, norm=None, eps=1e-6, bias=None, score="softmax",
+              groups=1, keep=1, group_top=1, renorm=False, residual=None, y=None, idx=None, weights=None, stream=None):
+    """A whole mixture-of-experts layer: n = x / rms(x) * norm rounded to x's type (x itself without a norm), logits = n @
+    router^T summed in 64 bits and rounded to float32, experts and weights as moe_route chooses them from those logits (bias,
+    score, groups, keep, group_top, renorm: see there), y = residual + the chosen experts' weighted products as q4_moe's.
+    x [T][d] (float32, float16 or bfloat16), norm [d] and router [E][d] float32 or x's type, residual [T][d] in x's type,
+    gate and up [E][f][d], down [E][d][f]; returns (y [T][d], idx int32 [T][k], weights float32 [T][k]), allocated if None.  y may
+    be the residual itself."""
+    _experts(gate, up, down, "moe_layer")
+    out = (_compiled or _calls()).layer(x, router, gate.handle, up.handle, down.handle, gate.device, k, norm, eps, bias,
+                                       _score(score), groups, keep, group_top, renorm, residual, y, idx, weights,
+                                       stream if stream is None else
+                                       _for(stream, x, router, norm, bias, residual, gate.data, up.data, down.data, y, idx,
+                                            weights))
+    if out.__class__ is int:
+        _check(out, "moe_layer")
+    return out
+
+
+# ---------------------------------------------------------------- norms around a block
+
+_NORMS = {"rms": False, "layer": True}
+
+
+def _norm(kind):
+    if kind not in _NORMS:
+        raise ValueError(f"kind must be 'rms' or 'layer', got {kind!r}")
+    return _NORMS[kind]
+
+
+def block_norm(x, b=None, post=None, post_bias=None, gate=None, scale=1.0, pre=None, pre_bias=None, kind="rms", eps=1e-6,
+               y=None, n=None, stream=None):
+    """The norms after and before a block, with its gate and residual scale: u = norm(b) * post + post_bias (b itself
+    without post), y = x + scale * gate * u rounded to its type (x itself without b), n = norm(y) * pre + pre_bias (None without
+    pre); norm(v) = v / sqrt(mean(v^2) + eps) ("rms") or (v - mean) / sqrt(var + eps) ("layer").  x and b [M][N] (float32,
+    float16 or bfloat16), post, pre and their biases [N] and gate [R][N] all float32 or all x's type; row m has gate row
+    m // (M / R).  Returns (y, n), allocated if None."""
+    out = (_compiled or _calls()).block(x, b, post, post_bias, gate, pre, pre_bias, scale, _norm(kind), eps, y, n,
+                                       stream if stream is None else
+                                       _for(stream, x, b, post, post_bias, gate, pre, pre_bias, y, n))
+    if out.__class__ is int:
+        _check(out, "block_norm")
+    return out
+
+
+def block_norm_backward(dy, y, dn=None, b=None, post=None, post_bias=None, gate=None, scale=1.0, pre=None, pre_bias=None,
+                        kind="rms", eps=1e-6, dx=None, db=None, stream=None):
+    """Gradient of block_norm from those of y and n (dy None: 0) and its arguments; y: the rows that it gave (x where there is
+    no b; not looked at without pre).  Returns a dict: dx and db (where there is a b; both in the rows' type, allocated if
+    None), and float32 sums for the parameters that were given, dgate [R][N], dpost, dpost_bias, dpre, dpre_bias [N]."""
+    out = (_compiled or _calls()).block_backward(dy, y, dn, b, post, post_bias, gate, pre, pre_bias, scale, _norm(kind), eps,
+                                                dx, db, stream if stream is None else
+                                                _for(stream, dy, y, dn, b, post, post_bias, gate, pre, pre_bias, dx, db))
+    if out.__class__ is int:
+        _check(out, "block_norm_backward")
     return out

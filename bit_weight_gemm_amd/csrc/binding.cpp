@@ -1,4 +1,4 @@
-// Python calls of the 4-bit weights and the mixture-of-experts operators.
+// Python calls of the 4-bit weights, the mixture-of-experts operators and a block's norms.
 //
 // A small kernel takes a few microseconds, as long as a call whose dozen arguments are
 // checked and converted in Python (6.0-7.1 us of host time for one launch; from here 3.0-3.9).
@@ -13,7 +13,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include "../../include/libtq2_moe.h"
+#include <array>
+
+#include "../../include/libtq2_block.h"
 
 namespace {
 
@@ -23,6 +25,12 @@ decltype(&moe_route) p_route;
 decltype(&moe_route_backward) p_route_backward;
 decltype(&q4_moe_workspace_size) p_moe_ws;
 decltype(&q4_moe) p_moe;
+decltype(&q4_linear) p_linear;
+decltype(&moe_layer_workspace_size) p_layer_ws;
+decltype(&moe_layer) p_layer;
+decltype(&block_norm) p_block;
+decltype(&block_norm_backward_workspace_size) p_block_backward_ws;
+decltype(&block_norm_backward) p_block_backward;
 
 struct Refused {};  // a Python error is set
 
@@ -177,7 +185,7 @@ PyObject *guarded(F &&body) {
 
 PyObject *py_bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
-        count(n, 6);
+        count(n, 12);
         auto at = [&](int i) { return PyLong_AsVoidPtr(a[i]); };
         p_gemm_ws = reinterpret_cast<decltype(p_gemm_ws)>(at(0));
         p_gemm = reinterpret_cast<decltype(p_gemm)>(at(1));
@@ -185,6 +193,12 @@ PyObject *py_bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
         p_route_backward = reinterpret_cast<decltype(p_route_backward)>(at(3));
         p_moe_ws = reinterpret_cast<decltype(p_moe_ws)>(at(4));
         p_moe = reinterpret_cast<decltype(p_moe)>(at(5));
+        p_linear = reinterpret_cast<decltype(p_linear)>(at(6));
+        p_layer_ws = reinterpret_cast<decltype(p_layer_ws)>(at(7));
+        p_layer = reinterpret_cast<decltype(p_layer)>(at(8));
+        p_block = reinterpret_cast<decltype(p_block)>(at(9));
+        p_block_backward_ws = reinterpret_cast<decltype(p_block_backward_ws)>(at(10));
+        p_block_backward = reinterpret_cast<decltype(p_block_backward)>(at(11));
         if (PyErr_Occurred()) throw Refused{};
         Py_RETURN_NONE;
     });
@@ -327,6 +341,244 @@ PyObject *py_moe(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+double real(PyObject *o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Refused{};
+    return v;
+}
+
+// Address of a tensor that a call may go without (None: nullptr).
+void *maybe(PyObject *o, at::ScalarType type, at::IntArrayRef shape, const char *name, int device) {
+    return o == Py_None ? nullptr : address(tensor(o, name), type, shape, name, device);
+}
+
+// A parameter vector, of float32 or the rows' type; `code` is set to its type.
+void *side(PyObject *o, const at::Tensor &rows, at::IntArrayRef shape, const char *name, int device, int &code) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = tensor(o, name);
+    if (t.scalar_type() != at::kFloat && t.scalar_type() != rows.scalar_type())
+        refuse(PyExc_TypeError, "%s must be torch.float32 or %s, got %s", name, name_of(rows.scalar_type()), name_of(t.scalar_type()));
+    code = type_code(t, name);
+    return address(t, t.scalar_type(), shape, name, device);
+}
+
+void no_gradient(PyObject *o, const char *name, const char *what) {
+    if (o != Py_None) no_gradient(tensor(o, name), what);
+}
+
+// linear(handle, device, x, bias, activation, residual, y, stream)
+PyObject *py_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        count(n, 8);
+        const q4_weight *w = weight(a[0]);
+        const int device = (int)number(a[1]), act = (int)number(a[4]);
+        const at::Tensor &x = tensor(a[2], "x");
+        if (x.dim() != 2) refuse(PyExc_ValueError, "x must be [M, %lld]", (long long)w->K);
+        const int64_t m = x.size(0);
+        const int code = type_code(x, "x");
+        int bias_code = code;
+        const void *px = address(x, x.scalar_type(), {m, w->K}, "x", device);
+        const void *pb = side(a[3], x, {w->N}, "bias", device, bias_code);
+        const void *pr = maybe(a[5], x.scalar_type(), {m, w->N}, "residual", device);
+        constexpr const char *kNo = "q4_linear forms no gradient, but an argument requires one (detach it, or call under torch.no_grad())";
+        no_gradient(x, kNo), no_gradient(a[3], "bias", kNo), no_gradient(a[5], "residual", kNo);
+        void *stream = raw_stream(a[7], device);
+        const at::Tensor y = output(a[6], {m, w->N}, x.scalar_type(), x, "y", stream);
+        void *py = address(y, x.scalar_type(), {m, w->N}, "y", device);
+        const size_t need = p_gemm_ws(w, m, code);
+        at::Tensor ws;
+        if (need) ws = scratch(need, x, stream);
+        void *pw = need ? ws.data_ptr() : nullptr;
+        return result(call([&] { return p_linear(w, px, pb, bias_code, act, pr, py, m, code, pw, need, stream); }), y);
+    });
+}
+
+// layer(x, router, gate, up, down, device, k, norm, eps, bias, score, groups, keep, group_top, renorm, residual, y, idx, weights,
+//       stream): handles of the three weights
+PyObject *py_layer(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        count(n, 20);
+        const at::Tensor &x = tensor(a[0], "x");
+        moe_layer_call c{};
+        c.gate = weight(a[2]), c.up = weight(a[3]), c.down = weight(a[4]);
+        const int device = (int)number(a[5]);
+        const int64_t e = c.gate->E, f = c.gate->N, d = c.gate->K;
+        if (x.dim() != 2) refuse(PyExc_ValueError, "x must be [T, %lld]", (long long)d);
+        const int64_t t = x.size(0);
+        c.T = t, c.k = number(a[6]), c.groups = number(a[11]), c.keep = number(a[12]), c.group_top = number(a[13]);
+        c.score = (int)number(a[10]), c.renorm = truth(a[14]), c.dtype = type_code(x, "x"), c.eps = real(a[8]);
+        if (c.k < 1 || c.k > e || c.k > 64)
+            refuse(PyExc_ValueError, "k must lie between 1 and %lld, got %lld", (long long)(e < 64 ? e : 64), (long long)c.k);
+        if (c.groups < 1 || c.groups > 64 || e % c.groups || c.keep < 1 || c.keep > c.groups || c.group_top < 1 || c.group_top > 2)
+            refuse(PyExc_ValueError, "no routing over E=%lld, groups=%lld, keep=%lld, group_top=%lld", (long long)e,
+                   (long long)c.groups, (long long)c.keep, (long long)c.group_top);
+        const at::ScalarType type = x.scalar_type();
+        c.x = address(x, type, {t, d}, "x", device);
+        if (a[1] == Py_None) refuse(PyExc_TypeError, "router must be a tensor on the GPU%s", "");
+        c.router = side(a[1], x, {e, d}, "router", device, c.router_dtype);
+        c.norm = side(a[7], x, {d}, "norm", device, c.norm_dtype);
+        c.bias = static_cast<const float *>(maybe(a[9], at::kFloat, {e}, "bias", device));
+        c.residual = maybe(a[15], type, {t, d}, "residual", device);
+        constexpr const char *kNo = "moe_layer forms no gradients, but an argument requires one (detach it, or call under torch.no_grad())";
+        no_gradient(x, kNo), no_gradient(a[1], "router", kNo), no_gradient(a[7], "norm", kNo);
+        no_gradient(a[9], "bias", kNo), no_gradient(a[15], "residual", kNo);
+        void *stream = raw_stream(a[19], device);
+        const at::Tensor y = output(a[16], {t, d}, type, x, "y", stream);
+        const at::Tensor idx = output(a[17], {t, c.k}, at::kInt, x, "idx", stream);
+        const at::Tensor wts = output(a[18], {t, c.k}, at::kFloat, x, "weights", stream);
+        c.y = address(y, type, {t, d}, "y", device);
+        c.idx = static_cast<int32_t *>(address(idx, at::kInt, {t, c.k}, "idx", device));
+        c.weights = static_cast<float *>(address(wts, at::kFloat, {t, c.k}, "weights", device));
+        const size_t need = p_layer_ws(t, c.k, e, d, f, c.dtype, c.norm != nullptr);
+        if (need == 0)
+            refuse(PyExc_ValueError, "no layer for T=%lld, k=%lld, E=%lld, d=%lld, f=%lld", (long long)t, (long long)c.k,
+                   (long long)e, (long long)d, (long long)f);
+        const at::Tensor ws = scratch(need, x, stream);
+        void *pws = ws.data_ptr();
+        const int st = call([&] { return p_layer(&c, pws, need, stream); });
+        if (st) return PyLong_FromLong(st);
+        return Py_BuildValue("NNN", THPVariable_Wrap(y), THPVariable_Wrap(idx), THPVariable_Wrap(wts));
+    });
+}
+
+// The norms' parameters, all of one type: [N], the gate [R, N].
+struct Parameters {
+    const void *at[5];  // post, post_bias, gate, pre, pre_bias
+    int64_t rows = 1;   // R
+    int code = -1;
+    Parameters(PyObject *const *a, const at::Tensor &x, int device) {
+        constexpr const char *names[5] = {"post", "post_bias", "gate", "pre", "pre_bias"};
+        const int64_t m = x.size(0), n = x.size(1);
+        for (int i = 0; i < 5; ++i) {
+            at[i] = nullptr;
+            if (a[i] == Py_None) continue;
+            const at::Tensor &t = tensor(a[i], names[i]);
+            int mine = 0;
+            if (i == 2) {
+                if (t.dim() != 2 || t.size(0) < 1 || (m % t.size(0)))
+                    refuse(PyExc_ValueError, "gate must be [R, %lld], where R divides %lld rows", (long long)n, (long long)m);
+                rows = t.size(0);
+                at[i] = side(a[i], x, {rows, n}, names[i], device, mine);
+            } else {
+                at[i] = side(a[i], x, {n}, names[i], device, mine);
+            }
+            if (code >= 0 && mine != code)
+                refuse(PyExc_TypeError, "%s must have the type of the other norms' weights and the gate", names[i]);
+            code = mine;
+        }
+        if (code < 0) code = type_code(x, "x");
+    }
+};
+
+// Rows without gradient; x [M, N] on a GPU.
+int64_t norm_rows(const at::Tensor &x, const char *name) {
+    if (x.dim() != 2) refuse(PyExc_ValueError, "%s must be [M, N]", name);
+    if (x.size(1) < 1 || x.size(1) > 16384)
+        refuse(PyExc_ValueError, "rows must have 1 to 16384 columns, got %lld", (long long)x.size(1));
+    return x.size(0);
+}
+
+// block(x, b, post, post_bias, gate, pre, pre_bias, scale, layer, eps, y, n, stream)
+PyObject *py_block(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        count(n, 13);
+        const at::Tensor &x = tensor(a[0], "x");
+        block_norm_call c{};
+        const int64_t m = norm_rows(x, "x"), cols = x.size(1);
+        const int device = gpu_of(x, "x");
+        const at::ScalarType type = x.scalar_type();
+        c.dtype = type_code(x, "x");
+        c.x = address(x, type, {m, cols}, "x", device);
+        c.b = maybe(a[1], type, {m, cols}, "b", device);
+        const Parameters p(a + 2, x, device);
+        c.post = p.at[0], c.post_bias = p.at[1], c.gate = p.at[2], c.pre = p.at[3], c.pre_bias = p.at[4];
+        c.M = m, c.N = cols, c.R = p.rows, c.weights_dtype = p.code;
+        c.scale = (float)real(a[7]), c.layer = truth(a[8]), c.eps = real(a[9]);
+        const bool b = a[1] != Py_None, pre = a[5] != Py_None;  // (tensors without rows have no address)
+        if (!b && (c.post || c.gate || a[10] != Py_None)) refuse(PyExc_ValueError, "post, gate and y go with b%s", "");
+        if ((!c.post && c.post_bias) || (!pre && (c.pre_bias || a[11] != Py_None)))
+            refuse(PyExc_ValueError, "post_bias goes with post, pre_bias and n with pre%s", "");
+        if (!b && !pre) refuse(PyExc_ValueError, "there is neither b nor pre: nothing to do%s", "");
+        constexpr const char *kNo = "block_norm records no gradient, but an argument requires one: it comes from block_norm_backward "
+                                    "(call block_norm under torch.no_grad())";
+        constexpr const char *names[7] = {"x", "b", "post", "post_bias", "gate", "pre", "pre_bias"};
+        for (int i = 0; i < 7; ++i) no_gradient(a[i], names[i], kNo);
+        void *stream = raw_stream(a[12], device);
+        at::Tensor y, out;
+        if (b) {
+            y = output(a[10], {m, cols}, type, x, "y", stream);
+            c.y = address(y, type, {m, cols}, "y", device);
+        }
+        if (pre) {
+            out = output(a[11], {m, cols}, type, x, "n", stream);
+            c.n = address(out, type, {m, cols}, "n", device);
+        }
+        const int st = call([&] { return p_block(&c, stream); });
+        if (st) return PyLong_FromLong(st);
+        PyObject *first = THPVariable_Wrap(b ? y : x);
+        if (pre) return Py_BuildValue("NN", first, THPVariable_Wrap(out));
+        return Py_BuildValue("NO", first, Py_None);
+    });
+}
+
+// block_backward(dy, y, dn, b, post, post_bias, gate, pre, pre_bias, scale, layer, eps, dx, db, stream): a dict
+PyObject *py_block_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        count(n, 15);
+        if (a[0] == Py_None && a[2] == Py_None) refuse(PyExc_ValueError, "there is neither dy nor dn%s", "");
+        const at::Tensor &x = a[0] == Py_None ? tensor(a[2], "dn") : tensor(a[0], "dy");
+        block_norm_backward_call c{};
+        const int64_t m = norm_rows(x, "dy"), cols = x.size(1);
+        const int device = gpu_of(x, "dy");
+        const at::ScalarType type = x.scalar_type();
+        c.dtype = type_code(x, "dy");
+        const std::array<int64_t, 2> rows{m, cols};
+        c.dy = maybe(a[0], type, rows, "dy", device), c.dn = maybe(a[2], type, rows, "dn", device);
+        c.b = maybe(a[3], type, rows, "b", device);
+        const Parameters p(a + 4, x, device);
+        c.post = p.at[0], c.post_bias = p.at[1], c.gate = p.at[2], c.pre = p.at[3], c.pre_bias = p.at[4];
+        c.M = m, c.N = cols, c.R = p.rows, c.weights_dtype = p.code;
+        c.scale = (float)real(a[9]), c.layer = truth(a[10]), c.eps = real(a[11]);
+        const bool b = a[3] != Py_None, pre = a[7] != Py_None;
+        if (!b && (c.post || c.gate || a[13] != Py_None)) refuse(PyExc_ValueError, "post, gate and db go with b%s", "");
+        if ((!c.post && c.post_bias) || (!pre && c.pre_bias) || pre != (a[2] != Py_None))
+            refuse(PyExc_ValueError, "post_bias goes with post, dn and pre_bias with pre%s", "");
+        if (pre && a[1] == Py_None) refuse(PyExc_ValueError, "y (x, where there is no b) is needed with pre%s", "");
+        if (pre) c.y = address(tensor(a[1], "y"), type, rows, "y", device);
+        void *stream = raw_stream(a[14], device);
+        std::array<std::pair<const char *, at::Tensor>, 7> outs;
+        int used = 0;
+        auto rows_out = [&](PyObject *given, const char *name) {
+            outs[used] = {name, output(given, rows, type, x, name, stream)};
+            return address(outs[used++].second, type, rows, name, device);
+        };
+        auto sums_out = [&](const void *of, at::IntArrayRef shape, const char *name) -> float * {
+            if (!of) return nullptr;
+            outs[used] = {name, output(Py_None, shape, at::kFloat, x, name, stream)};
+            return static_cast<float *>(outs[used++].second.data_ptr());
+        };
+        c.dx = rows_out(a[12], "dx");
+        if (b) c.db = rows_out(a[13], "db");
+        c.dgate = sums_out(c.gate, {c.R, cols}, "dgate");
+        c.dpost = sums_out(c.post, {cols}, "dpost"), c.dpost_bias = sums_out(c.post_bias, {cols}, "dpost_bias");
+        c.dpre = sums_out(c.pre, {cols}, "dpre"), c.dpre_bias = sums_out(c.pre_bias, {cols}, "dpre_bias");
+        const size_t need = p_block_backward_ws(m, cols, c.R, c.dtype);
+        at::Tensor ws;
+        if (need) ws = scratch(need, x, stream);
+        void *pw = need ? ws.data_ptr() : nullptr;
+        int st = call([&] { return p_block_backward(&c, pw, need, stream); });
+        if (st) return PyLong_FromLong(st);
+        PyObject *d = PyDict_New();
+        for (int i = 0; d && i < used; ++i) {
+            PyObject *v = THPVariable_Wrap(outs[i].second);
+            const int bad = !v || PyDict_SetItemString(d, outs[i].first, v);
+            Py_XDECREF(v);
+            if (bad) Py_CLEAR(d);
+        }
+        return d;
+    });
+}
+
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL
 PyMethodDef methods[] = {{"bind", FAST(py_bind), nullptr},
                          {"address", FAST(py_address), nullptr},
@@ -335,6 +587,10 @@ PyMethodDef methods[] = {{"bind", FAST(py_bind), nullptr},
                          {"route", FAST(py_route), nullptr},
                          {"route_backward", FAST(py_route_backward), nullptr},
                          {"moe", FAST(py_moe), nullptr},
+                         {"linear", FAST(py_linear), nullptr},
+                         {"layer", FAST(py_layer), nullptr},
+                         {"block", FAST(py_block), nullptr},
+                         {"block_backward", FAST(py_block_backward), nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

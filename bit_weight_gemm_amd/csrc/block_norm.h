@@ -1,0 +1,219 @@
+// Rows in registers and their sums: what the norms of a block and a mixture layer's router share (gfx950).
+#pragma once
+
+#include <type_traits>
+
+#include "q4.h"
+
+namespace tq2 {
+
+// ---- sums over a wave or a workgroup, the same bits in every lane
+
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_mov_dpp((int)b, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// v of both lanes of each exchanged pair, added
+__device__ __forceinline__ double add16(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const auto l = __builtin_amdgcn_permlane16_swap((unsigned)b, (unsigned)b, false, false);
+    const auto h = __builtin_amdgcn_permlane16_swap((unsigned)(b >> 32), (unsigned)(b >> 32), false, false);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)h[0] << 32 | (uint32_t)l[0]) +
+           __builtin_bit_cast(double, (uint64_t)(uint32_t)h[1] << 32 | (uint32_t)l[1]);
+}
+__device__ __forceinline__ double add32(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const auto l = __builtin_amdgcn_permlane32_swap((unsigned)b, (unsigned)b, false, false);
+    const auto h = __builtin_amdgcn_permlane32_swap((unsigned)(b >> 32), (unsigned)(b >> 32), false, false);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)h[0] << 32 | (uint32_t)l[0]) +
+           __builtin_bit_cast(double, (uint64_t)(uint32_t)h[1] << 32 | (uint32_t)l[1]);
+}
+__device__ __forceinline__ double wave_total(double v) {
+    v += dpp64<0xB1>(v);   // lane ^ 1
+    v += dpp64<0x4E>(v);   // lane ^ 2
+    v += dpp64<0x141>(v);  // mirrored in eight lanes
+    v += dpp64<0x140>(v);  // mirrored in sixteen
+    return add32(add16(v));
+}
+__device__ __forceinline__ float wave_total(float v) {
+    v = row16_sum(v);
+    float a = v, b = v;
+    swap16(a, b);
+    v = a + b;
+    a = v, b = v;
+    swap32(a, b);
+    return a + b;
+}
+
+// Sums of v[0 .. K-1] over the TPR threads of a row (whole waves; TPR 64: the wave's own).  `room` [TPR / 64][K] is
+// another one at each of two sums in a row, so that one barrier is enough.
+template <int TPR, int K, typename F>
+__device__ __forceinline__ void row_total(F (&v)[K], F *room) {
+#pragma unroll
+    for (int q = 0; q < K; ++q) v[q] = wave_total(v[q]);
+    if constexpr (TPR > 64) {
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int q = 0; q < K; ++q) room[wave * K + q] = v[q];
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < K; ++q) {
+            F s = 0;
+#pragma unroll
+            for (int w = 0; w < TPR / 64; ++w) s += room[w * K + q];
+            v[q] = s;
+        }
+    }
+}
+
+// ---- a thread's piece of a row: 16 bytes, V elements from column `at` on
+
+template <int DT>
+constexpr int kPiece = DT == kF32 ? 4 : 8;
+
+// How a piece that does not lie within the row's N columns is read: kWhole: there is none but empty ones (N is a
+// multiple of V); kTail: the last one is read up to the row's end and shifted (N >= V); kShort: element by element.
+enum PieceMode { kWhole = 0, kTail = 1, kShort = 2 };
+
+// V elements of type DT, any alignment of an element's.
+template <int DT, int V>
+struct Raw {
+    w4 v[V * (DT == kF32 ? 4 : 2) / 16];
+};
+template <int DT, int V>
+__device__ __forceinline__ void raw_values(const Raw<DT, V> &r, float (&out)[V]) {
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+        if constexpr (DT == kF32) {
+            const uint32_t b = r.v[q >> 2][q & 3];
+            out[q] = __builtin_bit_cast(float, b);
+        } else {
+            const uint32_t w = r.v[q >> 3][(q >> 1) & 3];
+            if constexpr (DT == kF16) out[q] = half_bits(q & 1 ? w >> 16 : w);
+            else out[q] = __builtin_bit_cast(float, q & 1 ? w & 0xffff0000u : w << 16);
+        }
+    }
+}
+
+// The piece's place in a row of N columns.
+template <int V, int MODE>
+struct Piece {
+    int at, left;  // first column; columns from there on (<= 0: none)
+    __device__ Piece(int piece, int N) : at(piece * V), left(N - piece * V) {}
+    __device__ bool full() const { return left >= V; }
+    __device__ bool any() const { return left > 0; }
+
+    template <int DT>
+    __device__ __forceinline__ void load(const void *p, int64_t row, int N, Raw<DT, V> &r) const {
+        constexpr int S = DT == kF32 ? 4 : 2;
+        const char *b = static_cast<const char *>(p) + row * S;
+        if constexpr (MODE == kShort) {
+            r = Raw<DT, V>{};
+#pragma unroll
+            for (int q = 0; q < V; ++q)
+                if (q < left) __builtin_memcpy(reinterpret_cast<char *>(&r) + q * S, b + (int64_t)(at + q) * S, S);
+        } else {
+            const int from = full() ? at : MODE == kTail && any() ? N - V : 0;  // (none: the row's first, unused)
+            __builtin_memcpy(&r, b + (int64_t)from * S, V * S);
+        }
+    }
+    // The piece's values, zeros past the row's end.
+    template <int DT>
+    __device__ __forceinline__ void values(const Raw<DT, V> &r, float (&v)[V]) const {
+        raw_values<DT, V>(r, v);
+        if constexpr (MODE == kTail) {
+            const int by = full() || !any() ? 0 : V - left;
+#pragma unroll
+            for (int o = 1; o < V; o <<= 1)
+#pragma unroll
+                for (int q = 0; q < V; ++q) v[q] = by & o ? (q + o < V ? v[q + o] : 0.0f) : v[q];
+        }
+        if constexpr (MODE != kShort) {
+#pragma unroll
+            for (int q = 0; q < V; ++q) v[q] = any() ? v[q] : 0.0f;
+        }
+    }
+    // Rounds to nearest even.
+    template <int DT>
+    __device__ __forceinline__ void store(void *p, int64_t row, const float (&v)[V]) const {
+        constexpr int S = DT == kF32 ? 4 : 2;
+        using E = std::conditional_t<DT == kF32, float, std::conditional_t<DT == kF16, _Float16, __bf16>>;
+        E e[V];
+#pragma unroll
+        for (int q = 0; q < V; ++q) e[q] = (E)v[q];
+        char *b = static_cast<char *>(p) + (row + at) * S;
+        if (full()) __builtin_memcpy(b, e, V * S);
+        else if (MODE != kWhole)
+#pragma unroll
+            for (int q = 0; q < V; ++q)
+                if (q < left) __builtin_memcpy(b + q * S, &e[q], S);
+    }
+};
+
+// v rounded to type DT.
+template <int DT>
+__device__ __forceinline__ float rounded(float v) {
+    if constexpr (DT == kF32) return v;
+    else if constexpr (DT == kF16) return (float)(_Float16)v;
+    else return (float)(__bf16)v;
+}
+
+// ---- a row's norm
+
+// Mean and 1 / standard deviation from the sums of N values and of their squares (rms: mean 0).  In f64: the sums lose
+// nothing to a mean far from 0, and the roundings of a normed row, which decide experts where a router follows, are those of
+// its exact value but for one in some 2^28 (a sum in another order would give another 2^-24).
+struct Norm {
+    double mean, rstd;
+};
+__device__ __forceinline__ Norm norm_of(double sum, double squares, int N, bool layer, double eps) {
+    Norm r;
+    r.mean = layer ? sum / N : 0.0;
+    const double var = squares / N - r.mean * r.mean;
+    r.rstd = 1.0 / sqrt((var < 0.0 ? 0.0 : var) + eps);
+    return r;
+}
+__device__ __forceinline__ float norm_value(const Norm &r, float v, float weight, float bias) {
+    float f = (float)(((double)v - r.mean) * r.rstd * (double)weight + (double)bias);
+    // rounded here, and again to the rows' type: the compiler would make one rounding of both, whose results differ from
+    // the two's (and from a cast through f32) in one f16 value of some 2^14, at twenty more instructions
+    asm("" : "+v"(f));
+    return f;
+}
+
+// ---- launchers (arguments checked by the C ABI layer)
+
+struct BlockNormArgs {
+    const void *x, *b;               // [M][N]; b may be null: y is x
+    const void *post, *post_bias;    // [N] or null
+    const void *gate;                // [R][N] or null
+    const void *pre, *pre_bias;      // [N] or null
+    void *y, *n;                     // [M][N] or null
+    int64_t M, gate_rows;            // rows that share a gate: M / R
+    int N;
+    bool layer;
+    float scale;
+    double eps;
+};
+hipError_t launch_block_norm(const BlockNormArgs &a, int dtype, bool wide_weights, hipStream_t s);
+
+struct BlockNormBackwardArgs {
+    const void *dy, *dn, *y, *b;     // [M][N]; null: none
+    const void *post, *post_bias, *gate, *pre, *pre_bias;
+    void *dx, *db;                   // [M][N]; db null: no b
+    float *dpost, *dpost_bias, *dgate, *dpre, *dpre_bias;  // null: not asked for
+    float *part;                     // workspace
+    int64_t M, gate_rows;
+    int N;
+    bool layer;
+    float scale;
+    double eps;
+};
+size_t block_norm_backward_workspace(int64_t M, int64_t N, int64_t R);
+hipError_t launch_block_norm_backward(const BlockNormBackwardArgs &a, int dtype, bool wide_weights, void *ws, hipStream_t s);
+
+}  // namespace tq2

@@ -2,50 +2,12 @@
 // and launches.  Declarations and the contract live in include/libtq2_moe.h.
 #include <hip/hip_runtime.h>
 
-#include <initializer_list>
-
 #include "../../include/libtq2_moe.h"
+#include "checks.h"
 #include "internal.h"
 #include "q4.h"
 
-namespace {
-
-bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return na && nb && x < y + nb && y < x + na;
-}
-
-size_t size_of(int dtype) { return dtype == Q4_F32 ? 4 : 2; }
-
-bool known(int dtype) { return dtype == Q4_F32 || dtype == Q4_F16 || dtype == Q4_BF16; }
-
-bool weight_ok(const q4_weight *w) {
-    return w && w->data && aligned(w->data, 256) && (w->zeros == 0 || w->zeros == 1) &&
-           q4_packed_size(w->E, w->N, w->K, w->G, w->zeros) != 0;
-}
-
-tq2::Q4View view(const q4_weight *w) { return tq2::q4_view(w->data, w->E, w->N, w->K, w->G, w->zeros != 0); }
-
-size_t bytes(const q4_weight *w) { return q4_packed_size(w->E, w->N, w->K, w->G, w->zeros); }
-
-struct Range {
-    const void *at;
-    size_t bytes;
-};
-
-// A caller's workspace: large enough, 256-byte aligned, clear of the call's other arguments.
-bool workspace_bad(const void *ws, size_t ws_bytes, size_t need, std::initializer_list<Range> others) {
-    if (!ws || ws_bytes < need || !aligned(ws, 256)) return true;
-    for (const Range &r : others)
-        if (overlap(ws, need, r.at, r.bytes)) return true;
-    return false;
-}
-
-constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
-
-}  // namespace
+using namespace tq2::check;
 
 extern "C" {
 
@@ -92,7 +54,7 @@ int q4_gemm(const q4_weight *w, const void *x, void *y, int64_t M, int dtype, vo
         return TQ2_EINVAL;
     const int st = tq2::current_device(nullptr);
     if (st) return st;
-    return tq2::status_of(tq2::launch_q4_gemm(view(w), x, y, M, dtype, workspace, static_cast<hipStream_t>(stream)));
+    return tq2::status_of(tq2::launch_q4_gemm(view(w), x, y, M, dtype, workspace, nullptr, static_cast<hipStream_t>(stream)));
 }
 
 int moe_route(const void *logits, const float *bias, int32_t *idx, float *weights, int64_t T, int64_t E, int64_t k,
@@ -165,8 +127,8 @@ int q4_moe(const void *x, const int32_t *idx, const float *weights, const q4_wei
     const int st = tq2::current_device(nullptr);
     if (st) return st;
     const tq2::MoePlan p = tq2::moe_plan(T, k, E, d, f, dtype);
-    return tq2::status_of(tq2::launch_q4_moe(p, x, idx, weights, view(gate), view(up), view(down), y, T, k, dtype,
-                                             workspace, static_cast<hipStream_t>(stream)));
+    return tq2::status_of(tq2::launch_q4_moe(p, x, idx, weights, view(gate), view(up), view(down), nullptr, y, T, k,
+                                             dtype, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

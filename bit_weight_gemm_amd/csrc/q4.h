@@ -160,7 +160,9 @@ hipError_t launch_q4_pack(const uint8_t *codes, const uint16_t *scales, const ui
                           hipStream_t s);
 hipError_t launch_q4_dequant(const Q4View &v, float *out, hipStream_t s);
 size_t q4_gemm_workspace(int64_t N, int64_t K, int64_t G, int64_t M, int dtype);
-hipError_t launch_q4_gemm(const Q4View &v, const void *x, void *y, int64_t M, int dtype, void *ws, hipStream_t s);
+struct Q4Epilogue;  // q4_epilogue.h; nullptr: none
+hipError_t launch_q4_gemm(const Q4View &v, const void *x, void *y, int64_t M, int dtype, void *ws, const Q4Epilogue *epi,
+                          hipStream_t s);
 
 // Experts' products.  Workspace: see MoePlan.
 struct MoePlan {
@@ -174,8 +176,8 @@ struct MoePlan {
 };
 MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtype);
 hipError_t launch_q4_moe(const MoePlan &p, const void *x, const int32_t *idx, const float *weights, const Q4View &gate,
-                         const Q4View &up, const Q4View &down, void *y, int64_t T, int64_t k, int dtype, void *ws,
-                         hipStream_t s);
+                         const Q4View &up, const Q4View &down, const void *residual, void *y, int64_t T, int64_t k, int dtype,
+                         void *ws, hipStream_t s);  // residual [T][d]: added to y (nullptr: none)
 
 struct RouteArgs {
     const void *logits;

@@ -60,32 +60,6 @@ __global__ __launch_bounds__(256) void q4_dequant_kernel(Q4View v, float *out) {
     }
 }
 
-// Column blocks per wave: one while that gives each of the 256 compute units one workgroup
-// at most (N = K = 4096, one row: 4.4 us, with two 6.0), two beyond (N = 5003, sixteen rows: 7.5
-// us, with one 8.8), so that x is read less often; four for f32 x beyond two workgroups each (x is
-// split for all columns at once; N = 14336, K = 4096, one row 15.7, with two 20.7 us).
-template <int XT, int G>
-hipError_t dense(const Q4Args &a, hipStream_t s) {
-    const int64_t nb = a.w.nb;
-    if (a.M <= 16) {
-        if (nb <= 256) return run_q4_skinny<XT, G, 1, 1, kDense>(a, 1, s);
-        if constexpr (XT == kXF32x3) {
-            if (nb > 512) return run_q4_skinny<XT, G, 1, 4, kDense>(a, 1, s);
-        }
-        return run_q4_skinny<XT, G, 1, 2, kDense>(a, 1, s);
-    }
-    // up to 32 rows as above (4096 x 4096, 17 rows 8.1 us, with two 9.4); the blocks of more rows fill the units
-    if (a.M <= 32 && nb <= 256) return run_q4_skinny<XT, G, 2, 1, kDense>(a, 1, s);
-    return run_q4_skinny<XT, G, 2, 2, kDense>(a, (a.M + 31) / 32, s);
-}
-
-template <int XT>
-hipError_t dense_g(const Q4Args &a, hipStream_t s) {
-    if (a.w.G == 32) return dense<XT, 32>(a, s);
-    if (a.w.G == 64) return dense<XT, 64>(a, s);
-    return dense<XT, 128>(a, s);
-}
-
 }  // namespace
 
 hipError_t launch_q4_pack(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, const Q4View &v,
@@ -170,7 +144,8 @@ size_t q4_gemm_workspace(int64_t N, int64_t K, int64_t G, int64_t M, int dtype) 
     return d.bm ? dense_ws(d, N, K, M, dtype).total : 0;
 }
 
-hipError_t launch_q4_gemm(const Q4View &v, const void *x, void *y, int64_t M, int dtype, void *ws, hipStream_t s) {
+hipError_t launch_q4_gemm(const Q4View &v, const void *x, void *y, int64_t M, int dtype, void *ws, const Q4Epilogue *epi,
+                          hipStream_t s) {
     const Deal d = deal(v.N, v.K, v.G, M, dtype);
     if (d.bm) {
         const DenseWs w = dense_ws(d, v.N, v.K, M, dtype);
@@ -190,15 +165,18 @@ hipError_t launch_q4_gemm(const Q4View &v, const void *x, void *y, int64_t M, in
             a.a = p.out, a.lda = p.lda, a.plane = p.plane, a.rowscale = p.rowscale;
         }
         if (d.split > 1) a.part = reinterpret_cast<float *>(b + w.off_part), a.part_stride = w.part_stride;
-        const hipError_t e = launch_q4_tiled_dense(a, dtype, d.bm, s);
+        if (epi) a.epi = *epi;
+        // shares are joined first: their products are q4_gemm's own
+        const hipError_t e = epi && d.split == 1 ? launch_q4_tiled_epilogue(a, dtype, d.bm, s) : launch_q4_tiled_dense(a, dtype, d.bm, s);
         if (e != hipSuccess || d.split == 1) return e;
+        if (epi) return launch_q4_join_epilogue(a, y, dtype, s);
         return launch_q4_join(a.part, a.part_stride, d.split, y, M * v.N, dtype, s);
     }
     Q4Args a{};
     a.w = v, a.x = x, a.y = y, a.M = M;
-    if (dtype == kF16) return dense_g<kXF16>(a, s);
-    if (dtype == kBF16) return dense_g<kXBF16>(a, s);
-    return dense_g<kXF32x3>(a, s);
+    if (!epi) return q4_dense<false>(a, dtype, s);
+    a.epi = *epi;
+    return launch_q4_dense_epilogue(a, dtype, s);
 }
 
 }  // namespace tq2

@@ -82,9 +82,9 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(const int32_t *idx, int 
 
 // The slots' parts of each token, in slot order: 2048 tokens of 8 slots, 2048 wide, 22 us (142 MB, 6.4 TB/s:
 // in part from the last-level cache).
-template <int DT>
-__global__ __launch_bounds__(256) void moe_sum_kernel(const float *part, const int32_t *idx, void *y, int64_t T, int k,
-                                                      int E, int d) {
+template <int DT, bool RES>
+__global__ __launch_bounds__(256) void moe_sum_kernel(const float *part, const int32_t *idx, const void *residual, void *y,
+                                                      int64_t T, int k, int E, int d) {
     const int64_t step = (int64_t)gridDim.x * 1024;
     for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < T * d; i += step) {
         const int64_t t = i / d;
@@ -95,7 +95,10 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(const float *part, const i
             if (e >= 0 && e < E) v += *reinterpret_cast<const f4 *>(part + (t * k + j) * d + n);
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) store_from_float<DT>(y, i + q, v[q]);
+        for (int q = 0; q < 4; ++q) {
+            if constexpr (RES) v[q] += load_as_float<DT>(residual, i + q);
+            store_from_float<DT>(y, i + q, v[q]);
+        }
     }
 }
 
@@ -115,17 +118,25 @@ hipError_t row_gate_up(const Q4RowArgs &a, int64_t slots, hipStream_t s) {
     return run_q4_row<XT, 128, 4, 8, 2, kRowGateUp, PH, kF32>(a, slots, s);
 }
 
-template <int XT, int DT>
+template <int XT, int DT, bool RES>
 hipError_t row_down_sum(const Q4RowArgs &a, int64_t T, hipStream_t s) {
-    if (a.w.G == 32) return run_q4_row<XT, 32, 1, 16, 2, kRowDownSum, 1, DT>(a, T, s);
-    if (a.w.G == 64) return run_q4_row<XT, 64, 1, 16, 2, kRowDownSum, 1, DT>(a, T, s);
-    return run_q4_row<XT, 128, 1, 16, 2, kRowDownSum, 1, DT>(a, T, s);
+    if (a.w.G == 32) return run_q4_row<XT, 32, 1, 16, 2, kRowDownSum, 1, DT, RES>(a, T, s);
+    if (a.w.G == 64) return run_q4_row<XT, 64, 1, 16, 2, kRowDownSum, 1, DT, RES>(a, T, s);
+    return run_q4_row<XT, 128, 1, 16, 2, kRowDownSum, 1, DT, RES>(a, T, s);
+}
+
+template <bool RES>
+hipError_t row_down_sum(const Q4RowArgs &a, int64_t T, int dtype, hipStream_t s) {
+    if (dtype == kF16) return row_down_sum<kXF32x2, kF16, RES>(a, T, s);
+    if (dtype == kBF16) return row_down_sum<kXF32x2, kBF16, RES>(a, T, s);
+    return row_down_sum<kXF32x3, kF32, RES>(a, T, s);
 }
 
 // A few slots: two launches, every slot with its own expert's weights; h in two
 // bfloat16 parts (relative error 2^-17) for 16-bit types, in three, which are exact, for f32.
 hipError_t direct(const MoePlan &p, const void *x, const int32_t *idx, const float *weights, const Q4View &gate,
-                  const Q4View &up, const Q4View &down, void *y, int64_t T, int64_t k, int dtype, char *b, hipStream_t s) {
+                  const Q4View &up, const Q4View &down, const void *residual, void *y, int64_t T, int64_t k, int dtype, char *b,
+                  hipStream_t s) {
     Q4RowArgs g{};
     g.w = gate, g.w2 = up, g.x = x, g.y = b + p.off_h, g.topk = (int)k, g.weights = weights, g.idx = idx, g.ldh = p.ldh;
     hipError_t e;
@@ -134,29 +145,32 @@ hipError_t direct(const MoePlan &p, const void *x, const int32_t *idx, const flo
     else e = row_gate_up<kXF32x3, 3>(g, p.slots, s);
     if (e != hipSuccess) return e;
     Q4RowArgs d = g;
-    d.w = down, d.x = g.y, d.y = y;
-    if (dtype == kF16) return row_down_sum<kXF32x2, kF16>(d, T, s);
-    if (dtype == kBF16) return row_down_sum<kXF32x2, kBF16>(d, T, s);
-    return row_down_sum<kXF32x3, kF32>(d, T, s);
+    d.w = down, d.x = g.y, d.y = y, d.residual = residual;
+    return residual ? row_down_sum<true>(d, T, dtype, s) : row_down_sum<false>(d, T, dtype, s);
 }
 
 template <int DT>
-void launch_sum(const float *part, const int32_t *idx, void *y, int64_t T, int64_t k, int E, int d, hipStream_t s) {
+void launch_sum(const float *part, const int32_t *idx, const void *residual, void *y, int64_t T, int64_t k, int E, int d,
+                hipStream_t s) {
     const int64_t blocks = (T * d / 4 + 255) / 256, most = (int64_t)1 << 20;
-    moe_sum_kernel<DT><<<dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, s>>>(part, idx, y, T, (int)k, E, d);
+    const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(256);
+    if (residual) moe_sum_kernel<DT, true><<<grid, block, 0, s>>>(part, idx, residual, y, T, (int)k, E, d);
+    else moe_sum_kernel<DT, false><<<grid, block, 0, s>>>(part, idx, residual, y, T, (int)k, E, d);
 }
 
-hipError_t sum(const float *part, const int32_t *idx, void *y, int64_t T, int64_t k, int E, int d, int dtype, hipStream_t s) {
-    if (dtype == kF16) launch_sum<kF16>(part, idx, y, T, k, E, d, s);
-    else if (dtype == kBF16) launch_sum<kBF16>(part, idx, y, T, k, E, d, s);
-    else launch_sum<kF32>(part, idx, y, T, k, E, d, s);
+hipError_t sum(const float *part, const int32_t *idx, const void *residual, void *y, int64_t T, int64_t k, int E, int d, int dtype,
+               hipStream_t s) {
+    if (dtype == kF16) launch_sum<kF16>(part, idx, residual, y, T, k, E, d, s);
+    else if (dtype == kBF16) launch_sum<kBF16>(part, idx, residual, y, T, k, E, d, s);
+    else launch_sum<kF32>(part, idx, residual, y, T, k, E, d, s);
     return hipGetLastError();
 }
 
 // A few rows per expert: every expert's workgroups find their slots, no plan.  As in
 // tiled(), h for 16-bit types is rounded to f16 under a power of two per row.
 hipError_t grouped(const MoePlan &p, const void *x, const int32_t *idx, const float *weights, const Q4View &gate,
-                   const Q4View &up, const Q4View &down, void *y, int64_t T, int64_t k, int dtype, char *b, hipStream_t s) {
+                   const Q4View &up, const Q4View &down, const void *residual, void *y, int64_t T, int64_t k, int dtype, char *b,
+                   hipStream_t s) {
     Q4GroupArgs g{};
     g.w = gate, g.w2 = up, g.x = x, g.y = reinterpret_cast<float *>(b + p.off_h), g.idx = idx, g.weights = weights;
     g.slots = (int)p.slots, g.topk = (int)k;
@@ -166,7 +180,7 @@ hipError_t grouped(const MoePlan &p, const void *x, const int32_t *idx, const fl
     d.w = down, d.x = g.y, d.y = reinterpret_cast<float *>(b + p.off_part);
     e = launch_q4_group_down(d, q4_planes(dtype), s);
     if (e != hipSuccess) return e;
-    return sum(d.y, idx, y, T, k, gate.E, down.N, dtype, s);
+    return sum(d.y, idx, residual, y, T, k, gate.E, down.N, dtype, s);
 }
 
 // Few rows per expert: tiles of 16 rows, h in f32.
@@ -271,11 +285,11 @@ MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtyp
 }
 
 hipError_t launch_q4_moe(const MoePlan &p, const void *x, const int32_t *idx, const float *weights, const Q4View &gate,
-                         const Q4View &up, const Q4View &down, void *y, int64_t T, int64_t k, int dtype, void *ws,
-                         hipStream_t s) {
+                         const Q4View &up, const Q4View &down, const void *residual, void *y, int64_t T, int64_t k, int dtype,
+                         void *ws, hipStream_t s) {
     char *b = static_cast<char *>(ws);
-    if (p.direct) return direct(p, x, idx, weights, gate, up, down, y, T, k, dtype, b, s);
-    if (p.grouped) return grouped(p, x, idx, weights, gate, up, down, y, T, k, dtype, b, s);
+    if (p.direct) return direct(p, x, idx, weights, gate, up, down, residual, y, T, k, dtype, b, s);
+    if (p.grouped) return grouped(p, x, idx, weights, gate, up, down, residual, y, T, k, dtype, b, s);
     int32_t *ntiles = reinterpret_cast<int32_t *>(b), *order = reinterpret_cast<int32_t *>(b + p.off_order);
     int4 *tiles = reinterpret_cast<int4 *>(b + p.off_tiles);
     const float *part = reinterpret_cast<const float *>(b + p.off_part);
@@ -294,7 +308,7 @@ hipError_t launch_q4_moe(const MoePlan &p, const void *x, const int32_t *idx, co
     if (e != hipSuccess) return e;
     e = p.tiled ? tiled(p, x, weights, gate, up, down, px, k, dtype, b, s) : skinny(p, x, weights, gate, up, down, k, dtype, b, s);
     if (e != hipSuccess) return e;
-    return sum(part, idx, y, T, k, gate.E, down.N, dtype, s);
+    return sum(part, idx, residual, y, T, k, gate.E, down.N, dtype, s);
 }
 
 }  // namespace tq2

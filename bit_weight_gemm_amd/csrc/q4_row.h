@@ -28,6 +28,7 @@ struct Q4RowArgs {
     int64_t ldh;
     int topk;
     Q4View w2;               // kRowGateUp: up
+    const void *residual;    // RES: [T][N] in y's type
 };
 
 // v as P bfloat16 parts (bits) that add up to it, the last of two rounded.
@@ -46,8 +47,8 @@ __device__ __forceinline__ void q4_parts(float v, uint16_t *out) {
 }
 
 // XT: the form of x (kXF16, kXBF16, kXF32x3), or of h (kXF32x2, kXF32x3: its parts).
-// PH: parts of the h that kRowGateUp writes.  DT: type of y (kRowDownSum).
-template <int XT, int G, int CB, int WAVES, int D, int MODE, int PH, int DT>
+// PH: parts of the h that kRowGateUp writes.  DT: type of y (kRowDownSum).  RES (kRowDownSum): plus the residual's row.
+template <int XT, int G, int CB, int WAVES, int D, int MODE, int PH, int DT, bool RES>
 __global__ __launch_bounds__(WAVES * 64) void q4_row_kernel(Q4RowArgs p) {
     constexpr bool BF = XT != kXF16, EXACT = XT == kXF32x3;
     constexpr int P = XT == kXF32x3 ? 3 : XT == kXF32x2 ? 2 : 1, GPU_ = 128 / G, T = WAVES * 64;
@@ -217,6 +218,7 @@ __global__ __launch_bounds__(WAVES * 64) void q4_row_kernel(Q4RowArgs p) {
                 v += p.weights[slot0 + j] * dot;
             }
         }
+        if constexpr (RES) v += load_as_float<DT>(p.residual, (int64_t)row * p.w.N + nn);
         store_from_float<DT>(p.y, (int64_t)row * p.w.N + nn, v);
     }
 }
@@ -224,11 +226,11 @@ __global__ __launch_bounds__(WAVES * 64) void q4_row_kernel(Q4RowArgs p) {
 // LDS that a call's rows take.
 inline size_t q4_row_lds(int64_t items, int parts) { return (size_t)items * parts * 256; }
 
-template <int XT, int G, int CB, int WAVES, int D, int MODE, int PH, int DT>
+template <int XT, int G, int CB, int WAVES, int D, int MODE, int PH, int DT, bool RES = false>
 inline hipError_t run_q4_row(const Q4RowArgs &a, int64_t rows, hipStream_t s) {
     constexpr int NC = MODE == kRowGateUp ? CB / 2 : CB, P = XT == kXF32x3 ? 3 : XT == kXF32x2 ? 2 : 1;
     const int64_t items = MODE == kRowGateUp ? a.w.ku : (int64_t)a.topk * a.w.ku;
-    q4_row_kernel<XT, G, CB, WAVES, D, MODE, PH, DT>
+    q4_row_kernel<XT, G, CB, WAVES, D, MODE, PH, DT, RES>
         <<<dim3((unsigned)((a.w.nb + NC - 1) / NC), (unsigned)rows), dim3(WAVES * 64), q4_row_lds(items, P), s>>>(a);
     return hipGetLastError();
 }

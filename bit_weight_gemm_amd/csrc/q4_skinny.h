@@ -34,7 +34,7 @@
 // count.  Rows that M does not have are not loaded (eight rows 12.5 -> 11.3 us).
 #pragma once
 
-#include "q4.h"
+#include "q4_epilogue.h"
 
 namespace tq2 {
 
@@ -57,6 +57,7 @@ struct Q4Args {
     const int4 *tiles;       // {expert, first place, rows, 0}
     const int32_t *ntiles;
     const float *weights;    // [slots]
+    Q4Epilogue epi;          // EPI
 };
 
 // sum_k x[k] W[n][k] of expert e term by term, k in order, eight at a time: one word of codes, x8(k) for the
@@ -127,7 +128,8 @@ __device__ __forceinline__ void q4_split(w4 lo, w4 hi, w4 *out) {
         }
 }
 
-template <int XT, int G, int RB, int CB, int D, int MODE>
+// EPI (kDense): bias, activation and residual on the way out.
+template <int XT, int G, int RB, int CB, int D, int MODE, bool EPI>
 __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
     constexpr bool BF = XT != kXF16;
     constexpr bool F32 = XT == kXF32x2 || XT == kXF32x3;
@@ -293,7 +295,9 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
             float v = total(group, rb * CB + cb, row, col);
             if (!__builtin_isfinite(v)) v = q4_slow_row<XT>(p.x, (int64_t)row0 + m, p.w, 0, nn);
             constexpr int DT = XT == kXF16 ? kF16 : XT == kXBF16 ? kBF16 : kF32;
-            store_from_float<DT>(p.y, ((int64_t)row0 + m) * p.w.N + nn, v);
+            const int64_t at = ((int64_t)row0 + m) * p.w.N + nn;
+            if constexpr (EPI) v = q4_epilogue<DT>(p.epi, v, nn, at);
+            store_from_float<DT>(p.y, at, v);
         } else if constexpr (MODE == kGateUp) {
             float g = total(group, rb * CB + 2 * cb, row, col), u = total(group, rb * CB + 2 * cb + 1, row, col);
             if (!__builtin_isfinite(g) || !__builtin_isfinite(u)) {
@@ -315,7 +319,7 @@ __global__ __launch_bounds__(512) void q4_skinny_kernel(Q4Args p) {
 // no further.
 constexpr int64_t kWavesWanted = 2048;
 
-template <int XT, int G, int RB, int CB, int MODE>
+template <int XT, int G, int RB, int CB, int MODE, bool EPI = false>
 inline hipError_t run_q4_skinny(Q4Args a, int64_t grid_y, hipStream_t s) {
     constexpr int PERX = XT == kXF32x2 || XT == kXF32x3 ? 8 : 4;
     constexpr int REGS = 4 * (RB * PERX + CB);  // registers of one unit in flight
@@ -325,8 +329,44 @@ inline hipError_t run_q4_skinny(Q4Args a, int64_t grid_y, hipStream_t s) {
     while (a.log_wk < 3 && (blocks * grid_y << a.log_wk) < kWavesWanted && (2 << a.log_wk) <= a.w.ku) ++a.log_wk;
     const int64_t wn = 8 >> a.log_wk;
     const dim3 grid((unsigned)((blocks + wn - 1) / wn), (unsigned)grid_y);
-    q4_skinny_kernel<XT, G, RB, CB, D, MODE><<<grid, dim3(512), 0, s>>>(a);
+    q4_skinny_kernel<XT, G, RB, CB, D, MODE, EPI><<<grid, dim3(512), 0, s>>>(a);
     return hipGetLastError();
 }
+
+// Column blocks per wave: one while that gives each of the 256 compute units one workgroup
+// at most (N = K = 4096, one row: 4.4 us, with two 6.0), two beyond (N = 5003, sixteen rows: 7.5
+// us, with one 8.8), so that x is read less often; four for f32 x beyond two workgroups each (x is
+// split for all columns at once; N = 14336, K = 4096, one row 15.7, with two 20.7 us).
+template <int XT, int G, bool EPI>
+hipError_t q4_dense(const Q4Args &a, hipStream_t s) {
+    const int64_t nb = a.w.nb;
+    if (a.M <= 16) {
+        if (nb <= 256) return run_q4_skinny<XT, G, 1, 1, kDense, EPI>(a, 1, s);
+        if constexpr (XT == kXF32x3) {
+            if (nb > 512) return run_q4_skinny<XT, G, 1, 4, kDense, EPI>(a, 1, s);
+        }
+        return run_q4_skinny<XT, G, 1, 2, kDense, EPI>(a, 1, s);
+    }
+    // up to 32 rows as above (4096 x 4096, 17 rows 8.1 us, with two 9.4); the blocks of more rows fill the units
+    if (a.M <= 32 && nb <= 256) return run_q4_skinny<XT, G, 2, 1, kDense, EPI>(a, 1, s);
+    return run_q4_skinny<XT, G, 2, 2, kDense, EPI>(a, (a.M + 31) / 32, s);
+}
+
+template <int XT, bool EPI>
+hipError_t q4_dense(const Q4Args &a, hipStream_t s) {
+    if (a.w.G == 32) return q4_dense<XT, 32, EPI>(a, s);
+    if (a.w.G == 64) return q4_dense<XT, 64, EPI>(a, s);
+    return q4_dense<XT, 128, EPI>(a, s);
+}
+
+template <bool EPI>
+hipError_t q4_dense(const Q4Args &a, int dtype, hipStream_t s) {
+    if (dtype == kF16) return q4_dense<kXF16, EPI>(a, s);
+    if (dtype == kBF16) return q4_dense<kXBF16, EPI>(a, s);
+    return q4_dense<kXF32x3, EPI>(a, s);
+}
+
+// q4_linear.hip
+hipError_t launch_q4_dense_epilogue(const Q4Args &a, int dtype, hipStream_t s);
 
 }  // namespace tq2

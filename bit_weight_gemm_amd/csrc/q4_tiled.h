@@ -25,7 +25,7 @@
 
 #include <type_traits>
 
-#include "q4.h"
+#include "q4_epilogue.h"
 
 namespace tq2 {
 
@@ -52,6 +52,7 @@ struct Q4TArgs {
     int16_t *hexp;           // f16 h: q4_h_exp of each place's row and unit of 128 columns, [places][units]
     int64_t ldh;             // kTGateUp, f16 h: row length, whole units of 128 (zeros past N)
     Q4View w2;               // kTGateUp: up
+    Q4Epilogue epi;          // EPI
 };
 
 __device__ __forceinline__ int q4_lds(int row, int chunk) { return row * 128 + ((chunk ^ (row & 15)) << 3); }
@@ -116,7 +117,8 @@ __device__ __forceinline__ float q4_silu_f16(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
 }
 
-template <int BM, int G, int P, int MODE, int DT>
+// EPI (kTDense, one share): bias, activation and residual on the way out.
+template <int BM, int G, int P, int MODE, int DT, bool EPI>
 __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     constexpr int RB = BM / 16, GPU_ = 128 / G, NCB = 2;
     constexpr int FRAG = P == 1;                  // fragments are read a row block ahead where registers allow
@@ -427,7 +429,8 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
                     if (m >= count || n >= p.w.N) continue;
                     const float v = acc[rb][cb][i] * rs[m];
                     const int64_t at = (row0 + m) * p.w.N + n;
-                    if (p.part) p.part[blockIdx.y * p.part_stride + at] = v;
+                    if constexpr (EPI) store_from_float<DT>(p.y, at, q4_epilogue<DT>(p.epi, v, n, at));
+                    else if (p.part) p.part[blockIdx.y * p.part_stride + at] = v;
                     else store_from_float<DT>(p.y, at, v);
                 }
             }
@@ -435,13 +438,32 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
     }
 }
 
-template <int BM, int G, int P, int MODE, int DT>
+template <int BM, int G, int P, int MODE, int DT, bool EPI = false>
 inline hipError_t run_q4_tiled(Q4TArgs a, int64_t tiles_m, hipStream_t s) {
     a.tiles_n = MODE == kTGateUp ? (a.w.nb + 7) / 8 : (a.w.nb + 15) / 16;
     const int64_t grid = (tiles_m * a.tiles_n + 7) / 8 * 8;
     const dim3 blocks((unsigned)grid, MODE == kTDense ? (unsigned)a.split : 1);
-    q4_tiled_kernel<BM, G, P, MODE, DT><<<blocks, dim3(512), 0, s>>>(a);
+    q4_tiled_kernel<BM, G, P, MODE, DT, EPI><<<blocks, dim3(512), 0, s>>>(a);
     return hipGetLastError();
+}
+
+template <int G, bool EPI>
+hipError_t q4_tiled_dense(const Q4TArgs &a, int dtype, int bm, hipStream_t s) {
+    const int64_t t64 = (a.M + 63) / 64, t128 = (a.M + 127) / 128;
+    if (dtype == kF32) {
+        if constexpr (G > 32)
+            if (bm == 128) return run_q4_tiled<128, G, 2, kTDense, kF32, EPI>(a, t128, s);
+        return run_q4_tiled<64, G, 2, kTDense, kF32, EPI>(a, t64, s);  // with G = 32 tiles of 64 only
+    }
+    if (dtype == kF16) return bm == 64 ? run_q4_tiled<64, G, 1, kTDense, kF16, EPI>(a, t64, s) : run_q4_tiled<128, G, 1, kTDense, kF16, EPI>(a, t128, s);
+    return bm == 64 ? run_q4_tiled<64, G, 1, kTDense, kBF16, EPI>(a, t64, s) : run_q4_tiled<128, G, 1, kTDense, kBF16, EPI>(a, t128, s);
+}
+
+template <bool EPI>
+hipError_t q4_tiled_dense(const Q4TArgs &a, int dtype, int bm, hipStream_t s) {
+    if (a.w.G == 32) return q4_tiled_dense<32, EPI>(a, dtype, bm, s);
+    if (a.w.G == 64) return q4_tiled_dense<64, EPI>(a, dtype, bm, s);
+    return q4_tiled_dense<128, EPI>(a, dtype, bm, s);
 }
 
 // x as f16 planes (see q4_prep.h).
@@ -459,6 +481,9 @@ inline bool q4_plain_x(int64_t K, int dtype) { return dtype == kF16 && K % 128 =
 inline int q4_planes(int dtype) { return dtype == kF32 ? 2 : 1; }
 hipError_t launch_q4_tiled_dense(const Q4TArgs &a, int dtype, int bm, hipStream_t s);
 hipError_t launch_q4_join(const float *part, int64_t stride, int split, void *y, int64_t n, int dtype, hipStream_t s);
+// q4_linear.hip
+hipError_t launch_q4_tiled_epilogue(const Q4TArgs &a, int dtype, int bm, hipStream_t s);
+hipError_t launch_q4_join_epilogue(const Q4TArgs &a, void *y, int dtype, hipStream_t s);
 hipError_t launch_q4_tiled_gate_up(const Q4TArgs &a, int planes, int bm, int64_t tiles, hipStream_t s);
 hipError_t launch_q4_tiled_down(const Q4TArgs &a, int planes, int bm, int64_t tiles, hipStream_t s);
 

@@ -23,18 +23,6 @@ __global__ __launch_bounds__(256) void q4_join_kernel(const float *part, int64_t
         if (i + q < n) store_from_float<DT>(y, i + q, v[q]);
 }
 
-template <int G>
-hipError_t dense(const Q4TArgs &a, int dtype, int bm, hipStream_t s) {
-    const int64_t t64 = (a.M + 63) / 64, t128 = (a.M + 127) / 128;
-    if (dtype == kF32) {
-        if constexpr (G > 32)
-            if (bm == 128) return run_q4_tiled<128, G, 2, kTDense, kF32>(a, t128, s);
-        return run_q4_tiled<64, G, 2, kTDense, kF32>(a, t64, s);  // with G = 32 tiles of 64 only
-    }
-    if (dtype == kF16) return bm == 64 ? run_q4_tiled<64, G, 1, kTDense, kF16>(a, t64, s) : run_q4_tiled<128, G, 1, kTDense, kF16>(a, t128, s);
-    return bm == 64 ? run_q4_tiled<64, G, 1, kTDense, kBF16>(a, t64, s) : run_q4_tiled<128, G, 1, kTDense, kBF16>(a, t128, s);
-}
-
 template <int G, int MODE>
 hipError_t grouped(const Q4TArgs &a, int planes, int bm, int64_t tiles, hipStream_t s) {
     if (planes == 2) return run_q4_tiled<64, G, 2, MODE, kF32>(a, tiles, s);  // tiles of 64 only
@@ -56,9 +44,7 @@ hipError_t launch_q4_prep(Q4Prep p, int dtype, hipStream_t s) {
 }
 
 hipError_t launch_q4_tiled_dense(const Q4TArgs &a, int dtype, int bm, hipStream_t s) {
-    if (a.w.G == 32) return dense<32>(a, dtype, bm, s);
-    if (a.w.G == 64) return dense<64>(a, dtype, bm, s);
-    return dense<128>(a, dtype, bm, s);
+    return q4_tiled_dense<false>(a, dtype, bm, s);
 }
 
 hipError_t launch_q4_join(const float *part, int64_t stride, int split, void *y, int64_t n, int dtype, hipStream_t s) {
