@@ -25,6 +25,7 @@
 
 #include <type_traits>
 
+#include "pieces.h"
 #include "q4_epilogue.h"
 
 namespace tq2 {
@@ -393,6 +394,63 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
         }
         return;
     }
+    if constexpr (EPI) {
+        // The sums go through LDS (x's, no longer needed) to threads with eight columns each, whose residual's and y's pieces are
+        // whole lines: 2048 x 4096, bf16, gelu and residual 113 us with single elements and erfcf, 80 so.
+        constexpr int PASSES = P == 1 ? 2 : 1, R = BM / PASSES, CH = R * 32 / 512;
+        float *room = reinterpret_cast<float *>(&As[0][0][0]);  // [R][256]
+        const int n0 = tn * 256, col = (tid & 31) * 8;
+        const Piece<8, kTail> at_n((n0 + col) >> 3, p.w.N);
+        float bias[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) bias[q] = n0 + col + q < p.w.N ? q4_bias_value<DT>(p.epi, q4_bias_bits<DT>(p.epi, n0 + col + q)) : 0.0f;
+#pragma unroll
+        for (int pass = 0; pass < PASSES; ++pass) {
+            Raw<DT, 8> res[CH];
+            if (p.epi.residual && p.w.N >= 8) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const int m = pass * R + (tid >> 5) + 16 * c;
+                    at_n.template load<DT>(p.epi.residual, (row0 + (m < count ? m : 0)) * p.w.N, p.w.N, res[c]);
+                }
+            }
+            if (pass) __syncthreads();
+#pragma unroll
+            for (int rb = pass * RB / PASSES; rb < (pass + 1) * RB / PASSES; ++rb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int m = rb * 16 + 4 * h + i;
+#pragma unroll
+                    for (int cb = 0; cb < NCB; ++cb)  // (the four rows of a store on different banks)
+                        room[(m - pass * R) * 256 + ((wave * 32 + cb * 16 + r) ^ (h << 4))] = acc[rb][cb][i] * rs[m];
+                }
+            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int m = pass * R + (tid >> 5) + 16 * c;
+                if (m >= count || !at_n.any()) continue;
+                const f4 *src = reinterpret_cast<const f4 *>(&room[(m - pass * R) * 256 + (col ^ (((m >> 2) & 3) << 4))]);
+                const f4 lo = src[0], hi = src[1];
+                float v[8], add[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = lo[q] + bias[q], v[4 + q] = hi[q] + bias[4 + q];
+                q4_activate<DT != kF32>(p.epi.act, v);
+                if (p.epi.residual) {
+                    if (p.w.N >= 8) {
+                        at_n.template values<DT>(res[c], add);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            add[q] = q < at_n.left ? load_as_float<DT>(p.epi.residual, (row0 + m) * p.w.N + n0 + col + q) : 0.0f;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[q] += add[q];
+                }
+                at_n.template store<DT>(p.y, (row0 + m) * p.w.N, v);
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         if constexpr (MODE == kTGateUp) {
@@ -429,8 +487,7 @@ __global__ __launch_bounds__(512) void q4_tiled_kernel(Q4TArgs p) {
                     if (m >= count || n >= p.w.N) continue;
                     const float v = acc[rb][cb][i] * rs[m];
                     const int64_t at = (row0 + m) * p.w.N + n;
-                    if constexpr (EPI) store_from_float<DT>(p.y, at, q4_epilogue<DT>(p.epi, v, n, at));
-                    else if (p.part) p.part[blockIdx.y * p.part_stride + at] = v;
+                    if (p.part) p.part[blockIdx.y * p.part_stride + at] = v;
                     else store_from_float<DT>(p.y, at, v);
                 }
             }
