@@ -15,7 +15,7 @@ blr_backward_workspace_size, tq2_workspace_allocs, tq2_select_path,
 tq2_set_path, tq2_set_m_small, tq2_strerror, tq2_version; and in include/libtq2_moe.h:
 q4_upload (packs into memory of its own), q4_gemm, q4_dequant, moe_route,
 moe_route_backward and q4_moe; and in include/libtq2_block.h: q4_linear, moe_layer,
-block_norm and block_norm_backward.  These and the last three and q4_gemm go through
+moe_layer_set_patience, block_norm and block_norm_backward.  These and the last three and q4_gemm go through
 a compiled module (csrc/binding.cpp): beside their kernels' few microseconds, checks
 and conversions in Python would be the larger part.
 
@@ -116,6 +116,7 @@ def lib():
         "q4_linear": ([p, p, p, i32, i32, p, p, i64, i32, p, sz, p], i32),
         "moe_layer_workspace_size": ([i64, i64, i64, i64, i64, i32, i32], sz),
         "moe_layer": ([p, p, sz, p], i32),
+        "moe_layer_set_patience": ([i32], i32),
         "block_norm": ([p, p], i32),
         "block_norm_backward_workspace_size": ([i64, i64, i64, i32], sz),
         "block_norm_backward": ([p, p, sz, p], i32),
@@ -669,6 +670,14 @@ def moe_layer(x, router, gate: Q4Weight, up: Q4Weight, down: Q4Weight, k, norm=N
     if out.__class__ is int:
         _check(out, "moe_layer")
     return out
+
+
+def moe_layer_set_patience(tries: int) -> int:
+    """Test hook: how often a workgroup looks for a value that another one forms before it forms it itself; returns the old setting."""
+    st = int(lib().moe_layer_set_patience(int(tries)))
+    if st < 0:
+        raise Tq2Error(st, "moe_layer_set_patience")
+    return st
 
 
 # ---------------------------------------------------------------- norms around a block

@@ -19,8 +19,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtq2.so")
 BINDING = os.path.join(HERE, "_binding.so")
-SOURCES = ["q4_linear.hip", "block_norm.hip", "q4_tiled.hip", "q4_gemm.hip", "q4_group.hip", "q4_moe.hip", "moe_route.hip",
-           "moe_layer.hip", "libtq2.cpp", "libq4.cpp", "libblock.cpp", "repack.cpp", "tq2_gemv.hip", "mfma_gemm.hip", "blr.hip", "skinny_gemm.hip"]
+SOURCES = ["moe_few.hip", "q4_linear.hip", "block_norm.hip", "q4_tiled.hip", "q4_gemm.hip", "q4_group.hip", "q4_moe.hip",
+           "moe_route.hip", "moe_layer.hip", "libtq2.cpp", "libq4.cpp", "libblock.cpp", "repack.cpp", "tq2_gemv.hip", "mfma_gemm.hip", "blr.hip", "skinny_gemm.hip"]
 ARCH = "gfx950"
 
 

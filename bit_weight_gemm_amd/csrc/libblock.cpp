@@ -2,6 +2,8 @@
 // include/libtq2_block.h.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
+
 #include "../../include/libtq2_block.h"
 #include "block_norm.h"
 #include "checks.h"
@@ -49,6 +51,9 @@ bool side_type(int type, int dtype) { return type == Q4_F32 || type == dtype; }
 
 constexpr int64_t kNormColumns = 16384;
 
+// Some tens of milliseconds.
+std::atomic<int> g_patience{1 << 16};
+
 bool norm_sizes(int64_t M, int64_t N, int64_t R, int dtype) {
     return M >= 0 && M <= kMaxRows && N >= 1 && N <= kNormColumns && R >= 1 && (M == 0 || (R <= M && M % R == 0)) && known(dtype);
 }
@@ -79,7 +84,7 @@ int q4_linear(const q4_weight *w, const void *x, const void *bias, int bias_dtyp
 
 size_t moe_layer_workspace_size(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtype, int with_norm) {
     if (q4_moe_workspace_size(T, k, E, d, f, dtype) == 0 || k > E) return 0;
-    return tq2::layer_plan(T, k, E, d, f, dtype, with_norm != 0).total;
+    return tq2::layer_plan(T, k, E, 1, d, f, dtype, with_norm != 0).total;
 }
 
 int moe_layer(const moe_layer_call *c, void *workspace, size_t workspace_bytes, void *stream) {
@@ -121,8 +126,13 @@ int moe_layer(const moe_layer_call *c, void *workspace, size_t workspace_bytes, 
     a.route.bias = c->bias, a.route.idx = c->idx, a.route.weights = c->weights, a.route.T = T;
     a.route.E = (int)E, a.route.k = (int)k, a.route.groups = (int)c->groups, a.route.keep = (int)c->keep;
     a.route.group_top = (int)c->group_top, a.route.sigmoid = c->score == MOE_SIGMOID, a.route.renorm = c->renorm != 0;
-    const tq2::LayerPlan p = tq2::layer_plan(T, k, E, d, f, c->dtype, c->norm != nullptr);
-    return tq2::status_of(tq2::launch_moe_layer(p, a, workspace, static_cast<hipStream_t>(stream)));
+    const tq2::LayerPlan p = tq2::layer_plan(T, k, E, c->groups, d, f, c->dtype, c->norm != nullptr);
+    return tq2::status_of(tq2::launch_moe_layer(p, a, workspace, g_patience, static_cast<hipStream_t>(stream)));
+}
+
+int moe_layer_set_patience(int tries) {
+    if (tries < 0) return TQ2_EINVAL;
+    return g_patience.exchange(tries);
 }
 
 int block_norm(const block_norm_call *c, void *stream) {

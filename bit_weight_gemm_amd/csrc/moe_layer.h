@@ -20,9 +20,21 @@ struct LayerArgs {
 // Workspace: n [T][d] where there is a norm, the logits, then the experts' own.
 struct LayerPlan {
     MoePlan moe;
+    bool few;                        // two launches: the logits, and everything behind them
     size_t off_logits, off_moe, total;
 };
-LayerPlan layer_plan(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtype, bool norm);
-hipError_t launch_moe_layer(const LayerPlan &p, const LayerArgs &a, void *ws, hipStream_t s);
+LayerPlan layer_plan(int64_t T, int64_t k, int64_t E, int64_t groups, int64_t d, int64_t f, int dtype, bool norm);
+hipError_t launch_moe_layer(const LayerPlan &p, const LayerArgs &a, void *ws, int patience, hipStream_t s);
+
+// moe_few.hip: the experts' choice and products of a few tokens, from their logits, in one launch.
+struct FewArgs {
+    const void *n;                   // [T][d], normed
+    const float *logits;             // [T][E]
+    void *h;                         // silu(g) u in bfloat16 parts [T k][parts][ldh], filled with bytes of 0xff
+    int64_t ldh;
+    int patience;                    // how often a value is looked for before a workgroup forms it itself
+};
+hipError_t launch_few_experts(const FewArgs &f, const LayerArgs &a, hipStream_t s);
+constexpr int kFewOwn = 4;           // experts of a lane that its router holds
 
 }  // namespace tq2

@@ -54,6 +54,10 @@ size_t moe_layer_workspace_size(int64_t T, int64_t k, int64_t E, int64_t d, int6
  * share one must not overlap in time.  Results are deterministic.  T == 0 is a no-op. */
 int moe_layer(const moe_layer_call *call, void *workspace, size_t workspace_bytes, void *stream);
 
+/* Test hook: with a few tokens, how often a workgroup looks for a value that another one forms before it forms it itself (the
+ * results are the same bits).  Returns the old setting. */
+int moe_layer_set_patience(int tries);
+
 /* The norms after and before a block, with its gate and residual scale:
  *   u = norm(b) * post + post_bias       (b itself without post)
  *   y = x + scale * gate * u, rounded to its type      (x itself without b)

@@ -170,6 +170,27 @@ def test_in_a_graph_and_on_another_stream(t):
     assert all(torch.equal(p, q) for p, q in zip(there, want))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [1, 5])
+def test_workgroups_that_form_what_they_wait_for(t, dtype):
+    """With no patience every down workgroup may find silu(g) u missing and form it itself: the same bits."""
+    x, r, w, a = inputs(t, 16, 256, 192, 64, True, dtype)
+    handles = [bw.q4_upload(*(cuda(v) for v in p)) for p in w]
+    note(f"[moe_layer] no patience T={t} {dtype}")
+    want = call(x, r, handles, 3, a)
+    torch.cuda.synchronize()
+    was = bw.moe_layer_set_patience(0)
+    try:
+        for _ in range(5):
+            got = call(x, r, handles, 3, a)
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(got, want))
+    finally:
+        assert bw.moe_layer_set_patience(was) == 0
+    with pytest.raises(bw.Tq2Error):
+        bw.moe_layer_set_patience(-1)
+
+
 def test_calls_side_by_side():
     """Many calls on two streams at once, each with a workspace of its own."""
     x, r, w, a = inputs(8, 16, 256, 128, 64, True, "bf16")
