@@ -30,8 +30,8 @@ hipError_t launch_moe_layer(const LayerPlan &p, const LayerArgs &a, void *ws, in
 struct FewArgs {
     const void *n;                   // [T][d], normed
     const float *logits;             // [T][E]
-    void *h;                         // silu(g) u in bfloat16 parts [T k][parts][ldh], filled with bytes of 0xff
-    int64_t ldh;
+    void *h;                         // silu(g) u in bfloat16 parts [T k][parts][whole units of 128 from f], filled with bytes
+                                     // of 0xff up to f and of 0 past it
     int patience;                    // how often a value is looked for before a workgroup forms it itself
 };
 hipError_t launch_few_experts(const FewArgs &f, const LayerArgs &a, hipStream_t s);

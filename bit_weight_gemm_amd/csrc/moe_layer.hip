@@ -15,8 +15,8 @@ struct LogitsArgs {
     const void *x, *norm, *router;
     void *n;                 // NORM: [T][d]
     float *logits;
-    w4 *fill;                // [T][fill_each] pieces of 0xff bytes
-    int fill_each;
+    w4 *fill;                // [T fill_rows][fill_pitch] pieces of 0xff bytes, of 0 from fill_own on
+    int fill_rows, fill_pitch, fill_own;
     double eps;
     int T, E, d;
 };
@@ -39,7 +39,9 @@ __global__ __launch_bounds__(256) void layer_logits_kernel(LogitsArgs p) {
         for (int q = 0; q < EB; ++q) at.template load<RT>(p.router, (int64_t)(e0 + q < p.E ? e0 + q : e0) * d, d, r[q]);
     };
     load(0);
-    for (int i = blockIdx.x * 256 + tid; i < p.fill_each; i += gridDim.x * 256) p.fill[t * p.fill_each + i] = ~w4{};
+    for (int row = blockIdx.x; row < p.fill_rows; row += gridDim.x)
+        for (int i = tid; i < p.fill_pitch; i += 256)
+            p.fill[(t * p.fill_rows + row) * p.fill_pitch + i] = i < p.fill_own ? ~w4{} : w4{};
     Norm norm{};
     if constexpr (NORM) {
         double sum[1] = {};
@@ -115,13 +117,19 @@ void prompt_logits(const void *x, const void *router, float *logits, int64_t T, 
     prompt_logits_kernel<DT, RT><<<dim3((unsigned)((T * E + 3) / 4)), dim3(256), 0, s>>>(x, router, logits, T, E, d);
 }
 
+// Up to so many slots the experts' choice and products are one launch (64 experts of 8, 2048 x 1024, bf16: one token 17.4 us, two 23,
+// four 31.6; the choice and the two products apart, four 32.9, eight 51 against 57).
+constexpr int64_t kFewMost = 32;
+// Tokens times experts up to which the norm and the logits are one launch.
+constexpr int64_t kLogitsSmall = 32768;
+
 }  // namespace
 
 LayerPlan layer_plan(int64_t T, int64_t k, int64_t E, int64_t groups, int64_t d, int64_t f, int dtype, bool norm) {
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     LayerPlan p{};
     p.moe = moe_plan(T, k, E, d, f, dtype);
-    p.few = p.moe.direct && route_own((int)E, (int)groups) <= kFewOwn;
+    p.few = p.moe.direct && T * k <= kFewMost && T * E <= kLogitsSmall && route_own((int)E, (int)groups) <= kFewOwn;
     p.off_logits = norm ? up((size_t)T * d * (dtype == kF32 ? 4 : 2)) : 0;
     p.off_moe = p.off_logits + up((size_t)T * E * 4);
     p.total = p.off_moe + p.moe.total;
@@ -134,31 +142,35 @@ hipError_t launch_moe_layer(const LayerPlan &p, const LayerArgs &a, void *ws, in
     float *logits = reinterpret_cast<float *>(b + p.off_logits);
     const void *n = a.norm ? b : a.x;
     hipError_t e;
-    if (p.few) {
+    if (a.T * E <= kLogitsSmall) {  // with the norm, in one launch
         LogitsArgs l{};
         l.x = a.x, l.norm = a.norm, l.router = a.router, l.n = b, l.logits = logits, l.eps = a.eps;
         l.T = (int)a.T, l.E = E, l.d = d;
         char *h = b + p.off_moe + p.moe.off_h;
-        l.fill = reinterpret_cast<w4 *>(h), l.fill_each = (int)(a.route.k * (a.dtype == kF32 ? 3 : 2) * p.moe.ldh / 8);
+        if (p.few) {
+            l.fill = reinterpret_cast<w4 *>(h), l.fill_rows = a.route.k * (a.dtype == kF32 ? 3 : 2);
+            l.fill_pitch = (int)(p.moe.ldh / 8), l.fill_own = a.gate.N / 8;
+        }
         if (a.dtype == kF32) e = a.norm ? logits_of<kF32, kF32, kF32, true>(l, s) : logits_of<kF32, kF32, kF32, false>(l, s);
         else if (a.dtype == kF16) e = logits_of<kF16>(l, a.wide_norm, a.wide_router, s);
         else e = logits_of<kBF16>(l, a.wide_norm, a.wide_router, s);
         if (e != hipSuccess) return e;
-        return launch_few_experts(FewArgs{n, logits, h, p.moe.ldh, patience}, a, s);
-    }
-    if (a.norm) {
-        BlockNormArgs q{};
-        q.x = a.x, q.pre = a.norm, q.n = b, q.M = a.T, q.gate_rows = a.T, q.N = d, q.eps = a.eps, q.scale = 1.0f;
-        e = launch_block_norm(q, a.dtype, a.wide_norm, s);
+        if (p.few) return launch_few_experts(FewArgs{n, logits, h, patience}, a, s);
+    } else {
+        if (a.norm) {
+            BlockNormArgs q{};
+            q.x = a.x, q.pre = a.norm, q.n = b, q.M = a.T, q.gate_rows = a.T, q.N = d, q.eps = a.eps, q.scale = 1.0f;
+            e = launch_block_norm(q, a.dtype, a.wide_norm, s);
+            if (e != hipSuccess) return e;
+        }
+        if (a.dtype == kF32) prompt_logits<kF32, kF32>(n, a.router, logits, a.T, E, d, s);
+        else if (a.dtype == kF16 && a.wide_router) prompt_logits<kF16, kF32>(n, a.router, logits, a.T, E, d, s);
+        else if (a.dtype == kF16) prompt_logits<kF16, kF16>(n, a.router, logits, a.T, E, d, s);
+        else if (a.wide_router) prompt_logits<kBF16, kF32>(n, a.router, logits, a.T, E, d, s);
+        else prompt_logits<kBF16, kBF16>(n, a.router, logits, a.T, E, d, s);
+        e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (a.dtype == kF32) prompt_logits<kF32, kF32>(n, a.router, logits, a.T, E, d, s);
-    else if (a.dtype == kF16 && a.wide_router) prompt_logits<kF16, kF32>(n, a.router, logits, a.T, E, d, s);
-    else if (a.dtype == kF16) prompt_logits<kF16, kF16>(n, a.router, logits, a.T, E, d, s);
-    else if (a.wide_router) prompt_logits<kBF16, kF32>(n, a.router, logits, a.T, E, d, s);
-    else prompt_logits<kBF16, kBF16>(n, a.router, logits, a.T, E, d, s);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
     RouteArgs r = a.route;
     r.logits = logits, r.dtype = kF32;
     e = launch_moe_route(r, s);

@@ -29,7 +29,6 @@ struct Q4RowArgs {
     int topk;
     Q4View w2;               // kRowGateUp: up
     const void *residual;    // RES: [T][N] in y's type
-    int patience;            // SHARED
 };
 
 // v as P bfloat16 parts (bits) that add up to it, the last of two rounded.
@@ -47,44 +46,25 @@ __device__ __forceinline__ void q4_parts(float v, uint16_t *out) {
     }
 }
 
-// Bits of an element of h that is not written yet: a NaN that no part of one is stored as.
-constexpr uint16_t kNoH = 0xffff;
-__device__ __forceinline__ bool q4_has_none(uint64_t four) {  // one of four halves is kNoH: its complement has a zero half
-    const uint64_t v = ~four;
-    return ((v - 0x0001000100010001ull) & four & 0x8000800080008000ull) != 0;
-}
-
-// What a task's slots are: the expert and the weight of the task's j-th.
-struct Q4Slots {
-    const int32_t *idx;      // of the task's first slot
-    const float *weights;
-    __device__ int expert(int j) const { return idx[j]; }
-    __device__ float weight(int j) const { return weights[j]; }
-};
-
-// One task of a workgroup: column blocks bx of a slot's gate and up products, or of a token's down products.
 // XT: the form of x (kXF16, kXBF16, kXF32x3), or of h (kXF32x2, kXF32x3: its parts).
 // PH: parts of the h that kRowGateUp writes.  DT: type of y (kRowDownSum).  RES (kRowDownSum): plus the residual's row.
-// SHARED: h goes from workgroup to workgroup within a launch, by accesses at device scope that go past the dies' own caches.
-// Every element is kNoH until it is written; who reads one that is not looks again, up to p.patience times, and gives up
-// (false, for all threads of the workgroup).
-// xs: LDS for the rows, red: for the waves' sums.
-template <int XT, int G, int CB, int WAVES, int D, int MODE, int PH, int DT, bool RES, bool SHARED>
-__device__ __forceinline__ bool q4_row_task(const Q4RowArgs &p, const int bx, const int row, const Q4Slots slots, uint16_t *xs,
-                                            float (*red)[CB * 16]) {
+template <int XT, int G, int CB, int WAVES, int D, int MODE, int PH, int DT, bool RES>
+__global__ __launch_bounds__(WAVES * 64) void q4_row_kernel(Q4RowArgs p) {
     constexpr bool BF = XT != kXF16, EXACT = XT == kXF32x3;
     constexpr int P = XT == kXF32x3 ? 3 : XT == kXF32x2 ? 2 : 1, GPU_ = 128 / G, T = WAVES * 64;
     constexpr int NC = MODE == kRowGateUp ? CB / 2 : CB;
-    // xs: [item][P][128]
+    extern __shared__ __attribute__((aligned(16))) uint16_t xs[];  // [item][P][128]
+    __shared__ float red[WAVES][CB * 16];
+
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, h = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int K = p.w.K, ku = p.w.ku;
+    const int K = p.w.K, ku = p.w.ku, row = blockIdx.y;
     const int slot0 = MODE == kRowGateUp ? row : row * p.topk;
     const int items = MODE == kRowGateUp ? ku : p.topk * ku;
     const bool zeros = p.w.zeros != nullptr;
     if (MODE == kRowGateUp) {
-        const int e = slots.expert(0);
-        if (e < 0 || e >= p.w.E) return true;  // the whole workgroup
+        const int e = p.idx[slot0];
+        if (e < 0 || e >= p.w.E) return;  // the whole workgroup
     }
 
     w4 breg[D][CB];
@@ -94,14 +74,14 @@ __device__ __forceinline__ bool q4_row_task(const Q4RowArgs &p, const int bx, co
     bool live[D];
     auto load = [&](int st, int it) {
         const int j = MODE == kRowGateUp ? 0 : it / ku, u = MODE == kRowGateUp ? it : it % ku;
-        const int e = slots.expert(j);
+        const int e = p.idx[slot0 + j];
         live[st] = e >= 0 && e < p.w.E;
         if (!live[st]) return;
-        wt[st] = MODE == kRowDownSum ? slots.weight(j) : 1.0f;
+        wt[st] = MODE == kRowDownSum ? p.weights[slot0 + j] : 1.0f;
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
             const Q4View &w = MODE == kRowGateUp && (cb & 1) ? p.w2 : p.w;
-            int nb = bx * NC + (MODE == kRowGateUp ? cb >> 1 : cb);
+            int nb = blockIdx.x * NC + (MODE == kRowGateUp ? cb >> 1 : cb);
             nb = nb < w.nb ? nb : w.nb - 1;  // past the last: not stored
             const int64_t unit = ((int64_t)e * w.nb + nb) * ku + u;
             breg[st][cb] = (w.codes + unit * 64)[lane];
@@ -114,13 +94,7 @@ __device__ __forceinline__ bool q4_row_task(const Q4RowArgs &p, const int bx, co
     for (int st = 0; st < D; ++st)
         if (st < n) load(st, wave + WAVES * st);
 
-    const int nn = bx * (NC * 16) + tid;
-    uint32_t residual = 0;  // its bits, on their way
-    if constexpr (RES) {
-        if (tid < NC * 16 && nn < p.w.N) residual = q4_bits<DT>(p.residual, (int64_t)row * p.w.N + nn);
-    }
     // the rows into LDS, eight k at a time
-    bool late = false;
     for (int i = tid; i < items * 16; i += T) {
         const int it = i >> 4, c = i & 15;
         const int j = MODE == kRowGateUp ? 0 : it / ku, k = (MODE == kRowGateUp ? it : it % ku) * 128 + 8 * c;
@@ -138,38 +112,17 @@ __device__ __forceinline__ bool q4_row_task(const Q4RowArgs &p, const int bx, co
                 }
             }
         } else {
-            const int e = slots.expert(j);
+            const int e = p.idx[slot0 + j];
             if (k < K && e >= 0 && e < p.w.E) {
 #pragma unroll
-                for (int q = 0; q < P; ++q) {
-                    const uint16_t *at = static_cast<const uint16_t *>(p.x) + ((int64_t)(slot0 + j) * P + q) * p.ldh + k;
-                    if constexpr (SHARED) {
-                        const uint64_t *two = reinterpret_cast<const uint64_t *>(at);
-                        for (int tries = 0;; ++tries) {
-                            const uint64_t a = __hip_atomic_load(two, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                            const uint64_t b = __hip_atomic_load(two + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                            v[q] = w4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
-                            if (!(q4_has_none(a) || q4_has_none(b))) break;
-                            if (tries >= p.patience) {
-                                late = true;
-                                break;
-                            }
-                            __builtin_amdgcn_s_sleep(1);
-                        }
-                    } else {
-                        v[q] = *reinterpret_cast<const w4 *>(at);
-                    }
-                }
+                for (int q = 0; q < P; ++q)
+                    v[q] = *reinterpret_cast<const w4 *>(static_cast<const uint16_t *>(p.x) + ((int64_t)(slot0 + j) * P + q) * p.ldh + k);
             }
         }
 #pragma unroll
         for (int q = 0; q < P; ++q) *reinterpret_cast<w4 *>(&xs[(it * P + q) * 128 + 8 * c]) = v[q];
     }
-    if constexpr (SHARED && MODE == kRowDownSum) {
-        if (__syncthreads_or(late)) return false;
-    } else {
-        __syncthreads();
-    }
+    __syncthreads();
 
     float acc[CB];
 #pragma unroll
@@ -228,31 +181,28 @@ __device__ __forceinline__ bool q4_row_task(const Q4RowArgs &p, const int bx, co
         for (int q = 0; q < WAVES; ++q) v += red[q][at];
         return v;
     };
+    const int nn = blockIdx.x * (NC * 16) + tid;
     if constexpr (MODE == kRowGateUp) {
-        if (tid >= NC * 16 || nn >= p.w.N) return true;
+        if (tid >= NC * 16 || nn >= p.w.N) return;
         const int at = (tid >> 4) * 32 + (tid & 15);
         float g = total(at), u = total(at + 16);
         if (!__builtin_isfinite(g) || !__builtin_isfinite(u)) {
-            const int e = slots.expert(0);
+            const int e = p.idx[slot0];
             g = q4_slow_row<XT>(p.x, row / p.topk, p.w, e, nn);
             u = q4_slow_row<XT>(p.x, row / p.topk, p.w2, e, nn);
         }
         uint16_t part[PH];
         q4_parts<PH>(g / (1.0f + expf(-g)) * u, part);
 #pragma unroll
-        for (int q = 0; q < PH; ++q) {
-            uint16_t *to = static_cast<uint16_t *>(p.y) + ((int64_t)row * PH + q) * p.ldh + nn;
-            if constexpr (SHARED) __hip_atomic_store(to, part[q] == kNoH ? (uint16_t)0x7fc0u : part[q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            else *to = part[q];
-        }
+        for (int q = 0; q < PH; ++q) static_cast<uint16_t *>(p.y)[((int64_t)row * PH + q) * p.ldh + nn] = part[q];
     } else {
-        if (tid >= NC * 16 || nn >= p.w.N) return true;
+        if (tid >= NC * 16 || nn >= p.w.N) return;
         float v = total(tid);
         if (!__builtin_isfinite(v)) {
             v = 0.0f;
 #pragma unroll 1
             for (int j = 0; j < p.topk; ++j) {
-                const int e = slots.expert(j);
+                const int e = p.idx[slot0 + j];
                 if (e < 0 || e >= p.w.E) continue;
                 const uint16_t *x = static_cast<const uint16_t *>(p.x) + (int64_t)(slot0 + j) * P * p.ldh;
                 const float dot = q4_slow_dot(p.w, e, nn, [&](int k, float (&v8)[8]) {
@@ -265,22 +215,12 @@ __device__ __forceinline__ bool q4_row_task(const Q4RowArgs &p, const int bx, co
                         for (int i = 0; i < 8; ++i) v8[i] += part[i];
                     }
                 });
-                v += slots.weight(j) * dot;
+                v += p.weights[slot0 + j] * dot;
             }
         }
-        if constexpr (RES) v += q4_value<DT>(residual);
+        if constexpr (RES) v += load_as_float<DT>(p.residual, (int64_t)row * p.w.N + nn);
         store_from_float<DT>(p.y, (int64_t)row * p.w.N + nn, v);
     }
-    return true;
-}
-
-template <int XT, int G, int CB, int WAVES, int D, int MODE, int PH, int DT, bool RES>
-__global__ __launch_bounds__(WAVES * 64) void q4_row_kernel(Q4RowArgs p) {
-    extern __shared__ __attribute__((aligned(16))) uint16_t q4_row_room[];
-    __shared__ float red[WAVES][CB * 16];
-    const int row = blockIdx.y;
-    const int64_t slot0 = MODE == kRowGateUp ? row : (int64_t)row * p.topk;
-    q4_row_task<XT, G, CB, WAVES, D, MODE, PH, DT, RES, false>(p, blockIdx.x, row, Q4Slots{p.idx + slot0, p.weights + slot0}, q4_row_room, red);
 }
 
 // LDS that a call's rows take.
