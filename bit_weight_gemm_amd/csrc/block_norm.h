@@ -91,8 +91,12 @@ __device__ __forceinline__ Norm norm_of(double sum, double squares, int N, bool 
     r.rstd = 1.0 / sqrt((var < 0.0 ? 0.0 : var) + eps);
     return r;
 }
+// (without FULL no mean, and no bias)
+template <bool FULL>
 __device__ __forceinline__ float norm_value(const Norm &r, float v, float weight, float bias) {
-    float f = (float)(((double)v - r.mean) * r.rstd * (double)weight + (double)bias);
+    float f;
+    if constexpr (FULL) f = (float)(((double)v - r.mean) * r.rstd * (double)weight + (double)bias);
+    else f = (float)((double)v * r.rstd * (double)weight);
     // rounded here, and again to the rows' type: the compiler would make one rounding of both, whose results differ from
     // the two's (and from a cast through f32) in one f16 value of some 2^14, at twenty more instructions
     asm("" : "+v"(f));

@@ -15,82 +15,94 @@ namespace {
 // Threads of a workgroup: rows of up to 256 threads share workgroups of 256.
 constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
 
-template <int DT, int WT, int TPR, int C, int MODE>
+// FULL: with means or biases.  The rows go round the workgroups.  Parameters that are the same for all rows stay in registers, and the next row's pieces are on
+// their way while one is normed.
+template <int DT, int WT, int TPR, int C, int MODE, bool FULL>
 __global__ __launch_bounds__(threads_of(TPR)) void block_norm_kernel(BlockNormArgs p) {
     constexpr int V = kPiece<DT>, ROWS = threads_of(TPR) / TPR;
+    constexpr bool HOLD = C == 1;  // (two pieces and more of everything would not fit)
     __shared__ double room[2][TPR / 64 * 2];
     const int tid = threadIdx.x % TPR, N = p.N;
-    for (int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR; row < p.M; row += (int64_t)gridDim.x * ROWS) {
-        const int64_t at = row * N, gate_at = p.gate ? row / p.gate_rows * N : 0;
-        Raw<DT, V> x[C], b[C];
-        Raw<WT, V> post[C], gate[C], pre[C], post_bias[C], pre_bias[C];
+    const int64_t step = (int64_t)gridDim.x * ROWS;
+    int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+    Raw<DT, V> x[C], b[C];
+    Raw<WT, V> post[C], gate[C], pre[C], post_bias[C], pre_bias[C];
+    auto piece = [&](int c) { return Piece<V, MODE>(tid + TPR * c, N); };
+    auto rows = [&](int64_t r) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const Piece<V, MODE> q(tid + TPR * c, N);
-            if (p.b) q.template load<DT>(p.b, at, N, b[c]);
-            q.template load<DT>(p.x, at, N, x[c]);
-            if (p.post) q.template load<WT>(p.post, 0, N, post[c]);
-            if (p.post_bias) q.template load<WT>(p.post_bias, 0, N, post_bias[c]);
-            if (p.gate) q.template load<WT>(p.gate, gate_at, N, gate[c]);
-            if (p.pre) q.template load<WT>(p.pre, 0, N, pre[c]);
-            if (p.pre_bias) q.template load<WT>(p.pre_bias, 0, N, pre_bias[c]);
+            if (p.b) piece(c).template load<DT>(p.b, r * N, N, b[c]);
+            piece(c).template load<DT>(p.x, r * N, N, x[c]);
         }
-        float y[C][V];
+    };
+    auto vector = [&](const void *from, int64_t at, Raw<WT, V> (&to)[C]) {
+        if (from)
+#pragma unroll
+            for (int c = 0; c < C; ++c) piece(c).template load<WT>(from, at, N, to[c]);
+    };
+    const bool one_gate = p.gate_rows == p.M;
+    if (row < p.M) rows(row);
+    if constexpr (HOLD) {
+        vector(p.post, 0, post), vector(p.post_bias, 0, post_bias), vector(p.pre, 0, pre), vector(p.pre_bias, 0, pre_bias);
+        if (one_gate) vector(p.gate, 0, gate);
+    }
+    // sums of a row's values (for FULL) and of their squares, and the norm of that
+    auto norm = [&](const float (&v)[C][V], double *where) {
+        double sum[2] = {};
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const double w = v[c][q];
+                sum[0] = __builtin_fma(w, w, sum[0]);
+                if constexpr (FULL) sum[1] += w;
+            }
+        row_total<TPR, FULL ? 2 : 1>(reinterpret_cast<double(&)[FULL ? 2 : 1]>(sum), where);
+        return norm_of(sum[1], sum[0], N, p.layer, p.eps);
+    };
+    auto scaled = [&](const Norm &r, float (&v)[C][V], const Raw<WT, V> (&weight)[C], bool biased, const Raw<WT, V> (&bias)[C]) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float w[V], k[V] = {};
+            piece(c).template values<WT>(weight[c], w);
+            if (FULL && biased) piece(c).template values<WT>(bias[c], k);
+#pragma unroll
+            for (int q = 0; q < V; ++q) v[c][q] = norm_value<FULL>(r, v[c][q], w[q], k[q]);
+        }
+    };
+    for (; row < p.M; row += step) {
+        const int64_t at = row * N;
+        float y[C][V], u[C][V];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            piece(c).template values<DT>(x[c], y[c]);
+            if (p.b) piece(c).template values<DT>(b[c], u[c]);
+        }
+        if (!one_gate) vector(p.gate, row / p.gate_rows * N, gate);
+        if (row + step < p.M) rows(row + step);
         if (p.b) {
-            float u[C][V];
-#pragma unroll
-            for (int c = 0; c < C; ++c) Piece<V, MODE>(tid + TPR * c, N).template values<DT>(b[c], u[c]);
             if (p.post) {
-                double sum[2] = {};
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int q = 0; q < V; ++q) sum[0] += u[c][q], sum[1] += (double)u[c][q] * u[c][q];
-                row_total<TPR, 2>(sum, room[0]);
-                const Norm r = norm_of(sum[0], sum[1], N, p.layer, p.eps);
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const Piece<V, MODE> at_c(tid + TPR * c, N);
-                    float w[V], k[V] = {};
-                    at_c.template values<WT>(post[c], w);
-                    if (p.post_bias) at_c.template values<WT>(post_bias[c], k);
-#pragma unroll
-                    for (int q = 0; q < V; ++q) u[c][q] = norm_value(r, u[c][q], w[q], k[q]);
-                }
+                if constexpr (!HOLD) vector(p.post, 0, post), vector(p.post_bias, 0, post_bias);
+                scaled(norm(u, room[0]), u, post, p.post_bias != nullptr, post_bias);
+            }
+            if constexpr (!HOLD) {
+                if (one_gate) vector(p.gate, 0, gate);
             }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Piece<V, MODE> at_c(tid + TPR * c, N);
                 float g[V];
-                at_c.template values<DT>(x[c], y[c]);
-                if (p.gate) at_c.template values<WT>(gate[c], g);
+                if (p.gate) piece(c).template values<WT>(gate[c], g);
 #pragma unroll
                 for (int q = 0; q < V; ++q)
                     y[c][q] = rounded<DT>(y[c][q] + p.scale * (p.gate ? g[q] : 1.0f) * u[c][q]);
-                if (p.y) at_c.template store<DT>(p.y, at, y[c]);
+                if (p.y) piece(c).template store<DT>(p.y, at, y[c]);
             }
-        } else {
-#pragma unroll
-            for (int c = 0; c < C; ++c) Piece<V, MODE>(tid + TPR * c, N).template values<DT>(x[c], y[c]);
         }
         if (p.n) {
-            double sum[2] = {};
+            if constexpr (!HOLD) vector(p.pre, 0, pre), vector(p.pre_bias, 0, pre_bias);
+            scaled(norm(y, room[1]), y, pre, p.pre_bias != nullptr, pre_bias);
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int q = 0; q < V; ++q) sum[0] += y[c][q], sum[1] += (double)y[c][q] * y[c][q];
-            row_total<TPR, 2>(sum, room[1]);
-            const Norm r = norm_of(sum[0], sum[1], N, p.layer, p.eps);
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const Piece<V, MODE> at_c(tid + TPR * c, N);
-                float w[V], k[V] = {};
-                at_c.template values<WT>(pre[c], w);
-                if (p.pre_bias) at_c.template values<WT>(pre_bias[c], k);
-#pragma unroll
-                for (int q = 0; q < V; ++q) y[c][q] = norm_value(r, y[c][q], w[q], k[q]);
-                at_c.template store<DT>(p.n, at, y[c]);
-            }
+            for (int c = 0; c < C; ++c) piece(c).template store<DT>(p.n, at, y[c]);
         }
         if (TPR > 64 && !(p.b && p.post && p.n)) __syncthreads();  // one of the rooms is used twice in a row
     }
@@ -324,8 +336,10 @@ __global__ __launch_bounds__(256) void zero_kernel(float *out, int64_t n) {
 template <int DT, int WT, int TPR, int C, int MODE>
 hipError_t run(const BlockNormArgs &a, hipStream_t s) {
     constexpr int ROWS = threads_of(TPR) / TPR;
-    const int64_t blocks = (a.M + ROWS - 1) / ROWS, most = (int64_t)1 << 21;
-    block_norm_kernel<DT, WT, TPR, C, MODE><<<dim3((unsigned)(blocks < most ? blocks : most)), dim3(threads_of(TPR)), 0, s>>>(a);
+    const int64_t blocks = (a.M + ROWS - 1) / ROWS, most = 256 * (2048 / threads_of(TPR));
+    const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(threads_of(TPR));
+    if (a.layer || a.post_bias || a.pre_bias) block_norm_kernel<DT, WT, TPR, C, MODE, true><<<grid, block, 0, s>>>(a);
+    else block_norm_kernel<DT, WT, TPR, C, MODE, false><<<grid, block, 0, s>>>(a);
     return hipGetLastError();
 }
 

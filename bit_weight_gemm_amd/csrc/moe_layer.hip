@@ -67,7 +67,7 @@ __global__ __launch_bounds__(256) void layer_logits_kernel(LogitsArgs p) {
             float k[8];
             at.template values<WT>(w, k);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = rounded<DT>(norm_value(norm, v[q], k[q], 0.0f));
+            for (int q = 0; q < 8; ++q) v[q] = rounded<DT>(norm_value<false>(norm, v[q], k[q], 0.0f));
             if (blockIdx.x == 0 && at.any()) at.template store<DT>(p.n, t * d, v);
         }
 #pragma unroll

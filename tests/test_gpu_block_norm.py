@@ -179,6 +179,19 @@ def test_no_gate():
     check_backward(a, y, 50, 300, "f32", "rms", 0.3)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True)])
+def test_biases_without_means(post, pre, dtype):
+    m, n = 20, 520
+    a = inputs(m, n, dtype, "layer", post, pre, 1)
+    note(f"[block_norm] rms with biases post={post} pre={pre} {dtype}")
+    y = check_forward(a, m, n, dtype, "rms", 0.8)
+    check_backward(a, y, m, n, dtype, "rms", 0.8)
+    for name in ("post_bias", "pre_bias"):  # one of the two
+        one = dict(a, **{name: None})
+        check_backward(one, check_forward(one, m, n, dtype, "rms", 0.8), m, n, dtype, "rms", 0.8)
+
+
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 def test_rows_far_from_zero_and_of_any_size(kind):
     """A mean 2000 times the deviation, rows of 1e30 and 1e-30, constant rows and rows of zeros."""
