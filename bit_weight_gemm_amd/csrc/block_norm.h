@@ -131,7 +131,7 @@ struct BlockNormBackwardArgs {
     float scale;
     double eps;
 };
-size_t block_norm_backward_workspace(int64_t M, int64_t N, int64_t R);
+size_t block_norm_backward_workspace(int64_t M, int64_t N, int64_t R, int dtype);
 hipError_t launch_block_norm_backward(const BlockNormBackwardArgs &a, int dtype, bool wide_weights, void *ws, hipStream_t s);
 
 }  // namespace tq2

@@ -156,7 +156,7 @@ int block_norm(const block_norm_call *c, void *stream) {
 }
 
 size_t block_norm_backward_workspace_size(int64_t M, int64_t N, int64_t R, int dtype) {
-    return norm_sizes(M, N, R, dtype) ? tq2::block_norm_backward_workspace(M, N, R) : 0;
+    return norm_sizes(M, N, R, dtype) ? tq2::block_norm_backward_workspace(M, N, R, dtype) : 0;
 }
 
 int block_norm_backward(const block_norm_backward_call *c, void *workspace, size_t workspace_bytes, void *stream) {
@@ -169,7 +169,7 @@ int block_norm_backward(const block_norm_backward_call *c, void *workspace, size
                  (!c->dy && !c->dn)))
         return TQ2_EINVAL;
     const size_t s = size_of(c->dtype), ws = size_of(c->weights_dtype), rows = (size_t)c->M * c->N * s, vec = (size_t)c->N * ws;
-    const size_t need = tq2::block_norm_backward_workspace(c->M, c->N, c->R), sums = (size_t)c->N * 4;
+    const size_t need = tq2::block_norm_backward_workspace(c->M, c->N, c->R, c->dtype), sums = (size_t)c->N * 4;
     const Tensor dy{c->dy, rows, s}, dn{c->dn, rows, s}, y{c->y, rows, s}, b{c->b, rows, s}, gate{c->gate, vec * c->R, ws};
     const Tensor post{c->post, vec, ws}, post_bias{c->post_bias, vec, ws}, pre{c->pre, vec, ws}, pre_bias{c->pre_bias, vec, ws};
     const Tensor dx{c->dx, rows, s}, db{c->db, rows, s}, dgate{c->dgate, sums * c->R, 4}, dpost{c->dpost, sums, 4};
