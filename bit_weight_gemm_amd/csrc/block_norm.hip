@@ -6,6 +6,10 @@
 //
 // One pass over memory: TPR threads hold a row (C pieces of 16 bytes each), every input is read once, sums go over the
 // wave by lane exchanges and over the waves through LDS.
+// Bound by memory where a thread has eight columns or fewer: 4096 x 4096 bf16, forward 30 us (134 MB, 4.5 TB/s; a large copy reaches 5.1),
+// gradient 52 us (201 MB and 25 MB of parts, 4.3 TB/s), f32 42 and 89 us; one row 3.6 and 8 us (launches).  With means
+// 45 and 83 us: their f64 sums and differences.  Gradients of longer rows (more than 4096 of 16 bits, 4096 of f32) have more of a row to a thread
+// than its registers hold and use scratch memory: 2048 x 8192 bf16 154 us, 1.3 TB/s.
 #include "block_norm.h"
 
 namespace tq2 {
@@ -24,7 +28,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void block_norm_kernel(BlockNormAr
     __shared__ double room[2][TPR / 64 * 2];
     const int tid = threadIdx.x % TPR, N = p.N;
     const int64_t step = (int64_t)gridDim.x * ROWS;
-    int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+    int64_t row = (int64_t)blockIdx.x * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
     Raw<DT, V> x[C], b[C];
     Raw<WT, V> post[C], gate[C], pre[C], post_bias[C], pre_bias[C];
     auto piece = [&](int c) { return Piece<V, MODE>(tid + TPR * c, N); };
@@ -124,8 +128,8 @@ struct Shares {
     int64_t groups, parts;   // runs of rows with one gate; workgroups of a run (1: whole runs, dealt round)
     int64_t workers;         // workgroups
 };
-// Threads of a row: of its pieces, a power of two from one wave to 512.  (1024 threads have 128 registers each: rows of 8192, bf16, took
-// 228 us instead of TODO.)
+// Threads of a row: of its pieces, a power of two from one wave to 512.  (1024 threads have 128 registers each: 2048 rows of 8192, bf16,
+// took 228 us instead of 154, 4096 rows of 4096, f32, 254 instead of 89.)
 constexpr int kMostThreads = 512;
 int row_threads(int64_t N, int dtype) {
     const int64_t pieces = (N + (dtype == kF32 ? 3 : 7)) / (dtype == kF32 ? 4 : 8);
@@ -258,13 +262,14 @@ __global__ __launch_bounds__(TPR) void block_norm_backward_kernel(BlockNormBackw
             }
             if (p.post) {
 #pragma unroll
-                for (int c = 0; c < C; ++c)
+                for (int c = 0; c < C; ++c) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         const double v = b[c][i];
                         sum[1] = __builtin_fma(v, v, sum[1]);
                         if constexpr (FULL) sum[4] += v;
                     }
+                }
             }
             row_total<TPR, S1>(sum, room[turn] + TPR / 64 * S0);
             if (p.pre) {

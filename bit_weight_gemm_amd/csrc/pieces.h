@@ -52,10 +52,10 @@ struct Piece {
             r = Raw<DT, V>{};
 #pragma unroll
             for (int q = 0; q < V; ++q)
-                if (q < left) __builtin_memcpy(reinterpret_cast<char *>(&r) + q * S, b + (int64_t)(at + q) * S, S);
+                if (q < left) __builtin_memcpy(reinterpret_cast<char *>(&r) + q * S, b + (uint32_t)((at + q) * S), S);
         } else {
             const int from = full() ? at : MODE == kTail && any() ? N - V : 0;  // (none: the row's first, unused)
-            __builtin_memcpy(&r, b + (int64_t)from * S, V * S);
+            __builtin_memcpy(&r, b + (uint32_t)(from * S), V * S);  // (unsigned: a scalar base and an offset of 32 bits)
         }
     }
     // The piece's values, zeros past the row's end.
@@ -82,7 +82,7 @@ struct Piece {
         E e[V];
 #pragma unroll
         for (int q = 0; q < V; ++q) e[q] = (E)v[q];
-        char *b = static_cast<char *>(p) + (row + at) * S;
+        char *b = static_cast<char *>(p) + row * S + (uint32_t)(at * S);
         if (full()) __builtin_memcpy(b, e, V * S);
         else if (MODE != kWhole)
 #pragma unroll
