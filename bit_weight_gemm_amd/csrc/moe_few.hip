@@ -13,7 +13,8 @@
 // running, it gives up, forms its token's silu(g) u itself (the same values at the same places) and begins again.
 //
 // One token of 8 of 64 experts, 2048 x 1024, bf16: 15.4 us from the first wave to the last.  The choice 2.5, the codes of all
-// products (25 MB, 3.5 TB/s) 7, silu(g) u from one workgroup to the next 2, the down products 3.
+// products (25 MB, 3.5 TB/s) 7, silu(g) u from one workgroup to the next 2, the down products 3.  As three launches 14 us of kernels and
+// their gaps: the same, for two launches' time of the host.
 // Products, decode, correction and the treatment of infinities are q4_row.h's.
 #include "moe_layer.h"
 #include "moe_route.h"

@@ -11,6 +11,9 @@ namespace tq2 {
 
 namespace {
 
+// Tokens times experts up to which the norm and the logits are one launch.
+constexpr int64_t kLogitsSmall = 32768;
+
 struct LogitsArgs {
     const void *x, *norm, *router;
     void *n;                 // NORM: [T][d]
@@ -86,42 +89,46 @@ __global__ __launch_bounds__(256) void layer_logits_kernel(LogitsArgs p) {
 
 template <int DT, int WT, int RT, bool NORM>
 hipError_t logits_of(const LogitsArgs &a, hipStream_t s) {
-    // one expert to a workgroup while the chip has room for them, then four
-    if ((int64_t)a.T * a.E <= 1024) layer_logits_kernel<DT, WT, RT, NORM, 1><<<dim3(a.E, a.T), dim3(256), 0, s>>>(a);
-    else layer_logits_kernel<DT, WT, RT, NORM, 4><<<dim3((a.E + 3) / 4, a.T), dim3(256), 0, s>>>(a);
+    // One expert to a workgroup while the chip has room for them, then four; behind a norm of its own eight
+    // (2048 tokens of 64 experts, d = 2048, bf16, f32 router: norm and logits 64 us).
+    const dim3 block(256);
+    if ((int64_t)a.T * a.E <= 1024) layer_logits_kernel<DT, WT, RT, NORM, 1><<<dim3(a.E, a.T), block, 0, s>>>(a);
+    else if (NORM || (int64_t)a.T * a.E <= kLogitsSmall) layer_logits_kernel<DT, WT, RT, NORM, 4><<<dim3((a.E + 3) / 4, a.T), block, 0, s>>>(a);
+    else if constexpr (!NORM) layer_logits_kernel<DT, WT, RT, NORM, 8><<<dim3((a.E + 7) / 8, a.T), block, 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <int DT>
 hipError_t logits_of(const LogitsArgs &a, bool wide_norm, bool wide_router, hipStream_t s) {
-    if (!a.norm) return wide_router ? logits_of<DT, DT, kF32, false>(a, s) : logits_of<DT, DT, DT, false>(a, s);
-    if (wide_norm) return wide_router ? logits_of<DT, kF32, kF32, true>(a, s) : logits_of<DT, kF32, DT, true>(a, s);
-    return wide_router ? logits_of<DT, DT, kF32, true>(a, s) : logits_of<DT, DT, DT, true>(a, s);
+    if constexpr (DT == kF32) {
+        return a.norm ? logits_of<DT, DT, DT, true>(a, s) : logits_of<DT, DT, DT, false>(a, s);
+    } else {
+        if (!a.norm) return wide_router ? logits_of<DT, DT, kF32, false>(a, s) : logits_of<DT, DT, DT, false>(a, s);
+        if (wide_norm) return wide_router ? logits_of<DT, kF32, kF32, true>(a, s) : logits_of<DT, kF32, DT, true>(a, s);
+        return wide_router ? logits_of<DT, DT, kF32, true>(a, s) : logits_of<DT, DT, DT, true>(a, s);
+    }
 }
 
-// One wave per token and expert.
-template <int DT, int RT>
-__global__ __launch_bounds__(256) void prompt_logits_kernel(const void *x, const void *router, float *logits, int64_t T, int E, int d) {
-    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (at >= T * E) return;
-    const int64_t t = at / E, e = at % E;
-    double sum = 0.0;
-    for (int k = lane; k < d; k += 64) sum += (double)load_as_float<DT>(x, t * d + k) * load_as_float<RT>(router, e * d + k);
-    sum = wave_total(sum);
-    if (lane == 0) logits[at] = (float)sum;
+// All tokens', as many at a time as a grid's second axis has.
+hipError_t launch_logits(LogitsArgs l, int64_t T, int dtype, bool wide_norm, bool wide_router, hipStream_t s) {
+    constexpr int64_t kMost = 65535;
+    const size_t row = (size_t)l.d * (dtype == kF32 ? 4 : 2);
+    hipError_t e = hipSuccess;
+    for (int64_t t = 0; t < T && e == hipSuccess; t += kMost) {
+        l.T = (int)(T - t < kMost ? T - t : kMost);
+        if (dtype == kF32) e = logits_of<kF32>(l, wide_norm, wide_router, s);
+        else if (dtype == kF16) e = logits_of<kF16>(l, wide_norm, wide_router, s);
+        else e = logits_of<kBF16>(l, wide_norm, wide_router, s);
+        l.x = static_cast<const char *>(l.x) + kMost * row, l.logits += kMost * l.E;
+    }
+    return e;
 }
 
-template <int DT, int RT>
-void prompt_logits(const void *x, const void *router, float *logits, int64_t T, int E, int d, hipStream_t s) {
-    prompt_logits_kernel<DT, RT><<<dim3((unsigned)((T * E + 3) / 4)), dim3(256), 0, s>>>(x, router, logits, T, E, d);
-}
-
-// Up to so many slots the experts' choice and products are one launch (64 experts of 8, 2048 x 1024, bf16: one token 17.4 us, two 23,
-// four 31.6; the choice and the two products apart, four 32.9, eight 51 against 57).
-constexpr int64_t kFewMost = 32;
-// Tokens times experts up to which the norm and the logits are one launch.
-constexpr int64_t kLogitsSmall = 32768;
+// One launch behind the logits' for a token or two, and for up to four of eight slots and more.  Graph-replayed, bf16, norm and residual,
+// together / apart (choice, two products): 64 experts of 8, 2048 x 1024, one token 19.3 / 19.7 us, two 22.5 / 23.7, four 31.5 / 33.0; of 2, one
+// 14.1 / 14.6, two 15.0 / 15.3, four 18.4 / 17.5; 32 of 4, 1024 x 512, two 12.9 / 12.4, with a host in front of each call 13.0 / 14.7;
+// eight tokens of 8 57 / 51.
+bool few_tokens(int64_t T, int64_t k) { return T * k <= 32 && (T <= 2 || k >= 8); }
 
 }  // namespace
 
@@ -129,7 +136,7 @@ LayerPlan layer_plan(int64_t T, int64_t k, int64_t E, int64_t groups, int64_t d,
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     LayerPlan p{};
     p.moe = moe_plan(T, k, E, d, f, dtype);
-    p.few = p.moe.direct && T * k <= kFewMost && T * E <= kLogitsSmall && route_own((int)E, (int)groups) <= kFewOwn;
+    p.few = p.moe.direct && few_tokens(T, k) && T * E <= kLogitsSmall && route_own((int)E, (int)groups) <= kFewOwn;
     p.off_logits = norm ? up((size_t)T * d * (dtype == kF32 ? 4 : 2)) : 0;
     p.off_moe = p.off_logits + up((size_t)T * E * 4);
     p.total = p.off_moe + p.moe.total;
@@ -142,35 +149,23 @@ hipError_t launch_moe_layer(const LayerPlan &p, const LayerArgs &a, void *ws, in
     float *logits = reinterpret_cast<float *>(b + p.off_logits);
     const void *n = a.norm ? b : a.x;
     hipError_t e;
-    if (a.T * E <= kLogitsSmall) {  // with the norm, in one launch
-        LogitsArgs l{};
-        l.x = a.x, l.norm = a.norm, l.router = a.router, l.n = b, l.logits = logits, l.eps = a.eps;
-        l.T = (int)a.T, l.E = E, l.d = d;
-        char *h = b + p.off_moe + p.moe.off_h;
-        if (p.few) {
-            l.fill = reinterpret_cast<w4 *>(h), l.fill_rows = a.route.k * (a.dtype == kF32 ? 3 : 2);
-            l.fill_pitch = (int)(p.moe.ldh / 8), l.fill_own = a.gate.N / 8;
-        }
-        if (a.dtype == kF32) e = a.norm ? logits_of<kF32, kF32, kF32, true>(l, s) : logits_of<kF32, kF32, kF32, false>(l, s);
-        else if (a.dtype == kF16) e = logits_of<kF16>(l, a.wide_norm, a.wide_router, s);
-        else e = logits_of<kBF16>(l, a.wide_norm, a.wide_router, s);
+    LogitsArgs l{};
+    l.x = a.x, l.norm = a.norm, l.router = a.router, l.n = b, l.logits = logits, l.eps = a.eps, l.E = E, l.d = d;
+    if (a.norm && a.T * E > kLogitsSmall) {  // the norm in a launch of its own, once for all experts
+        BlockNormArgs q{};
+        q.x = a.x, q.pre = a.norm, q.n = b, q.M = a.T, q.gate_rows = a.T, q.N = d, q.eps = a.eps, q.scale = 1.0f;
+        e = launch_block_norm(q, a.dtype, a.wide_norm, s);
         if (e != hipSuccess) return e;
-        if (p.few) return launch_few_experts(FewArgs{n, logits, h, patience}, a, s);
-    } else {
-        if (a.norm) {
-            BlockNormArgs q{};
-            q.x = a.x, q.pre = a.norm, q.n = b, q.M = a.T, q.gate_rows = a.T, q.N = d, q.eps = a.eps, q.scale = 1.0f;
-            e = launch_block_norm(q, a.dtype, a.wide_norm, s);
-            if (e != hipSuccess) return e;
-        }
-        if (a.dtype == kF32) prompt_logits<kF32, kF32>(n, a.router, logits, a.T, E, d, s);
-        else if (a.dtype == kF16 && a.wide_router) prompt_logits<kF16, kF32>(n, a.router, logits, a.T, E, d, s);
-        else if (a.dtype == kF16) prompt_logits<kF16, kF16>(n, a.router, logits, a.T, E, d, s);
-        else if (a.wide_router) prompt_logits<kBF16, kF32>(n, a.router, logits, a.T, E, d, s);
-        else prompt_logits<kBF16, kBF16>(n, a.router, logits, a.T, E, d, s);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        l.x = n, l.norm = nullptr;
     }
+    char *h = b + p.off_moe + p.moe.off_h;
+    if (p.few) {
+        l.fill = reinterpret_cast<w4 *>(h), l.fill_rows = a.route.k * (a.dtype == kF32 ? 3 : 2);
+        l.fill_pitch = (int)(p.moe.ldh / 8), l.fill_own = a.gate.N / 8;
+    }
+    e = launch_logits(l, a.T, a.dtype, a.wide_norm, a.wide_router, s);
+    if (e != hipSuccess) return e;
+    if (p.few) return launch_few_experts(FewArgs{n, logits, h, patience}, a, s);
     RouteArgs r = a.route;
     r.logits = logits, r.dtype = kF32;
     e = launch_moe_route(r, s);

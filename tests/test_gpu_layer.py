@@ -94,6 +94,27 @@ def test_numbers_of_experts(e, k, d, t):
     check(x, r, w, k, a, "bf16", "experts", renorm=True)
 
 
+def test_more_tokens_than_a_grids_axis():
+    """70000 tokens: every choice against torch's f64 product, some rows of the result against the reference."""
+    t, e, k, d = 70000, 4, 1, 64
+    x, r, w, a = inputs(t, e, d, 32, 32, False, "bf16")
+    handles = [bw.q4_upload(*(cuda(v) for v in p)) for p in w]
+    note(f"[moe_layer] T={t}")
+    y, idx, _ = call(x, r, handles, k, a)
+    v = x.cuda().double()
+    n = (v / ((v * v).mean(1, keepdim=True) + 1e-6).sqrt() * a["norm"].cuda().double()).bfloat16()
+    logits = (n.double() @ r.cuda().double().T.contiguous()).float()
+    top = logits.topk(2, 1).values
+    clear = top[:, 0] - top[:, 1] > 2.0 ** -10  # (a row whose roundings differ moves its logits by less)
+    assert torch.equal(idx[clear, 0].long(), logits.argmax(1)[clear])
+    some = torch.cat((torch.arange(5), torch.arange(65530, 65545), torch.arange(t - 5, t)))
+    part, want_i, _, _ = layer64(x[some], r, *w, k, norm=a["norm"])
+    want = part + a["residual"][some].double()
+    assert torch.equal(idx[some.cuda()].cpu(), want_i)
+    err = (y[some.cuda()].cpu().double() - want).norm(dim=1)
+    assert (err <= (2.0 ** -18 + 2.0 ** -11) * part.norm(dim=1) + half_step("bf16") * want.norm(dim=1) * 1.01).all()
+
+
 @pytest.mark.parametrize("t", [1, 7, 200])
 def test_masked_experts_and_tokens_without_one(t):
     """Biases of -inf mask experts; where fewer are left than slots these are -1, and a token without any gets its residual."""
