@@ -474,7 +474,9 @@ template <int DT, int WT, int TPR, int C, int MODE>
 hipError_t run_back(const BlockNormBackwardArgs &a, hipStream_t s) {
     const Shares d = shares_of(a.M, a.N, a.M / a.gate_rows, DT);
     const dim3 grid((unsigned)d.workers), block(TPR);
-    if (a.layer || a.post_bias || a.pre_bias) block_norm_backward_kernel<DT, WT, TPR, C, MODE, true><<<grid, block, 0, s>>>(a, d);
+    // (a bias's gradient may be asked for without its bias)
+    const bool full = a.layer || a.post_bias || a.pre_bias || a.dpost_bias || a.dpre_bias;
+    if (full) block_norm_backward_kernel<DT, WT, TPR, C, MODE, true><<<grid, block, 0, s>>>(a, d);
     else block_norm_backward_kernel<DT, WT, TPR, C, MODE, false><<<grid, block, 0, s>>>(a, d);
     return hipGetLastError();
 }
