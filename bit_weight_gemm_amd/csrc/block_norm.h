@@ -78,12 +78,15 @@ __device__ __forceinline__ float rounded(float v) {
 
 // ---- a row's norm
 
-// Mean and 1 / standard deviation from the sums of N values and of their squares (rms: mean 0).  In f64: the sums lose
-// nothing to a mean far from 0, and the roundings of a normed row, which decide experts where a router follows, are those of
-// its exact value but for one in some 2^28 (a sum in another order would give another 2^-24).
+// Mean and 1 / standard deviation from the sums of N values and of their squares (rms: mean 0).  In f64: the roundings of a
+// normed row, which decide experts where a router follows, are those of its exact value but for one in some 2^28 (a sum in another
+// order would give another 2^-24).  The variance is a difference: its relative error is some 2^-47 (mean / deviation)^2, so it is good
+// for means of up to kFarMean deviations.  Callers whose rows may lie farther away subtract a mean first, or sum again (is_far).
 struct Norm {
     double mean, rstd;
 };
+constexpr double kFarMean = 1024.0;
+__device__ __forceinline__ bool is_far(const Norm &r) { return __builtin_fabs(r.mean) * r.rstd > kFarMean; }
 __device__ __forceinline__ Norm norm_of(double sum, double squares, int N, bool layer, double eps) {
     Norm r;
     r.mean = layer ? sum / N : 0.0;

@@ -26,6 +26,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void block_norm_kernel(BlockNormAr
     constexpr int V = kPiece<DT>, ROWS = threads_of(TPR) / TPR;
     constexpr bool HOLD = C * V <= 8;  // (more of everything would not fit)
     __shared__ double room[2][TPR / 64 * 2];
+    __shared__ double far_room[FULL ? TPR / 64 : 1];  // (its uses lie between those of the other two: one is enough)
     const int tid = threadIdx.x % TPR, N = p.N;
     const int64_t step = (int64_t)gridDim.x * ROWS;
     int64_t row = (int64_t)blockIdx.x * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
@@ -62,7 +63,22 @@ __global__ __launch_bounds__(threads_of(TPR)) void block_norm_kernel(BlockNormAr
                 if constexpr (FULL) sum[1] += w;
             }
         row_total<TPR, FULL ? 2 : 1>(reinterpret_cast<double(&)[FULL ? 2 : 1]>(sum), where);
-        return norm_of(sum[1], sum[0], N, p.layer, p.eps);
+        Norm r = norm_of(sum[1], sum[0], N, p.layer, p.eps);
+        if constexpr (FULL) {
+            if (p.layer && is_far(r)) {  // (the same for all threads of the row) the squares again, of the differences
+                double again[1] = {};
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int q = 0; q < V; ++q) {
+                        const double w = q < piece(c).left ? (double)v[c][q] - r.mean : 0.0;
+                        again[0] = __builtin_fma(w, w, again[0]);
+                    }
+                row_total<TPR, 1>(again, far_room);
+                r.rstd = norm_of(0.0, again[0], N, true, p.eps).rstd;
+            }
+        }
+        return r;
     };
     auto scaled = [&](const Norm &r, float (&v)[C][V], const Raw<WT, V> (&weight)[C], bool biased, const Raw<WT, V> (&bias)[C]) {
 #pragma unroll
