@@ -673,7 +673,8 @@ def moe_layer(x, router, gate: Q4Weight, up: Q4Weight, down: Q4Weight, k, norm=N
 
 
 def moe_layer_set_patience(tries: int) -> int:
-    """Test hook: how often a workgroup looks for a value that another one forms before it forms it itself; returns the old setting."""
+    """Test hook: how often a workgroup looks for a value that another one forms before it forms it itself, 0 to 65536 (the
+    setting at first), for the whole process; returns the old setting."""
     st = int(lib().moe_layer_set_patience(int(tries)))
     if st < 0:
         raise Tq2Error(st, "moe_layer_set_patience")

@@ -51,8 +51,9 @@ bool side_type(int type, int dtype) { return type == Q4_F32 || type == dtype; }
 
 constexpr int64_t kNormColumns = 16384;
 
-// Some tens of milliseconds.
-std::atomic<int> g_patience{1 << 16};
+// Some tens of milliseconds, and no call may wait longer.
+constexpr int kMostPatience = 1 << 16;
+std::atomic<int> g_patience{kMostPatience};
 
 bool norm_sizes(int64_t M, int64_t N, int64_t R, int dtype) {
     return M >= 0 && M <= kMaxRows && N >= 1 && N <= kNormColumns && R >= 1 && (M == 0 || (R <= M && M % R == 0)) && known(dtype);
@@ -131,7 +132,7 @@ int moe_layer(const moe_layer_call *c, void *workspace, size_t workspace_bytes, 
 }
 
 int moe_layer_set_patience(int tries) {
-    if (tries < 0) return TQ2_EINVAL;
+    if (tries < 0 || tries > kMostPatience) return TQ2_EINVAL;
     return g_patience.exchange(tries);
 }
 

@@ -55,7 +55,8 @@ size_t moe_layer_workspace_size(int64_t T, int64_t k, int64_t E, int64_t d, int6
 int moe_layer(const moe_layer_call *call, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Test hook: with a few tokens, how often a workgroup looks for a value that another one forms before it forms it itself (the
- * results are the same bits).  Returns the old setting. */
+ * results are the same bits), 0 to 65536, which it is at first: some tens of milliseconds.  Of the whole process.  Returns the old
+ * setting, or TQ2_EINVAL. */
 int moe_layer_set_patience(int tries);
 
 /* The norms after and before a block, with its gate and residual scale:
