@@ -1,0 +1,99 @@
+"""GPU: a mixture layer of a few tokens with more pieces of work than workgroups, mixed group sizes, and without patience.
+
+The launch behind the logits has at most 512 workgroups; a call with more gate, up and down products than that gives several to
+each, in the same LDS.  Tolerances as in test_gpu_layer.py.
+"""
+
+import pytest
+import torch
+
+import bit_weight_gemm_amd as bw
+from gpu_util import note
+from q4_util import cuda, gen, weight
+from test_gpu_layer import call, check, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def pieces(t, k, d, f):
+    """Gate and up products of 32 columns of a slot, down products of 16 columns of a token."""
+    return t * (k * -(-f // 32) + -(-d // 16))
+
+
+def mixed(e, d, f, up_group, down_group, zeros, seed=1):
+    return [weight(seed, (e,), f, d, up_group, zeros), weight(seed + 1, (e,), f, d, up_group, zeros), weight(seed + 2, (e,), d, f, down_group, not zeros)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("t,k,d,f,up_group,down_group,residual", [(2, 8, 2048, 1024, 128, 128, True), (4, 8, 2048, 1024, 32, 128, False),
+                                                                 (2, 16, 1024, 512, 64, 32, True), (3, 9, 1568, 736, 32, 32, False),
+                                                                 (1, 8, 8192, 1024, 128, 64, True), (1, 16, 256, 512, 64, 64, True)])
+def test_more_work_than_workgroups(t, k, d, f, up_group, down_group, residual, dtype):
+    """(The last two: one token, of more and of fewer pieces than workgroups.)  With patience and without: the same bits."""
+    e = k + 2
+    assert (pieces(t, k, d, f) > 512) == (d > 256)
+    x, r, _, a = inputs(t, e, d, 64, 32, False, dtype, residual=residual)
+    w = mixed(e, d, f, up_group, down_group, t % 2 == 0)
+    got = check(x, r, w, k, a, dtype, f"{pieces(t, k, d, f)} pieces", renorm=True)
+    handles = [bw.q4_upload(*(cuda(v) for v in p)) for p in w]
+    was = bw.moe_layer_set_patience(0)
+    try:
+        for _ in range(3):
+            again = call(x, r, handles, k, a, renorm=True)
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(got, again))
+    finally:
+        bw.moe_layer_set_patience(was)
+
+
+def test_more_work_than_workgroups_in_a_graph():
+    """Replays with new rows: what the fill before them left, and nothing of the replay before."""
+    t, k, d, f = 2, 8, 2048, 1024
+    x, r, _, a = inputs(t, 10, d, 64, 32, False, "bf16")
+    handles = [bw.q4_upload(*(cuda(v) for v in p)) for p in mixed(10, d, f, 128, 64, True)]
+    x, r, a = x.cuda(), r.cuda(), {n: cuda(v) for n, v in a.items()}
+    note("[moe_layer] graph of several pieces a workgroup")
+    bw.moe_layer(x, r, *handles, k, **a)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = bw.moe_layer(x, r, *handles, k, **a)
+    for rep in range(4):
+        x.copy_(3 * torch.randn(x.shape, generator=gen(60 + rep)))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = bw.moe_layer(x, r, *handles, k, **a)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), rep
+
+
+def test_without_patience_a_workgroup_forms_it_itself():
+    """One token whose workgroups all start at once: without patience those of the down products find silu(g) u missing and
+    form all of it, 128 times the work, which shows in the time (the bits are the same)."""
+    t, k, d, f = 1, 8, 2048, 1024
+    assert pieces(t, k, d, f) <= 512
+    x, r, _, a = inputs(t, 16, d, 64, 32, False, "bf16")
+    handles = [bw.q4_upload(*(cuda(v) for v in p)) for p in mixed(16, d, f, 128, 128, False)]
+    x, r, a = x.cuda(), r.cuda(), {n: cuda(v) for n, v in a.items()}
+    note("[moe_layer] without patience")
+
+    def best():
+        times = []
+        for _ in range(8):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            out = bw.moe_layer(x, r, *handles, k, **a)
+            end.record()
+            torch.cuda.synchronize()
+            times.append(start.elapsed_time(end))
+        return out, min(times)
+
+    want, patient = best()
+    was = bw.moe_layer_set_patience(0)
+    try:
+        got, hasty = best()
+    finally:
+        bw.moe_layer_set_patience(was)
+    note(f"  {1e3 * patient:.0f} us, without patience {1e3 * hasty:.0f}")
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert hasty > 3 * patient
