@@ -85,7 +85,7 @@ int q4_linear(const q4_weight *w, const void *x, const void *bias, int bias_dtyp
 
 size_t moe_layer_workspace_size(int64_t T, int64_t k, int64_t E, int64_t d, int64_t f, int dtype, int with_norm) {
     if (q4_moe_workspace_size(T, k, E, d, f, dtype) == 0 || k > E) return 0;
-    return tq2::layer_plan(T, k, E, 1, d, f, dtype, with_norm != 0).total;
+    return tq2::layer_plan(T, k, E, 1, d, f, dtype, with_norm != 0, false).total;
 }
 
 int moe_layer(const moe_layer_call *c, void *workspace, size_t workspace_bytes, void *stream) {
@@ -127,7 +127,8 @@ int moe_layer(const moe_layer_call *c, void *workspace, size_t workspace_bytes, 
     a.route.bias = c->bias, a.route.idx = c->idx, a.route.weights = c->weights, a.route.T = T;
     a.route.E = (int)E, a.route.k = (int)k, a.route.groups = (int)c->groups, a.route.keep = (int)c->keep;
     a.route.group_top = (int)c->group_top, a.route.sigmoid = c->score == MOE_SIGMOID, a.route.renorm = c->renorm != 0;
-    const tq2::LayerPlan p = tq2::layer_plan(T, k, E, c->groups, d, f, c->dtype, c->norm != nullptr);
+    const bool coarse = gate->G == tq2::kFewGroup && down->G == tq2::kFewGroup;
+    const tq2::LayerPlan p = tq2::layer_plan(T, k, E, c->groups, d, f, c->dtype, c->norm != nullptr, coarse);
     return tq2::status_of(tq2::launch_moe_layer(p, a, workspace, g_patience, static_cast<hipStream_t>(stream)));
 }
 

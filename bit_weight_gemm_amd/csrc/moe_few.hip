@@ -1,5 +1,5 @@
 // A few tokens through a mixture's experts in one launch, from the router's logits: y[t] = residual[t] +
-// sum_j w_j down_e(silu(gate_e n_t) * (up_e n_t)).
+// sum_j w_j down_e(silu(gate_e n_t) * (up_e n_t)), for weights in groups of 128.
 //
 // Tasks: the slots' gate and up products (32 columns of one slot each), then the down products (16 columns of one token each),
 // dealt to at most 512 workgroups in turn.  Each wave chooses some tokens' experts from the logits first (against a
@@ -12,9 +12,10 @@
 // in order; but should a down task have looked `patience` times for a value, because the workgroup that has it is not
 // running, it gives up, forms its token's silu(g) u itself (the same values at the same places) and begins again.
 //
-// One token of 8 of 64 experts, 2048 x 1024, bf16: 15.4 us from the first wave to the last.  The choice 2.5, the codes of all
+// One token of 8 of 64 experts, 2048 x 1024, bf16: 17.1 us, the least of 30 15.1 (inputs in turn).  The choice 2.5, the codes of all
 // products (25 MB, 3.5 TB/s) 7, silu(g) u from one workgroup to the next 2, the down products 3.  As three launches 14 us of kernels and
-// their gaps: the same, for two launches' time of the host.
+// their gaps: the same, for two launches' time of the host.  The 128 registers that two workgroups to a compute unit leave a lane
+// do not hold all: 20 to 36 bytes of a lane lie in scratch.
 // Products, decode, correction and the treatment of infinities are q4_row.h's.
 #include "moe_layer.h"
 #include "moe_route.h"
@@ -26,6 +27,7 @@ namespace tq2 {
 namespace {
 
 constexpr int kFewWaves = 8, kFewSlots = 64;
+static_assert(kFewGroup == 128, "a unit has one group");
 
 // Bits of an element of h that is not written yet: a NaN that no part of one is stored as.
 constexpr uint16_t kNoH = 0xffff;
@@ -55,84 +57,78 @@ struct FewCall {
 static_assert(sizeof(FewCall) <= 192, "three lines");
 enum { kFewSigmoid = 1, kFewRenorm = 2, kFewTopTwo = 4, kFewOne = 8 };  // kFewOne: a lane of the router has one expert at most
 
-__device__ __forceinline__ Q4View few_view(const FewWeight &w, int E, int N, int K, int G) {
+__device__ __forceinline__ Q4View few_view(const FewWeight &w, int E, int N, int K) {
     Q4View v{};
-    v.codes = w.codes, v.scales = w.scales, v.zeros = w.zeros, v.E = E, v.N = N, v.K = K, v.G = G;
+    v.codes = w.codes, v.scales = w.scales, v.zeros = w.zeros, v.E = E, v.N = N, v.K = K, v.G = kFewGroup;
     v.nb = (N + 15) >> 4, v.ku = (K + 127) >> 7;
     return v;
 }
 
 // A column block's units, one after another.
-template <int G>
 struct Units {
     const w4 *codes;
     const uint16_t *scales;
     const uint8_t *zeros;
     __device__ Units(const FewWeight &w, int64_t unit) {
-        codes = w.codes + unit * 64, scales = w.scales + unit * (16 * (128 / G));
-        zeros = w.zeros ? w.zeros + unit * (16 * (128 / G)) : nullptr;
+        codes = w.codes + unit * 64, scales = w.scales + unit * 16, zeros = w.zeros ? w.zeros + unit * 16 : nullptr;
     }
     __device__ __forceinline__ void load(int u, int lane, w4 &b, uint2 &s, uint32_t &z) const {
         b = (codes + u * 64)[lane];
-        q4_load_groups<G>(scales + u * (16 * (128 / G)), zeros ? zeros + u * (16 * (128 / G)) : nullptr, lane & 15, s, z);
+        q4_load_groups<kFewGroup>(scales + u * 16, zeros ? zeros + u * 16 : nullptr, lane & 15, s, z);
     }
 };
 
 // acc[cb] += weight times a unit of CB column blocks times a row.  The row's P parts are rows of the matrix instruction (its
 // other rows repeat the last part): one instruction for all of them, where one each took 16 and with the sums of x by another
-// against ones 32 to a unit.  xs: the lane's part, from its first column on; sums: of x over the unit's groups [P][128/G] (pitch apart).
-template <int XT, int G, int CB>
+// against ones 32 to a unit.  xs: the lane's part, from its first column on; sums: of x over the unit, the parts' pitch apart.
+template <int XT, int CB>
 __device__ __forceinline__ void few_unit(const uint16_t *xs, const float *sums, int pitch, const w4 *b, const uint2 *s, const uint32_t *z,
                                          float weight, float (&acc)[CB]) {
     constexpr bool BF = XT != kXF16, EXACT = XT == kXF32x3;
     constexpr int P = XT == kXF32x3 ? 3 : XT == kXF32x2 ? 2 : 1;
-    f4 part[CB];
+    f4 part[CB] = {};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const bool first = (32 * j) % G == 0, last = (32 * (j + 1)) % G == 0;
-        const int g = 32 * j / G;
         const w4 a = *reinterpret_cast<const w4 *>(xs + 32 * j);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
-            const float zero = (float)((z[cb] >> (8 * g)) & 255u);
             w4 w;
-            if constexpr (EXACT) w = q4_word_exact(b[cb][j], zero);
+            if constexpr (EXACT) w = q4_word_exact(b[cb][j], (float)(z[cb] & 255u));
             else w = q4_word16<BF>(b[cb][j]);
-            if (first) part[cb] = f4{};
             part[cb] = mfma16<BF>(a, w, part[cb]);
-            if (last) {
-                float v = part[cb][0];
-#pragma unroll
-                for (int q = 1; q < P; ++q) v += part[cb][q];
-                if constexpr (!EXACT) {
-                    float sum = sums[g];
-#pragma unroll
-                    for (int q = 1; q < P; ++q) sum += sums[q * pitch + g];
-                    v -= (16.0f + zero) * sum;
-                }
-                acc[cb] += weight * half_bits((g & 2 ? s[cb].y : s[cb].x) >> (16 * (g & 1))) * v;
-            }
         }
+    }
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+        float v = part[cb][0];
+#pragma unroll
+        for (int q = 1; q < P; ++q) v += part[cb][q];
+        if constexpr (!EXACT) {
+            float sum = sums[0];
+#pragma unroll
+            for (int q = 1; q < P; ++q) sum += sums[q * pitch];
+            v -= (16.0f + (float)(z[cb] & 255u)) * sum;
+        }
+        acc[cb] += weight * half_bits(s[cb].x) * v;
     }
 }
 
-// Sum of the eight values of a piece, over the lanes that hold its group's pieces (neighbours); for those of f16 or bfloat16.
-template <bool BF, int G>
-__device__ __forceinline__ float group_sum(w4 v) {
+// Sum of the eight values of a piece, over the sixteen lanes that hold its unit's pieces; for those of f16 or bfloat16.
+template <bool BF>
+__device__ __forceinline__ float unit_sum(w4 v) {
     float s = 0.0f;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         if constexpr (BF) s += __builtin_bit_cast(float, v[q] << 16) + __builtin_bit_cast(float, v[q] & 0xffff0000u);
         else s += half_bits(v[q]) + half_bits(v[q] >> 16);
     }
-    s += dpp<0xB1>(s), s += dpp<0x4E>(s);            // four pieces: 32 columns
-    if constexpr (G >= 64) s += dpp<0x141>(s);       // mirrored in eight lanes
-    if constexpr (G == 128) s += dpp<0x140>(s);      // mirrored in sixteen
+    s += dpp<0xB1>(s), s += dpp<0x4E>(s);    // lane ^ 1, lane ^ 2
+    s += dpp<0x141>(s), s += dpp<0x140>(s);  // mirrored in eight lanes, in sixteen
     return s;
 }
 
 // h of 32 columns of a slot with expert e (below 0: dropped, h is 0).
-template <int XT, int G, int PH>
+template <int XT, int PH>
 __device__ __forceinline__ void up_task(const FewCall &p, int slot, int t, int bx, int e, uint16_t *xs, float *sums, float (*red)[64]) {
     constexpr bool F32 = XT == kXF32x3;
     constexpr int P = F32 ? 3 : 1, CB = 4, D = 2, WAVES = kFewWaves;
@@ -148,7 +144,7 @@ __device__ __forceinline__ void up_task(const FewCall &p, int slot, int t, int b
         return;
     }
     const int64_t u0 = ((int64_t)e * nb + 2 * bx) * ku, u1 = u0 + (2 * bx + 1 < nb ? ku : 0);  // (past the last: not stored)
-    const Units<G> w[CB] = {Units<G>(p.gate, u0), Units<G>(p.up, u0), Units<G>(p.gate, u1), Units<G>(p.up, u1)};
+    const Units w[CB] = {Units(p.gate, u0), Units(p.up, u0), Units(p.gate, u1), Units(p.up, u1)};
     w4 b[D][CB];
     uint2 s[D][CB];
     uint32_t z[D][CB];
@@ -174,8 +170,8 @@ __device__ __forceinline__ void up_task(const FewCall &p, int slot, int t, int b
 #pragma unroll
         for (int q = 0; q < P; ++q) *reinterpret_cast<w4 *>(xs + ((i >> 4) * P + q) * 128 + (i & 15) * 8) = v[q];
         if constexpr (!F32) {
-            const float sum = group_sum<XT == kXBF16, G>(v[0]);
-            if ((i & (G / 8 - 1)) == 0) sums[i / (G / 8)] = sum;
+            const float sum = unit_sum<XT == kXBF16>(v[0]);
+            if ((i & 15) == 0) sums[i >> 4] = sum;
         }
     }
     __syncthreads();
@@ -186,7 +182,7 @@ __device__ __forceinline__ void up_task(const FewCall &p, int slot, int t, int b
         for (int st = 0; st < D; ++st) {
             const int at = u + WAVES * st;
             if (at < ku) {
-                few_unit<XT, G, CB>(xs + (at * P + mine) * 128 + 8 * h, sums + at * (128 / G), 0, b[st], s[st], z[st], 1.0f, acc);
+                few_unit<XT, CB>(xs + (at * P + mine) * 128 + 8 * h, sums + at, 0, b[st], s[st], z[st], 1.0f, acc);
                 if (at + WAVES * D < ku) load(st, at + WAVES * D);
             }
         }
@@ -201,8 +197,8 @@ __device__ __forceinline__ void up_task(const FewCall &p, int slot, int t, int b
 #pragma unroll
     for (int q = 0; q < WAVES; ++q) g += red[q][(tid >> 4) * 32 + (tid & 15)], u += red[q][(tid >> 4) * 32 + 16 + (tid & 15)];
     if (!__builtin_isfinite(g) || !__builtin_isfinite(u)) {
-        g = q4_slow_row<XT>(p.n, t, few_view(p.gate, p.E, p.f, p.d, G), e, col);
-        u = q4_slow_row<XT>(p.n, t, few_view(p.up, p.E, p.f, p.d, G), e, col);
+        g = q4_slow_row<XT>(p.n, t, few_view(p.gate, p.E, p.f, p.d), e, col);
+        u = q4_slow_row<XT>(p.n, t, few_view(p.up, p.E, p.f, p.d), e, col);
     }
     uint16_t part[PH];
     q4_parts<PH>(g / (1.0f + expf(-g)) * u, part);
@@ -212,10 +208,10 @@ __device__ __forceinline__ void up_task(const FewCall &p, int slot, int t, int b
 }
 
 // y of 16 columns of a token; false (for all threads): some of h was not there.
-template <int XT, int G, int DT, bool RES>
+template <int XT, int DT, bool RES>
 __device__ __forceinline__ bool down_task(const FewCall &p, int t, int bx, const int32_t *chosen, const float *weights, uint16_t *xs,
                                           float *sums, float (*red)[16]) {
-    constexpr int P = XT == kXF32x3 ? 3 : 2, D = G == 32 ? 6 : 8, WAVES = kFewWaves;  // D: units ahead, as registers allow
+    constexpr int P = XT == kXF32x3 ? 3 : 2, D = 8, WAVES = kFewWaves;  // D: units ahead
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ku = (p.f + 127) >> 7, nb = (p.d + 15) >> 4, k = p.k, col = bx * 16 + tid;
@@ -237,7 +233,7 @@ __device__ __forceinline__ bool down_task(const FewCall &p, int t, int bx, const
     auto load = [&](int st) {
         if (next.j < k) {
             const int e = __builtin_amdgcn_readlane(slots, next.j);
-            if (e >= 0) Units<G>(p.down, ((int64_t)e * nb + bx) * ku).load(next.u, lane, b[st], s[st], z[st]);
+            if (e >= 0) Units(p.down, ((int64_t)e * nb + bx) * ku).load(next.u, lane, b[st], s[st], z[st]);
             next.u += WAVES;
             next.settle(ku);
         }
@@ -282,8 +278,8 @@ __device__ __forceinline__ bool down_task(const FewCall &p, int t, int bx, const
             const w4 piece = {(uint32_t)v[q][0], (uint32_t)(v[q][0] >> 32), (uint32_t)v[q][1], (uint32_t)(v[q][1] >> 32)};
             if (i < pieces) *reinterpret_cast<w4 *>(xs + i * 8) = piece;
             if constexpr (XT != kXF32x3) {
-                const float sum = group_sum<true, G>(piece);
-                if (i < pieces && (i & (G / 8 - 1)) == 0) sums[i / (G / 8)] = sum;
+                const float sum = unit_sum<true>(piece);
+                if (i < pieces && (i & 15) == 0) sums[i >> 4] = sum;
             }
         }
     }
@@ -295,9 +291,8 @@ __device__ __forceinline__ bool down_task(const FewCall &p, int t, int bx, const
         for (int st = 0; st < D; ++st) {
             if (now.j >= k) break;
             if (__builtin_amdgcn_readlane(slots, now.j) >= 0)
-                few_unit<XT, G, 1>(xs + ((now.j * P + mine) * ku + now.u) * 128 + 8 * h, sums + (now.j * P * ku + now.u) * (128 / G),
-                                   ku * (128 / G), &b[st], &s[st], &z[st],
-                                   __builtin_bit_cast(float, __builtin_amdgcn_readlane(parts, now.j)), acc);
+                few_unit<XT, 1>(xs + ((now.j * P + mine) * ku + now.u) * 128 + 8 * h, sums + now.j * P * ku + now.u, ku, &b[st], &s[st],
+                                &z[st], __builtin_bit_cast(float, __builtin_amdgcn_readlane(parts, now.j)), acc);
             now.u += WAVES;
             now.settle(ku);
             load(st);
@@ -316,7 +311,7 @@ __device__ __forceinline__ bool down_task(const FewCall &p, int t, int bx, const
             const int e = chosen[t * k + j];
             if (e < 0) continue;
             const uint16_t *x = xs + j * P * ku * 128;
-            const float dot = q4_slow_dot(few_view(p.down, p.E, p.d, p.f, G), e, col, [&](int c, float (&v8)[8]) {
+            const float dot = q4_slow_dot(few_view(p.down, p.E, p.d, p.f), e, col, [&](int c, float (&v8)[8]) {
                 q4_x8<kXBF16>(x, c, v8);
 #pragma unroll
                 for (int q = 1; q < P; ++q) {
@@ -334,10 +329,10 @@ __device__ __forceinline__ bool down_task(const FewCall &p, int t, int bx, const
     return true;
 }
 
-template <int XT, int XH, int G, int GD, int PH, int DT, bool RES>
+template <int XT, int XH, int PH, int DT, bool RES>
 __global__ __launch_bounds__(kFewWaves * 64, 4) void few_experts_kernel(FewCall p) {
     asm volatile("" ::"s"(p.gate.codes), "s"(p.down.zeros), "s"(p.weights));  // a value of each line
-    extern __shared__ __attribute__((aligned(16))) uint16_t few_room[];  // a row, or a token's h; behind it sums by group
+    extern __shared__ __attribute__((aligned(16))) uint16_t few_room[];  // a row, or a token's h; behind it sums by unit
     __shared__ float red[kFewWaves][64];
     __shared__ int32_t chosen[kFewSlots];
     __shared__ float weights[kFewSlots];
@@ -369,12 +364,12 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void few_experts_kernel(FewCall 
                 const int first = is_up ? task : t * k * p.gx, last = is_up ? task + 1 : (t + 1) * k * p.gx;
                 for (int i = first; i < last; ++i) {
                     const int slot = __builtin_amdgcn_readfirstlane(i / p.gx);
-                    up_task<XT, G, PH>(p, slot, t, i - slot * p.gx, __builtin_amdgcn_readfirstlane(chosen[slot]), few_room, sums, red);
+                    up_task<XT, PH>(p, slot, t, i - slot * p.gx, __builtin_amdgcn_readfirstlane(chosen[slot]), few_room, sums, red);
                     __syncthreads();  // the rooms are free again
                 }
                 if (is_up) break;
             }
-            const bool done = down_task<XH, GD, DT, RES>(p, t, at - t * p.dx, chosen, weights, few_room, sums,
+            const bool done = down_task<XH, DT, RES>(p, t, at - t * p.dx, chosen, weights, few_room, sums,
                                                          reinterpret_cast<float(*)[16]>(&red[0][0]));
             __syncthreads();
             if (done) break;
@@ -382,29 +377,14 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void few_experts_kernel(FewCall 
     }
 }
 
-template <int XT, int XH, int PH, int DT, int G, int GD>
-hipError_t run(const FewCall &c, size_t lds, bool residual, hipStream_t s) {
+template <int XT, int XH, int PH, int DT>
+hipError_t run(const FewCall &c, size_t lds, hipStream_t s) {
     // two workgroups to each of the 256 compute units, if there is work for them
     const int tasks = c.T * (c.k * c.gx + c.dx);
     const dim3 grid((unsigned)(tasks < 512 ? tasks : 512)), block(kFewWaves * 64);
-    if (residual) few_experts_kernel<XT, XH, G, GD, PH, DT, true><<<grid, block, lds, s>>>(c);
-    else few_experts_kernel<XT, XH, G, GD, PH, DT, false><<<grid, block, lds, s>>>(c);
+    if (c.residual) few_experts_kernel<XT, XH, PH, DT, true><<<grid, block, lds, s>>>(c);
+    else few_experts_kernel<XT, XH, PH, DT, false><<<grid, block, lds, s>>>(c);
     return hipGetLastError();
-}
-
-template <int XT, int XH, int PH, int DT, int G>
-hipError_t run(const FewCall &c, int gd, size_t lds, bool residual, hipStream_t s) {
-    if (gd == 32) return run<XT, XH, PH, DT, G, 32>(c, lds, residual, s);
-    if (gd == 64) return run<XT, XH, PH, DT, G, 64>(c, lds, residual, s);
-    return run<XT, XH, PH, DT, G, 128>(c, lds, residual, s);
-}
-
-template <int XT, int XH, int PH, int DT>
-hipError_t run(const FewCall &c, const LayerArgs &a, size_t lds, hipStream_t s) {
-    const bool residual = a.residual != nullptr;
-    if (a.gate.G == 32) return run<XT, XH, PH, DT, 32>(c, a.down.G, lds, residual, s);
-    if (a.gate.G == 64) return run<XT, XH, PH, DT, 64>(c, a.down.G, lds, residual, s);
-    return run<XT, XH, PH, DT, 128>(c, a.down.G, lds, residual, s);
 }
 
 }  // namespace
@@ -423,11 +403,11 @@ hipError_t launch_few_experts(const FewArgs &f, const LayerArgs &a, hipStream_t 
     const int parts = a.dtype == kF32 ? 3 : 2;
     const size_t up = q4_row_lds(a.gate.ku, a.dtype == kF32 ? 3 : 1), down = q4_row_lds((int64_t)r.k * a.down.ku, parts);
     const size_t rows = up > down ? up : down;
-    const size_t lds = rows + rows / 16;  // a sum of 4 bytes to 32 values at most
+    const size_t lds = rows + rows / 64;  // a sum of 4 bytes to a unit of 256
     c.room = (int)(rows / 2);
-    if (a.dtype == kF16) return run<kXF16, kXF32x2, 2, kF16>(c, a, lds, s);
-    if (a.dtype == kBF16) return run<kXBF16, kXF32x2, 2, kBF16>(c, a, lds, s);
-    return run<kXF32x3, kXF32x3, 3, kF32>(c, a, lds, s);
+    if (a.dtype == kF16) return run<kXF16, kXF32x2, 2, kF16>(c, lds, s);
+    if (a.dtype == kBF16) return run<kXBF16, kXF32x2, 2, kBF16>(c, lds, s);
+    return run<kXF32x3, kXF32x3, 3, kF32>(c, lds, s);
 }
 
 }  // namespace tq2

@@ -23,10 +23,11 @@ struct LayerPlan {
     bool few;                        // two launches: the logits, and everything behind them
     size_t off_logits, off_moe, total;
 };
-LayerPlan layer_plan(int64_t T, int64_t k, int64_t E, int64_t groups, int64_t d, int64_t f, int dtype, bool norm);
+// coarse: the weights' groups are of kFewGroup (the sizes do not depend on it, nor on the router's groups)
+LayerPlan layer_plan(int64_t T, int64_t k, int64_t E, int64_t groups, int64_t d, int64_t f, int dtype, bool norm, bool coarse);
 hipError_t launch_moe_layer(const LayerPlan &p, const LayerArgs &a, void *ws, int patience, hipStream_t s);
 
-// moe_few.hip: the experts' choice and products of a few tokens, from their logits, in one launch.
+// moe_few.hip: the experts' choice and products of a few tokens, from their logits, in one launch, for weights in groups of kFewGroup.
 struct FewArgs {
     const void *n;                   // [T][d], normed
     const float *logits;             // [T][E]
@@ -36,5 +37,6 @@ struct FewArgs {
 };
 hipError_t launch_few_experts(const FewArgs &f, const LayerArgs &a, hipStream_t s);
 constexpr int kFewOwn = 4;           // experts of a lane that its router holds
+constexpr int kFewGroup = 128;
 
 }  // namespace tq2

@@ -124,19 +124,26 @@ hipError_t launch_logits(LogitsArgs l, int64_t T, int dtype, bool wide_norm, boo
     return e;
 }
 
-// One launch behind the logits' for a token or two, and for up to four of eight slots and more.  Graph-replayed, bf16, norm and residual,
-// together / apart (choice, two products): 64 experts of 8, 2048 x 1024, one token 19.3 / 19.7 us, two 22.5 / 23.7, four 31.5 / 33.0; of 2, one
-// 14.1 / 14.6, two 15.0 / 15.3, four 18.4 / 17.5; 32 of 4, 1024 x 512, two 12.9 / 12.4, with a host in front of each call 13.0 / 14.7;
-// eight tokens of 8 57 / 51.
+// One launch behind the logits' for a token or two, and for up to four of eight slots and more, where the weights have groups of 128.
+// Together / apart (choice, two products), us of graph replays with norm and residual, zero points or not within 3%:
+//                                       bf16: one token    two          three        four         f32: one     two          four
+//   64 experts of 8, 2048 x 1024        19.5 / 19.9        22.8 / 23.9  27.9 / 30.2  31.8 / 33.0  24.0 / 24.6  29.4 / 30.8  46.0 / 45.0
+//   128 of 8, 2048 x 768                18.3 / 18.5        22.7 / 22.0  25.2 / 29.3  27.9 / 30.2  22.7 / 22.5  28.0 / 28.5  37.1 / 39.4
+//   32 of 16, 2048 x 512                19.9 / 20.3        23.6 / 23.2  (above 32 slots)          23.9 / 24.6  29.3 / 30.1
+//   64 of 4, 1024 x 1024                13.8 / 14.6        14.5 / 15.2                            15.4 / 16.8  16.6 / 17.6
+//   8 of 2, 1024 x 1024                 11.9 / 11.9        12.4 / 12.1                            13.1 / 13.6  13.5 / 13.8
+// With a host in front of each call the small ones are 12.1 / 15.4 and 12.6 / 15.8 (8 of 2): it has one launch less to make.  Four tokens
+// of 64 of 2 18.4 / 17.5, eight of 8 57 / 51.  With groups of 32 and 64 the one launch kept up to 336 bytes a lane in scratch and
+// lost: 64 of 8, one token 39 / 21 and 24 / 20, four 81 / 35 and 41 / 33 (f32, 32: 46 / 25 and 98 / 52).
 bool few_tokens(int64_t T, int64_t k) { return T * k <= 32 && (T <= 2 || k >= 8); }
 
 }  // namespace
 
-LayerPlan layer_plan(int64_t T, int64_t k, int64_t E, int64_t groups, int64_t d, int64_t f, int dtype, bool norm) {
+LayerPlan layer_plan(int64_t T, int64_t k, int64_t E, int64_t groups, int64_t d, int64_t f, int dtype, bool norm, bool coarse) {
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     LayerPlan p{};
     p.moe = moe_plan(T, k, E, d, f, dtype);
-    p.few = p.moe.direct && few_tokens(T, k) && T * E <= kLogitsSmall && route_own((int)E, (int)groups) <= kFewOwn;
+    p.few = coarse && p.moe.direct && few_tokens(T, k) && T * E <= kLogitsSmall && route_own((int)E, (int)groups) <= kFewOwn;
     p.off_logits = norm ? up((size_t)T * d * (dtype == kF32 ? 4 : 2)) : 0;
     p.off_moe = p.off_logits + up((size_t)T * E * 4);
     p.total = p.off_moe + p.moe.total;

@@ -1,7 +1,7 @@
-"""GPU: a mixture layer of a few tokens with more pieces of work than workgroups, mixed group sizes, and without patience.
+"""GPU: a mixture layer of a few tokens: more pieces of work than workgroups, without patience, masks, mixed group sizes.
 
-The launch behind the logits has at most 512 workgroups; a call with more gate, up and down products than that gives several to
-each, in the same LDS.  Tolerances as in test_gpu_layer.py.
+Weights in groups of 128 have one launch behind the logits, of at most 512 workgroups; a call with more gate, up and down products
+than that gives several to each, in the same LDS.  Other groups have several launches.  Tolerances as in test_gpu_layer.py.
 """
 
 import pytest
@@ -25,11 +25,13 @@ def mixed(e, d, f, up_group, down_group, zeros, seed=1):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("t,k,d,f,up_group,down_group,residual", [(2, 8, 2048, 1024, 128, 128, True), (4, 8, 2048, 1024, 32, 128, False),
-                                                                 (2, 16, 1024, 512, 64, 32, True), (3, 9, 1568, 736, 32, 32, False),
-                                                                 (1, 8, 8192, 1024, 128, 64, True), (1, 16, 256, 512, 64, 64, True)])
+@pytest.mark.parametrize("t,k,d,f,up_group,down_group,residual", [(2, 8, 2048, 1024, 128, 128, True), (4, 8, 2048, 1024, 128, 128, False),
+                                                                 (2, 16, 1024, 512, 128, 128, True), (3, 9, 1536, 640, 128, 128, False),
+                                                                 (1, 8, 8192, 1024, 128, 128, True), (1, 16, 256, 512, 128, 128, True),
+                                                                 (2, 8, 1024, 1024, 128, 64, True), (4, 8, 2048, 1024, 32, 128, False),
+                                                                 (3, 9, 1568, 736, 32, 32, False)])
 def test_more_work_than_workgroups(t, k, d, f, up_group, down_group, residual, dtype):
-    """(The last two: one token, of more and of fewer pieces than workgroups.)  With patience and without: the same bits."""
+    """(One of fewer pieces among them.)  With patience and without: the same bits."""
     e = k + 2
     assert (pieces(t, k, d, f) > 512) == (d > 256)
     x, r, _, a = inputs(t, e, d, 64, 32, False, dtype, residual=residual)
@@ -46,11 +48,66 @@ def test_more_work_than_workgroups(t, k, d, f, up_group, down_group, residual, d
         bw.moe_layer_set_patience(was)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("router", ["plain", "masked", "groups", "all masked"])
+@pytest.mark.parametrize("t,k,d,f", [(1, 1, 128, 128), (2, 3, 256, 128), (1, 24, 256, 256), (2, 16, 384, 128), (4, 8, 256, 384)])
+def test_few_tokens(t, k, d, f, router, dtype):
+    """Groups of 128 and zero points; tokens with fewer experts than slots, or none."""
+    x, r, w, a = inputs(t, 24, d, f, 128, True, dtype, norm="f32" if t == 2 else "own", bias=router != "plain")
+    kw = dict(score="sigmoid", renorm=True)
+    if "masked" in router:
+        a["bias"][0 if router == "all masked" else 5:] = -float("inf")
+    if router == "groups":
+        kw.update(groups=8, keep=4, group_top=2)
+    got = check(x, r, w, k, a, dtype, "few " + router, **kw)
+    if router == "all masked":
+        assert (got[1] == -1).all() and torch.equal(got[0].cpu(), a["residual"])
+    handles = [bw.q4_upload(*(cuda(v) for v in p)) for p in w]
+    was = bw.moe_layer_set_patience(0)
+    try:
+        again = call(x, r, handles, k, a, **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, again))
+    finally:
+        bw.moe_layer_set_patience(was)
+
+
+@pytest.mark.parametrize("group", [32, 64])
+@pytest.mark.parametrize("t", [1, 4])
+def test_finer_groups_take_about_as_long(t, group):
+    """They have the same codes to read: within half as much again of groups of 128 (one launch for them took 1.2 to 2.6 times
+    as long)."""
+    k, d, f, e = 8, 2048, 1024, 64
+    x, r, _, a = inputs(t, e, d, 64, 32, False, "bf16")
+    x, r, a = x.cuda(), r.cuda(), {n: cuda(v) for n, v in a.items()}
+    note(f"[moe_layer] groups of {group} and of 128, T={t}")
+    best = {}
+    for g in (group, 128):
+        handles = [bw.q4_upload(*(cuda(v) for v in p)) for p in mixed(e, d, f, g, g, False)]
+        bw.moe_layer(x, r, *handles, k, **a)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(20):
+                bw.moe_layer(x, r, *handles, k, **a)
+        times = []
+        for _ in range(6):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            graph.replay()
+            end.record()
+            torch.cuda.synchronize()
+            times.append(start.elapsed_time(end) / 20)
+        best[g] = min(times)
+    note(f"  {1e3 * best[group]:.1f} and {1e3 * best[128]:.1f} us")
+    assert best[group] <= 1.5 * best[128]
+
+
 def test_more_work_than_workgroups_in_a_graph():
     """Replays with new rows: what the fill before them left, and nothing of the replay before."""
     t, k, d, f = 2, 8, 2048, 1024
     x, r, _, a = inputs(t, 10, d, 64, 32, False, "bf16")
-    handles = [bw.q4_upload(*(cuda(v) for v in p)) for p in mixed(10, d, f, 128, 64, True)]
+    handles = [bw.q4_upload(*(cuda(v) for v in p)) for p in mixed(10, d, f, 128, 128, True)]
     x, r, a = x.cuda(), r.cuda(), {n: cuda(v) for n, v in a.items()}
     note("[moe_layer] graph of several pieces a workgroup")
     bw.moe_layer(x, r, *handles, k, **a)
