@@ -11,8 +11,13 @@ namespace tq2 {
 
 namespace {
 
-// Tokens times experts up to which the norm and the logits are one launch.
-constexpr int64_t kLogitsSmall = 32768;
+// Tokens times experts up to which the norm and the logits are one launch, whose workgroups norm a row again for every four experts.
+// Norm and logits in one launch / apart, bf16 rows, f32 router, us: 64 experts, d = 2048, 64 tokens 7.3 / 8.6, 128 9.7 / 9.6, 256 16 / 14,
+// 512 25 / 18; 256 experts, 16 tokens 6.3 / 7.5, 32 10.3 / 10.2, 64 17 / 15; 8 experts, d = 1024, 512 tokens 6.3 / 8.0, 1024 10.6 / 10.0.
+constexpr int64_t kNormWithLogits = 8192;
+// And up to which a workgroup without a norm has four experts, beyond eight.  Layers with four / eight, f32 router, us: 128 tokens of 128
+// experts, d = 4096, 61 / 63, 256 of them 80 / 82; 2048 of 64, d = 2048, 111 / 110, 1024 of 256 183 / 178 (bf16 router 190 / 184).
+constexpr int64_t kLogitsOfFour = 32768;
 
 struct LogitsArgs {
     const void *x, *norm, *router;
@@ -89,11 +94,11 @@ __global__ __launch_bounds__(256) void layer_logits_kernel(LogitsArgs p) {
 
 template <int DT, int WT, int RT, bool NORM>
 hipError_t logits_of(const LogitsArgs &a, hipStream_t s) {
-    // One expert to a workgroup while the chip has room for them, then four; behind a norm of its own eight
-    // (2048 tokens of 64 experts, d = 2048, bf16, f32 router: norm and logits 64 us).
+    // One expert to a workgroup while the chip has room for them, then four, then eight (2048 tokens of 64 experts, d = 2048,
+    // bf16, f32 router: norm and logits 64 us).
     const dim3 block(256);
     if ((int64_t)a.T * a.E <= 1024) layer_logits_kernel<DT, WT, RT, NORM, 1><<<dim3(a.E, a.T), block, 0, s>>>(a);
-    else if (NORM || (int64_t)a.T * a.E <= kLogitsSmall) layer_logits_kernel<DT, WT, RT, NORM, 4><<<dim3((a.E + 3) / 4, a.T), block, 0, s>>>(a);
+    else if (NORM || (int64_t)a.T * a.E <= kLogitsOfFour) layer_logits_kernel<DT, WT, RT, NORM, 4><<<dim3((a.E + 3) / 4, a.T), block, 0, s>>>(a);
     else if constexpr (!NORM) layer_logits_kernel<DT, WT, RT, NORM, 8><<<dim3((a.E + 7) / 8, a.T), block, 0, s>>>(a);
     return hipGetLastError();
 }
@@ -143,7 +148,7 @@ LayerPlan layer_plan(int64_t T, int64_t k, int64_t E, int64_t groups, int64_t d,
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     LayerPlan p{};
     p.moe = moe_plan(T, k, E, d, f, dtype);
-    p.few = coarse && p.moe.direct && few_tokens(T, k) && T * E <= kLogitsSmall && route_own((int)E, (int)groups) <= kFewOwn;
+    p.few = coarse && p.moe.direct && few_tokens(T, k) && T * E <= kNormWithLogits && route_own((int)E, (int)groups) <= kFewOwn;
     p.off_logits = norm ? up((size_t)T * d * (dtype == kF32 ? 4 : 2)) : 0;
     p.off_moe = p.off_logits + up((size_t)T * E * 4);
     p.total = p.off_moe + p.moe.total;
@@ -158,7 +163,7 @@ hipError_t launch_moe_layer(const LayerPlan &p, const LayerArgs &a, void *ws, in
     hipError_t e;
     LogitsArgs l{};
     l.x = a.x, l.norm = a.norm, l.router = a.router, l.n = b, l.logits = logits, l.eps = a.eps, l.E = E, l.d = d;
-    if (a.norm && a.T * E > kLogitsSmall) {  // the norm in a launch of its own, once for all experts
+    if (a.norm && a.T * E > kNormWithLogits) {  // the norm in a launch of its own, once for all experts
         BlockNormArgs q{};
         q.x = a.x, q.pre = a.norm, q.n = b, q.M = a.T, q.gate_rows = a.T, q.N = d, q.eps = a.eps, q.scale = 1.0f;
         e = launch_block_norm(q, a.dtype, a.wide_norm, s);
