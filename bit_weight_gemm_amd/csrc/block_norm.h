@@ -36,20 +36,11 @@ __device__ __forceinline__ double wave_total(double v) {
     v += dpp64<0x140>(v);  // mirrored in sixteen
     return add32(add16(v));
 }
-__device__ __forceinline__ float wave_total(float v) {
-    v = row16_sum(v);
-    float a = v, b = v;
-    swap16(a, b);
-    v = a + b;
-    a = v, b = v;
-    swap32(a, b);
-    return a + b;
-}
 
 // Sums of v[0 .. K-1] over the TPR threads of a row (whole waves; TPR 64: the wave's own).  `room` [TPR / 64][K] is
 // another one at each of two sums in a row, so that one barrier is enough.
-template <int TPR, int K, typename F>
-__device__ __forceinline__ void row_total(F (&v)[K], F *room) {
+template <int TPR, int K>
+__device__ __forceinline__ void row_total(double (&v)[K], double *room) {
 #pragma unroll
     for (int q = 0; q < K; ++q) v[q] = wave_total(v[q]);
     if constexpr (TPR > 64) {
@@ -60,7 +51,7 @@ __device__ __forceinline__ void row_total(F (&v)[K], F *room) {
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < K; ++q) {
-            F s = 0;
+            double s = 0;
 #pragma unroll
             for (int w = 0; w < TPR / 64; ++w) s += room[w * K + q];
             v[q] = s;

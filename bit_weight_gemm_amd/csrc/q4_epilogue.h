@@ -17,9 +17,12 @@ struct Q4Epilogue {
 };
 
 // The three that are v times a sigmoid-like factor tend to 0 at -inf, where the product would be -inf * 0.
-// For 16-bit results (SHORT) from the hardware's exp2 and reciprocal: relative errors below 2^-17, an f16 half step is 2^-11.
+// For 16-bit results (SHORT) from the hardware's exp2 and reciprocal.  Relative errors, with the steps rounded to f32: below 2^-17 from
+// v = -6 on; below, where results are under 1e-8 (gelu) and 1e-10 (its form with tanh), the rounding of the exponent counts more: up
+// to 2^-16.6 and 2^-15.9 at -14 (silu 2^-19.9).  An f16 half step is 2^-11, a bf16 one 2^-8.
 // gelu is then v Phi(v) with Phi(-a) = e^(-a^2/2) erfcx(a / sqrt 2) / 2 (a = |v|), the second factor a polynomial in 1 / (1 + 0.31 a)
-// fitted to least relative error on 0 .. 14.5 (2^-17.7; beyond, e^(-a^2/2) is 0).
+// fitted to least relative error on 0 .. 14.5 (2^-17.7; beyond, e^(-a^2/2) is 0).  What is v times a factor below f32's normal
+// range may come out as 0.
 template <int ACT, bool SHORT>
 __device__ __forceinline__ float q4_act(float v) {
     if constexpr (ACT == kActNone) return v;

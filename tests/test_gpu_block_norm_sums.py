@@ -1,4 +1,4 @@
-"""GPU: the norms' parameter gradients as the C entry point gives them, each asked for by itself.
+"""GPU: the norms and their parameter gradients as the C entry points give them, each asked for by itself.
 
 A bias's gradient needs no bias (it is a sum of dn or of du): its bits are the same with a bias of zeros and with none.  Against
 64 bits: sums over M rows in any order round at most M - 1 times (2^-24 each, f32), and a row's terms are within 64 2^-24 of what
@@ -13,7 +13,7 @@ import pytest
 import torch
 
 import bit_weight_gemm_amd as bw
-from block_util import CODES, NormBackwardCall, hat64
+from block_util import CODES, NormBackwardCall, NormCall, hat64
 from gpu_util import note
 from q4_util import DTYPES, gen
 
@@ -92,3 +92,39 @@ def test_any_selection_of_outputs(post, pre, kind):
     for asked in itertools.chain(*(itertools.combinations(names, i) for i in (1, 2))):
         for name, v in backward(m, n, gates, "bf16", 0.5, ins, asked, kind).items():
             assert torch.equal(v, want[biased(asked)][name]), (asked, name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [(1, 264), (5000, 100), (3001, 1111), (1300, 4096)])
+def test_sums_over_rows_round_as_often_as_they_are_added(m, n, dtype):
+    """The sum of dn: a workgroup adds its rows (M over their number, rounded up), a second kernel every 64th part and then
+    64 sums in pairs: so many roundings of 2^-24, and no more, of what is added."""
+    ins = rows(m, n, dtype, 1)
+    ins["dn"] = (ins["dn"].float().abs() + 0.25).to(DTYPES[dtype])
+    need = bw.lib().block_norm_backward_workspace_size(m, n, 1, CODES[dtype])
+    parts = need // (4 * 5 * n) if m > 1 else 1  # four sums' parts and the gate's
+    assert need == (5 if m > 1 else 4) * 4 * n * parts
+    note(f"[block_norm_backward] {parts} parts M={m} N={n} {dtype}")
+    got = backward(m, n, 1, dtype, 1.0, ins, ("dpre_bias",))["dpre_bias"].double()
+    want = ins["dn"].double().sum(0)
+    err, tol = (got - want).abs() / want, 2.0 ** -24 * (-(-m // parts) + -(-parts // 64) + 6)
+    note(f"  worst err/tol {float(err.max() / tol):.3g}")
+    assert (err <= tol).all()
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_sum_need_not_be_kept(dtype, kind):
+    """Without y the normed rows are the same; the sum's rounding to its type is part of them."""
+    m, n, t = 37, 1000, DTYPES[dtype]
+    ins = rows(m, n, dtype, 1)
+    x = ins["y"]
+    y, want = bw.block_norm(x, b=ins["b"], post=ins["post"], gate=ins["gate"], scale=0.7, pre=ins["pre"], kind=kind)
+    got = torch.full((m, n), float("nan"), dtype=t, device="cuda")
+    call = NormCall(x=x.data_ptr(), b=ins["b"].data_ptr(), post=ins["post"].data_ptr(), gate=ins["gate"].data_ptr(),
+                    pre=ins["pre"].data_ptr(), n=got.data_ptr(), eps=EPS, M=m, N=n, R=1, scale=0.7, layer=kind == "layer",
+                    dtype=CODES[dtype], weights_dtype=CODES[dtype])
+    note(f"[block_norm] without the sum {kind} {dtype}")
+    assert bw.lib().block_norm(ctypes.addressof(call), None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import bit_weight_gemm_amd as bw
+from block_util import half_step, layer64
 from gpu_util import note
 from q4_util import cuda, gen, weight
 from test_gpu_layer import call, check, inputs
@@ -70,6 +71,20 @@ def test_few_tokens(t, k, d, f, router, dtype):
         assert all(torch.equal(p, q) for p, q in zip(got, again))
     finally:
         bw.moe_layer_set_patience(was)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("t,k,d,f,group", [(1, 8, 512, 256, 128), (2, 8, 1024, 512, 128), (4, 8, 256, 384, 128), (1, 8, 512, 256, 64), (3, 4, 288, 96, 32)])
+def test_few_tokens_keep_more_than_16_bits(t, k, d, f, group, dtype):
+    """silu(g) u is in two bfloat16 parts: 2^-17 of the experts' part of a row, f32 sums 2^-18, and one rounding of the result."""
+    x, r, w, a = inputs(t, 12, d, f, group, True, dtype, residual=False)
+    handles = [bw.q4_upload(*(cuda(v) for v in p)) for p in w]
+    note(f"[moe_layer] T={t} k={k} G={group} {dtype}")
+    y, idx, _ = call(x, r, handles, k, a, renorm=True)
+    want, want_i, _, _ = layer64(x, r, *w, k, **a, renorm=True)
+    assert torch.equal(idx.cpu(), want_i)
+    rest = (y.cpu().double() - want).abs() - half_step(dtype) * want.abs() * 1.01  # beyond the result's own rounding
+    assert (rest.clamp(min=0).norm(dim=1) <= (2.0 ** -17 + 2.0 ** -18) * want.norm(dim=1)).all()
 
 
 @pytest.mark.parametrize("group", [32, 64])
