@@ -169,3 +169,68 @@ def test_without_patience_a_workgroup_forms_it_itself():
     note(f"  {1e3 * patient:.0f} us, without patience {1e3 * hasty:.0f}")
     assert all(torch.equal(p, q) for p, q in zip(got, want))
     assert hasty > 3 * patient
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [1, 2])
+@pytest.mark.parametrize("e,k,groups", [(1, 1, 1), (3, 3, 1), (65, 7, 1), (130, 16, 1), (256, 8, 8), (257, 8, 1), (1024, 8, 1), (66, 4, 33)])
+def test_numbers_of_experts_of_a_few_tokens(e, k, groups, t, dtype):
+    """A lane of the router has one expert, or up to four; beyond 256 experts the router has a launch of its own."""
+    x, r, w, a = inputs(t, e, 256, 128, 128, False, dtype, norm=None if t == 2 else "own", bias=True, residual=t == 2)
+    check(x, r, w, k, a, dtype, "experts", renorm=True, groups=groups, keep=max(1, groups // 2), group_top=2 if groups > 1 else 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("t", [1, 2, 4])
+def test_rows_of_a_few_tokens_that_are_not_finite(t, dtype):
+    """A NaN row stays alone; an expert whose weights make silu(g) u infinite or NaN shows in the tokens that have it."""
+    e, k, d, f = 12, 8, 256, 256
+    x, r, w, a = inputs(t, e, d, f, 128, False, dtype)
+    handles = [bw.q4_upload(*(cuda(v) for v in p)) for p in w]
+    clean = call(x, r, handles, k, a)
+    bad = x.clone()
+    bad[t - 1, 3] = float("nan")
+    note(f"[moe_layer] not finite T={t} {dtype}")
+    got = call(bad, r, handles, k, a)
+    torch.cuda.synchronize()
+    assert torch.isnan(got[0][t - 1]).all()
+    assert all(torch.equal(p[: t - 1], q[: t - 1]) for p, q in zip(got, clean))
+    for value in (float("inf"), float("nan")):
+        w[1][1][5, :, 0] = value  # expert 5's up weights
+        broken = [bw.q4_upload(*(cuda(v) for v in p)) for p in w]
+        y, idx, _ = call(x, r, broken, k, a)
+        torch.cuda.synchronize()
+        has = (idx == 5).any(1)
+        assert torch.equal(idx, clean[1]) and torch.isfinite(y[~has]).all() and not torch.isfinite(y[has]).any()
+        was = bw.moe_layer_set_patience(0)
+        try:
+            again, _, _ = call(x, r, broken, k, a)
+            torch.cuda.synchronize()
+        finally:
+            bw.moe_layer_set_patience(was)
+        assert torch.equal(torch.isnan(again), torch.isnan(y)) and torch.equal(again[~torch.isnan(y)], y[~torch.isnan(y)])
+
+
+def test_calls_of_a_few_tokens_side_by_side():
+    """Many calls on three streams at once beside a long product, each with a workspace of its own."""
+    x, r, w, a = inputs(8, 16, 1024, 512, 128, True, "bf16")
+    handles = [bw.q4_upload(*(cuda(v) for v in p)) for p in w]
+    x, r, a = x.cuda(), r.cuda(), {k: cuda(v) for k, v in a.items()}
+    cuts = ((0, 1), (1, 2), (3, 1), (4, 4))
+    rows = [x[i: i + n].contiguous() for i, n in cuts]
+    res = [a["residual"][i: i + n].contiguous() for i, n in cuts]
+    one = lambda i, s=None: bw.moe_layer(rows[i], r, *handles, 8, norm=a["norm"], residual=res[i], stream=s)  # noqa: E731
+    want = [one(i) for i in range(4)]
+    big = bw.q4_upload(*(cuda(v) for v in weight(70, (), 4096, 4096, 128, False)))
+    wide = torch.randn((4096, 4096), generator=gen(71)).bfloat16().cuda()
+    torch.cuda.synchronize()
+    note("[moe_layer] a few tokens on three streams")
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for i in range(48):
+        if i % 8 == 0:
+            bw.q4_gemm(big, wide, stream=streams[3])
+        got.append((i % 4, one(i % 4, streams[i % 3])))
+    torch.cuda.synchronize()
+    for i, out in got:
+        assert all(torch.equal(p, q) for p, q in zip(out, want[i]))
