@@ -225,7 +225,8 @@ def test_calls_of_a_few_tokens_side_by_side():
     wide = torch.randn((4096, 4096), generator=gen(71)).bfloat16().cuda()
     torch.cuda.synchronize()
     note("[moe_layer] a few tokens on three streams")
-    streams = [torch.cuda.Stream() for _ in range(4)]
+    # (torch hands out 32 streams in turn: a whole round leaves the turn, on which other tests' fresh streams depend, where it was)
+    streams = [torch.cuda.Stream() for _ in range(32)][:4]
     got = []
     for i in range(48):
         if i % 8 == 0:
