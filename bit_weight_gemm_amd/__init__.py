@@ -711,7 +711,9 @@ def block_norm_backward(dy, y, dn=None, b=None, post=None, post_bias=None, gate=
                         kind="rms", eps=1e-6, dx=None, db=None, stream=None):
     """Gradient of block_norm from those of y and n (dy None: 0) and its arguments; y: the rows that it gave (x where there is
     no b; not looked at without pre).  Returns a dict: dx and db (where there is a b; both in the rows' type, allocated if
-    None), and float32 sums for the parameters that were given, dgate [R][N], dpost, dpost_bias, dpre, dpre_bias [N]."""
+    None), and float32 sums for the parameters that were given, dgate [R][N], dpost, dpost_bias, dpre, dpre_bias [N].  As
+    moe_route_backward it records nothing and says nothing about arguments that require a gradient: there are no second
+    derivatives."""
     out = (_compiled or _calls()).block_backward(dy, y, dn, b, post, post_bias, gate, pre, pre_bias, scale, _norm(kind), eps,
                                                 dx, db, stream if stream is None else
                                                 _for(stream, dy, y, dn, b, post, post_bias, gate, pre, pre_bias, dx, db))

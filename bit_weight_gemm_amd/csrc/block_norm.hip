@@ -6,10 +6,13 @@
 //
 // One pass over memory: TPR threads hold a row (C pieces of 16 bytes each), every input is read once, sums go over the
 // wave by lane exchanges and over the waves through LDS.
-// Bound by memory where a thread has eight columns or fewer: 4096 x 4096 bf16, forward 30 us (134 MB, 4.5 TB/s; a large copy reaches 5.1),
-// gradient 52 us (201 MB and 25 MB of parts, 4.3 TB/s), f32 42 and 89 us; one row 3.6 and 8 us (launches).  With means
-// 45 and 83 us: their f64 sums and differences.  Gradients of longer rows (more than 4096 of 16 bits, 4096 of f32) have more of a row to a thread
-// than its registers hold and use scratch memory: 2048 x 8192 bf16 154 us, 1.3 TB/s.
+// Bound by memory where a thread has eight columns or fewer: 4096 x 4096 bf16, three sets of inputs in turn, forward 33 us (134 MB,
+// 4.1 TB/s; a large copy reaches 5.1), gradient 54 us (201 MB and 25 MB of parts, 4.2 TB/s), f32 53 and 89 us; one row 3.6 and 8.1 us
+// (launches).  With means 50-54 and 84 us: their f64 sums and differences.  Narrower rows: 4096 x 1024 bf16 11.5 and 28 us (a row's
+// threads are a whole workgroup in the gradient).  Longer ones (more than 4096 columns) have more of a row to a thread than its
+// registers hold.  Forward: 2048 x 8192 bf16 43 us (3.1 TB/s), with means 53; 60 to 988 bytes a lane of scratch beyond 8192 columns (f32 with
+// means beyond 4096): 1000 x 16384 bf16 44.  Gradient, scratch of 440 bytes a lane and more, up to 3240: 2048 x 5000 bf16 146 us (0.8 TB/s),
+// 2048 x 8192 161 (1.3 TB/s), with means 295, 1000 x 16384 443; f32, 2048 x 5120, 301, 1000 x 8192 185.
 #include "block_norm.h"
 
 namespace tq2 {

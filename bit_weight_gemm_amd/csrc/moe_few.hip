@@ -12,7 +12,7 @@
 // in order; but should a down task have looked `patience` times for a value, because the workgroup that has it is not
 // running, it gives up, forms its token's silu(g) u itself (the same values at the same places) and begins again.
 //
-// One token of 8 of 64 experts, 2048 x 1024, bf16: 17.1 us, the least of 30 15.1 (inputs in turn).  The choice 2.5, the codes of all
+// One token of 8 of 64 experts, 2048 x 1024, bf16: 16.0 us, the least of 30 15.4 (inputs in turn).  The choice 2.5, the codes of all
 // products (25 MB, 3.5 TB/s) 7, silu(g) u from one workgroup to the next 2, the down products 3.  As three launches 14 us of kernels and
 // their gaps: the same, for two launches' time of the host.  The 128 registers that two workgroups to a compute unit leave a lane
 // do not hold all: 20 to 36 bytes of a lane lie in scratch.

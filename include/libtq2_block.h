@@ -85,7 +85,9 @@ int block_norm(const block_norm_call *call, void *stream);
  * dy, dn, dx, db [M][N] of type dtype, the others f32: dgate [R][N], the rest [N]; all are overwritten.  Inputs as block_norm's, with y the
  * rows that it gave (x where there is no b).  dy may be NULL (0); dn and y go with pre; without pre they are NULL.  Outputs that are NULL are not
  * formed; db, dgate, dpost and dpost_bias need b, and what their names say.  f32 sums, whose order is fixed: results are
- * deterministic; sums over no rows are 0.  Outputs overlap neither each other nor inputs. */
+ * deterministic; sums over no rows are 0.  (A row's sum of dn * pre * y, and where there are means of y and of b, over the up to 32
+ * columns of a thread, is one of them: where it passes f32's range, the row's gradient is not finite.)  A bias's gradient needs no
+ * bias.  Outputs overlap neither each other nor inputs. */
 typedef struct block_norm_backward_call {
     const void *dy, *dn, *y, *b, *post, *post_bias, *gate, *pre, *pre_bias;
     void *dx, *db;
